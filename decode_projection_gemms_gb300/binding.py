@@ -29,7 +29,10 @@ KIND_AUTO, KIND_CC, KIND_TC05, KIND_SMALLK = 0, 1, 2, 3
 KIND_NAMES = {0: "auto", 1: "cc", 2: "tc05", 3: "smallk"}
 FLAG_PDL = 1
 FLAG_FUSE_FB = 2
-DTYPE_BF16, DTYPE_FP16 = 0, 1
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
+# enum kp_act, enum kp_ffn_op
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+FFN_MX4_GEMM, FFN_MX4_GATED, FFN_GATED = 0, 1, 2
 BRANCH_QKVG, BRANCH_FAB, BRANCH_FB = 0, 1, 2
 
 # exported symbols (must match include/kdaproj.h)
@@ -39,6 +42,8 @@ EXPORTS = (
     "kda_proj_overlap_at", "kda_proj_run", "kda_proj_destroy", "kp_last_error", "kp_version",
     "kp_device_error", "kp_scratch_bytes", "skinny_gemm_noalloc", "skinny_gemm_ex",
     "kp_selftest_timeout", "kp_pdl_consumer_checksum",
+    "kp_ffn_workspace", "kp_mx4_bytes", "kp_mx4_quantize", "kp_mx4_dequantize", "kp_mx4_gemm",
+    "kp_mx4_gated_ffn", "kp_gated_ffn",
 )
 DEV_SELFTEST = 5   # device error code of kp_selftest_timeout
 
@@ -83,6 +88,7 @@ def load(path: str | None = None):
             raise ImportError(f"{p} is missing: build it with decode_projection_gemms_gb300.build.build()")
         lib = ctypes.CDLL(p)
         vp, ci, cfgp = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(KpCfg)
+        i64, sz = ctypes.c_int64, ctypes.c_size_t
         sig = {
             "skinny_gemm": [vp, vp, vp, ci, ci, ci, cfgp, vp],
             "kp_select_config": [ci, ci, ci, ci, cfgp],
@@ -104,6 +110,13 @@ def load(path: str | None = None):
             "skinny_gemm_ex": [vp, vp, vp, vp, ci, ci, ci, ci, cfgp, vp],
             "kp_selftest_timeout": [ci, vp],
             "kp_pdl_consumer_checksum": [vp, ctypes.c_int64, vp, ci, vp],
+            "kp_ffn_workspace": [ci, ci, ci, ci, ctypes.POINTER(ctypes.c_size_t)],
+            "kp_mx4_bytes": [ci, ci, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)],
+            "kp_mx4_quantize": [vp, i64, ci, ci, ci, vp, vp, vp],
+            "kp_mx4_dequantize": [vp, vp, ci, ci, vp, i64, ci, vp],
+            "kp_mx4_gemm": [vp, i64, vp, vp, vp, vp, vp, i64, ci, ci, ci, ci, vp, sz, vp],
+            "kp_mx4_gated_ffn": [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, ci, ci, ci, ci, ci, vp, sz, vp],
+            "kp_gated_ffn": [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp, sz, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -287,6 +300,264 @@ def skinny_gemm_noalloc(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor,
                                       ctypes.byref(cfg) if cfg is not None else None,
                                       _stream_handle(stream)))
     return y
+
+
+# ---- feed-forward operators ---------------------------------------------------
+
+_FFN_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+_FFN_WORK: dict = {}   # workspace bytes by (device, operator, sizes): host arithmetic only
+
+
+def _rows(t, name: str, dtype=None, device=None) -> int:
+    """Check a 2-D row-major CUDA matrix (rows may be strided); returns the row
+    stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if rows <= 1:   # a stride of one row (or none) says nothing
+        ld = max(cols, (cols + 7) // 8 * 8 if rows else cols)
+    if (inner != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous rows (strides {tuple(t.stride())})")
+    return ld
+
+
+def _half_rows(t, name: str, dtype=None, device=None) -> int:
+    if isinstance(t, torch.Tensor) and t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return _rows(t, name, dtype, device)
+
+
+def _act_code(act: str) -> int:
+    try:
+        return ACTIVATIONS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}") from None
+
+
+class _On:
+    """The call's device and stream: current while the call's buffers are
+    allocated (so the allocator hands them out in that stream's order) and its
+    kernels launched."""
+
+    __slots__ = ("dev", "stream", "handle", "_ctx")
+
+    def __init__(self, device, stream):
+        cur = torch.cuda.current_device()
+        self._ctx = []
+        if device.index is not None and device.index != cur:
+            self._ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            self._ctx.append(torch.cuda.stream(stream))
+        self.dev, self.stream = device, stream
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def _work(op: int, M: int, N: int, K: int, device):
+    """A workspace for this call, or None when it needs none."""
+    key = (device.index, op, M, N, K)
+    n = _FFN_WORK.get(key)
+    if n is None:
+        b = ctypes.c_size_t()
+        _check(load().kp_ffn_workspace(op, M, N, K, ctypes.byref(b)))
+        if len(_FFN_WORK) > 4096:
+            _FFN_WORK.clear()
+        n = _FFN_WORK[key] = int(b.value)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _out(t, name: str, shape, dtype, device, contiguous=False):
+    """The caller's output, checked, or a new one; returns (tensor, row stride)."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+    ld = _rows(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t, ld
+
+
+class Mx4Tensor:
+    """A matrix ``[rows, cols]`` held in microscaled 4-bit floating point: 4-bit
+    codes and one power-of-two scale per 32 columns (4.25 bits an element), in
+    the layout that ``include/kdaproj.h`` describes. Made by ``mx4_quantize``."""
+
+    __slots__ = ("codes", "scales", "shape")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        nb = (cols + 31) // 32
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("codes and scales must be uint8")
+        if rows < 0 or cols < 1 or not codes.is_contiguous() or not scales.is_contiguous() \
+                or codes.numel() != rows * nb * 16 \
+                or scales.numel() != (rows + 127) // 128 * ((nb + 3) // 4) * 512 \
+                or codes.device != scales.device:
+            raise ValueError(f"codes and scales do not hold a {rows} x {cols} matrix")
+        self.codes, self.scales, self.shape = codes, scales, (rows, cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+    def __repr__(self):
+        return f"Mx4Tensor({self.shape[0]} x {self.shape[1]}, {self.device})"
+
+
+def _mx4(q, name: str, device=None) -> Mx4Tensor:
+    if not isinstance(q, Mx4Tensor):
+        raise TypeError(f"{name} must be an Mx4Tensor (mx4_quantize), got {type(q).__name__}")
+    if not q.codes.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if device is not None and q.device != device:
+        raise ValueError(f"{name} is on {q.device}, expected {device}")
+    return q
+
+
+def mx4_quantize(x: torch.Tensor, stream=None) -> Mx4Tensor:
+    """Quantise ``x`` [rows, cols] (bfloat16, float16 or float32; any sizes, rows
+    may be strided) to microscaled 4 bits: per 32 columns the scale
+    ``2^(floor(log2 max|x|) - 2)``, elements to the nearest of 0, .5, 1, 1.5, 2,
+    3, 4, 6 scales, ties to even. A block with a NaN or an infinity becomes NaN."""
+    ld = _rows(x, "x")
+    dt = _FFN_DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    rows, cols = x.shape
+    nb = (cols + 31) // 32
+    with _On(x.device, stream) as on:
+        codes = torch.empty((rows, nb * 16), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((rows + 127) // 128 * ((nb + 3) // 4) * 512, dtype=torch.uint8, device=x.device)
+        _check(load().kp_mx4_quantize(x.data_ptr(), ld, rows, cols, dt, codes.data_ptr(), scales.data_ptr(),
+                                      on.handle))
+    return Mx4Tensor(codes, scales, rows, cols)
+
+
+def mx4_dequantize(q: Mx4Tensor, dtype=torch.bfloat16, y: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The values that ``q`` stands for: exact in bfloat16 and float32."""
+    _mx4(q, "q")
+    if dtype not in _FFN_DTYPES:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    with _On(q.device, stream) as on:
+        y, ld = _out(y, "y", q.shape, dtype, q.device)
+        _check(load().kp_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.shape[0], q.shape[1],
+                                        y.data_ptr(), ld, _FFN_DTYPES[dtype], on.handle))
+    return y
+
+
+def _mx4_x(x, dtype):
+    """(rows, cols, device, element type, x arguments) of a 4-bit product's
+    left side: a 16-bit matrix, quantised within the call, or an Mx4Tensor."""
+    if isinstance(x, Mx4Tensor):
+        _mx4(x, "x")
+        dt = torch.bfloat16 if dtype is None else dtype
+        if dt not in _DTYPES:
+            raise TypeError(f"dtype must be bfloat16 or float16, got {dt}")
+        return x.shape[0], x.shape[1], x.device, dt, (None, 0, x.codes.data_ptr(), x.scales.data_ptr())
+    ld = _half_rows(x, "x")
+    if dtype is not None and dtype is not x.dtype:
+        raise TypeError(f"the output has x's type {x.dtype}")
+    return x.shape[0], x.shape[1], x.device, x.dtype, (x.data_ptr(), ld, None, None)
+
+
+def mx4_gemm(x, W: Mx4Tensor, y: torch.Tensor | None = None, dtype=None, stream=None) -> torch.Tensor:
+    """``y = round(Q(x) @ Q(W).T)`` on the 4-bit tensor cores, sums in fp32. ``x``
+    [M, K] is bfloat16 or float16 (quantised within the call; y has its type) or
+    an ``Mx4Tensor`` (y has ``dtype``, bfloat16 unless given). ``W`` [N, K]. Any
+    sizes; with ``x`` empty nothing runs."""
+    M, K, dev, dt, xargs = _mx4_x(x, dtype)
+    _mx4(W, "W", dev)
+    N = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError(f"W has K={W.shape[1]}, x has K={K}")
+    with _On(dev, stream) as on:
+        y, ld = _out(y, "y", (M, N), dt, dev)
+        work = _work(FFN_MX4_GEMM, M, N, K, dev)
+        _check(load().kp_mx4_gemm(*xargs, W.codes.data_ptr(), W.scales.data_ptr(), y.data_ptr(), ld, M, N, K,
+                                  _DTYPES[dt], *_work_args(work), on.handle))
+    return y
+
+
+def _work_args(work):
+    return (None, 0) if work is None else (work.data_ptr(), work.numel())
+
+
+def mx4_gated_ffn(x, Wg: Mx4Tensor, Wu: Mx4Tensor, act: str = "silu", h: torch.Tensor | None = None,
+                  dtype=None, stream=None) -> torch.Tensor:
+    """``h = round(act(Q(x) @ Q(Wg).T) * (Q(x) @ Q(Wu).T))``: the gated block over
+    4-bit weights [F, K] and activations, in one product kernel. ``x`` as for
+    ``mx4_gemm``; ``act`` as for ``gated_ffn``."""
+    code = _act_code(act)
+    T, K, dev, dt, xargs = _mx4_x(x, dtype)
+    _mx4(Wg, "Wg", dev)
+    _mx4(Wu, "Wu", dev)
+    F = Wg.shape[0]
+    if Wg.shape != Wu.shape or Wg.shape[1] != K:
+        raise ValueError(f"Wg {Wg.shape} and Wu {Wu.shape} must both be [F, {K}]")
+    with _On(dev, stream) as on:
+        h, ld = _out(h, "h", (T, F), dt, dev)
+        work = _work(FFN_MX4_GATED, T, F, K, dev)
+        _check(load().kp_mx4_gated_ffn(*xargs, Wg.codes.data_ptr(), Wg.scales.data_ptr(), Wu.codes.data_ptr(),
+                                       Wu.scales.data_ptr(), h.data_ptr(), ld, T, F, K, code, _DTYPES[dt],
+                                       *_work_args(work), on.handle))
+    return h
+
+
+def _gated_operands(x, Wg, Wu):
+    ldx = _half_rows(x, "x")
+    ldg = _rows(Wg, "Wg", x.dtype, x.device)
+    ldu = _rows(Wu, "Wu", x.dtype, x.device)
+    T, K = x.shape
+    F = Wg.shape[0]
+    if Wg.shape != Wu.shape or Wg.shape[1] != K:
+        raise ValueError(f"Wg {tuple(Wg.shape)} and Wu {tuple(Wu.shape)} must both be [F, {K}]")
+    return T, F, K, ldx, ldg, ldu
+
+
+def gated_ffn(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu",
+              h: torch.Tensor | None = None, save: bool = False, stream=None):
+    """``h = round(act(x @ Wg.T) * (x @ Wu.T))``: both projections of a gated
+    feed-forward block, the activation and the product in one kernel, sums in
+    fp32. ``x`` [T, K], ``Wg`` and ``Wu`` [F, K], all bfloat16 or all float16; rows
+    may be strided (strides and K multiples of 8, 16-byte aligned). ``act``:
+    "silu", "gelu" (erf) or "gelu_tanh". With ``save`` returns ``(h, g, u)``, the
+    two products rounded to x's type, for ``gated_ffn_backward``."""
+    code = _act_code(act)
+    T, F, K, ldx, ldg, ldu = _gated_operands(x, Wg, Wu)
+    dev = x.device
+    with _On(dev, stream) as on:
+        h, ldh = _out(h, "h", (T, F), x.dtype, dev)
+        g = u = None
+        if save:
+            g = torch.empty((T, F), dtype=x.dtype, device=dev)
+            u = torch.empty((T, F), dtype=x.dtype, device=dev)
+        work = _work(FFN_GATED, T, F, K, dev)
+        _check(load().kp_gated_ffn(x.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu, h.data_ptr(), ldh,
+                                   g.data_ptr() if save else None, u.data_ptr() if save else None, T, F, K, code,
+                                   _DTYPES[x.dtype], *_work_args(work), on.handle))
+    return (h, g, u) if save else h
 
 
 class KdaPlan:

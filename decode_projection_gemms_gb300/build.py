@@ -33,8 +33,11 @@ SOURCES = [
     "kp_tc05.cu",
     "kp_smallk.cu",
     "kp_noalloc.cu",
+    "kp_mx4.cu",
+    "kp_ffn_stream.cu",
+    "kp_ffn_api.cu",
 ]
-HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh"]
+HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh", "kp_ffn.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

@@ -17,6 +17,7 @@
 #include <string>
 #include <vector>
 
+#include "kp_ffn.cuh"
 #include "kp_internal.cuh"
 
 namespace kp {
@@ -100,6 +101,18 @@ static int device_state(DevState **out) {
         d.ok = true;
     }
     *out = &d;
+    return KP_OK;
+}
+
+int ffn_device(FfnDev *out) {
+    DevState *d = nullptr;
+    int rc = device_state(&d);
+    if (rc) return rc;
+    if ((rc = refuse_after_give_up(d->err_host))) return rc;
+    const cudaError_t e = cudaGetDevice(&out->dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    out->sms = d->sms;
+    out->err = d->err;
     return KP_OK;
 }
 

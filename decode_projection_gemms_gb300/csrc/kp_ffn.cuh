@@ -1,0 +1,169 @@
+// Shared parts of the feed-forward operators: microscaled 4-bit quantisation
+// (kp_mx4.cu), the weight-streaming kernel for few tokens (kp_ffn_stream.cu)
+// and the tile kernel for many (kp_ffn_tile.cu), behind kp_ffn_api.cu.
+//
+// Microscaled 4-bit layout of a matrix [rows, cols] (cols the contraction):
+//   codes   [rows][nb * 16] bytes, nb = ceil(cols / 32): two E2M1 codes a byte,
+//           the lower column in the low nibble; columns past `cols` hold 0.
+//   scales  one E8M0 byte per (row, 32-column block), in tiles of 128 rows x 4
+//           blocks = 512 bytes, tile (rt, kt) at (rt * ceil(nb / 4) + kt) * 512,
+//           byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 within it. This is
+//           the order in which tcgen05.cp (32x128b, repeated for the four warps)
+//           lays a tile into tensor memory where the block-scaled MMA reads it:
+//           lane r % 32, column r / 32, byte b, so a tile is one 512-byte copy
+//           in and one instruction on. Rows and blocks past the end hold 0.
+#pragma once
+
+#include "kp_internal.cuh"
+
+namespace kp {
+
+// Device properties of the current device and its error word (kp_api.cu).
+struct FfnDev {
+    int dev = 0;
+    int sms = 0;
+    int *err = nullptr;
+};
+int ffn_device(FfnDev *out);   // KP_OK, or a status with the message set (KP_EDEVICE included)
+
+// Tensor map of a row-major matrix of 16-bit elements (KP_BF16, KP_FP16) or of
+// bytes (kMapU8), box_cols x box_rows, 128-byte swizzle, zero fill outside.
+constexpr int kMapU8 = 16;
+cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld,
+                           int box_rows, int box_cols, int dtype);
+// Shared memory to request for a CTA that holds `cols` TMEM columns: at least
+// cols/512 of the SM's, so CTAs that share an SM never need more than 512
+// columns together and no allocation can wait for a CTA that waits for it.
+cudaError_t ffn_smem_for_tmem(int dev, uint32_t cols, size_t need, size_t *smem);
+
+// One operand in the microscaled layout.
+struct Mx4Mat {
+    const uint8_t *codes = nullptr;
+    const uint8_t *scales = nullptr;
+};
+inline int64_t mx4_blocks(int64_t cols) { return (cols + 31) / 32; }
+inline int64_t mx4_pitch(int64_t cols) { return mx4_blocks(cols) * 16; }
+inline int64_t mx4_ktiles(int64_t cols) { return (mx4_blocks(cols) + 3) / 4; }
+inline size_t mx4_code_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * mx4_pitch(cols); }
+inline size_t mx4_scale_bytes(int64_t rows, int64_t cols) {
+    return static_cast<size_t>((rows + 127) / 128) * mx4_ktiles(cols) * 512;
+}
+// pad: also write the scales of the rows that fill the last 128-row tile
+// (operands that outlive the call); without it those bytes stay as they are,
+// which only reaches products of rows that do not exist.
+cudaError_t mx4_quantize_launch(const void *x, int64_t ldx, int rows, int cols, int dtype, uint8_t *codes,
+                                uint8_t *scales, bool pad, int sms, cudaStream_t s);
+cudaError_t mx4_dequantize_launch(const uint8_t *codes, const uint8_t *scales, int rows, int cols, void *y,
+                                  int64_t ldy, int dtype, int sms, cudaStream_t s);
+
+// One forward product: y[M, N] = round(x W^T), or with Wb the gated block
+// h[M, N] = round(act(x Wa^T) * (x Wb^T)), over 16-bit or microscaled operands.
+struct FfnArgs {
+    bool mx4 = false;
+    bool gated = false;
+    int act = 0;                 // enum kp_act
+    int dtype = KP_BF16;         // x and W (16-bit), y, g, u
+    const void *x = nullptr;     // 16-bit: [M, ldx]
+    int64_t ldx = 0;
+    const void *Wa = nullptr, *Wb = nullptr;   // 16-bit: [N, lda / ldb]
+    int64_t lda = 0, ldb = 0;
+    Mx4Mat qx, qa, qb;           // microscaled operands
+    void *y = nullptr;
+    int64_t ldy = 0;
+    void *g = nullptr, *u = nullptr;   // optional, 16-bit gated: both products, rounded, [M, N]
+    int M = 0, N = 0, K = 0;
+    float *ws = nullptr;         // split-K partial tiles
+    bool pdl = false;            // launched behind a kernel that writes only qx
+    int *err = nullptr;
+};
+// Few tokens: weight streaming, split-K over a cluster (kp_ffn_stream.cu).
+size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms);   // bytes
+cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s);
+
+}  // namespace kp
+
+#if defined(__CUDACC__)
+
+namespace kp {
+
+// ---- activations ------------------------------------------------------------
+// act(g), in fp32.
+__device__ __forceinline__ float ffn_act(float g, int act) {
+    if (act == KP_ACT_SILU) return __fdividef(g, 1.f + __expf(-g));
+    if (act == KP_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+    // 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)), z = sqrt(2/pi) (g + 0.044715 g^3)
+    const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+    return __fdividef(g, 1.f + __expf(-z2));
+}
+
+// ---- shared-memory matrix descriptors ----------------------------------------
+// K-major, 128-byte swizzle: 8-row groups of 1024 bytes.
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+// A 512-byte scale tile: no swizzle, 8-row (of 16 bytes) groups of 128 bytes.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// ---- tcgen05 --------------------------------------------------------------------
+// Scale tile from shared memory into four TMEM columns: lane i of each of the
+// four 32-lane quarters gets 16-byte row i.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// D[tmem] (+)= (sA * A) (sB * B)^T over 64 E2M1 columns, one E8M0 scale per 32.
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sa, uint32_t sb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// 32 lanes x 32 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]),
+          "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+          "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+// kind::f16 instruction descriptor: D fp32, A and B bf16 or fp16, M x N tile;
+// a_mn / b_mn: that operand is stored with M / N contiguous instead of K.
+__host__ __device__ __forceinline__ uint32_t idesc_f16(int dtype, int M, int N, bool a_mn = false, bool b_mn = false) {
+    const uint32_t ab = dtype == KP_FP16 ? 0u : (1u << 7) | (1u << 10);
+    return (1u << 4) | ab | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// kind::mxf4 instruction descriptor: A and B E2M1 (1), E8M0 scales (bit 23).
+// The scale bytes' position in their 32-bit column goes to bits 29 and 4.
+__host__ __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N) {
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_sf(uint32_t idesc, uint32_t byte) {
+    return idesc | (byte << 29) | (byte << 4);
+}
+
+// Wait (bounded by time only) for a barrier phase; used to drain copies.
+__device__ __forceinline__ void ffn_drain_wait(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > 1000000000ull) break;
+}
+
+}  // namespace kp
+
+#endif  // __CUDACC__

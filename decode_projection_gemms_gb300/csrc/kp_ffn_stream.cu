@@ -1,0 +1,414 @@
+// Forward products for few tokens, where the cost is reading the weights once:
+//     y[m, n] = round( sum_k x[m, k] W[n, k] )                      (plain)
+//     h[m, n] = round( act(sum_k x[m, k] Wg[n, k]) * sum_k x[m, k] Wu[n, k] )   (gated)
+// over bf16 / fp16 operands or over microscaled 4-bit ones.
+//
+// The MMA's 128 rows are output features, its columns the tokens (16 .. 128 a
+// tile, further tiles along the grid's y axis read the weights from L2). The
+// gated form keeps two accumulators, gate and up, over the same token operand,
+// so a thread of the epilogue holds both factors of its outputs. A feature
+// tile's K range is split over the C CTAs of a cluster; their fp32 partial
+// tiles go through L2 and the cluster sums them in rank order, so the result
+// does not depend on timing. A K block is 128 bytes of a row (64 16-bit or 256
+// 4-bit columns), one 16 KB TMA box per weight; a 4-bit stage also brings its
+// scale tiles, which tcgen05.cp lays into the stage's own TMEM columns (their
+// last readers finished before the stage was refilled).
+//
+// Warp 0: copies; warp 1: TMEM and MMA; warps 2 .. 5: epilogue; all six reduce.
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "kp_ffn.cuh"
+
+namespace kp {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kRows = 128;                 // features per tile
+constexpr uint32_t kWBox = kRows * 128;    // one K block of one weight
+constexpr int kMaxTok = 128;               // tokens per tile
+constexpr int kMaxStages = 10;
+constexpr size_t kBarBytes = 256;
+constexpr size_t kMaxSmem = 227 * 1024;
+
+struct StreamParams {
+    const uint8_t *sa, *sb, *sx;   // 4-bit: scale tiles
+    int kt_n;                      // 128-column scale tiles per row tile
+    uint16_t *y, *g, *u;
+    int64_t ldy;
+    float *ws;
+    int *err;
+    int M, N, K, Mpad, KB, C, stages, n_tiles, act, dtype, vec4;
+    uint32_t idesc, tmem_cols, stage_bytes, sf_col;
+};
+
+// TMEM columns of one stage's scales: 8 for each operand.
+constexpr uint32_t sf_cols_of(bool mx4, bool gated) { return mx4 ? (gated ? 24 : 16) : 0; }
+
+template <bool kMx4, bool kGated>
+struct StageLayout {
+    static constexpr uint32_t off_x = kGated ? 2 * kWBox : kWBox;
+    static __host__ __device__ uint32_t off_sc(int Mpad) { return off_x + static_cast<uint32_t>(Mpad) * 128; }
+    static __host__ __device__ uint32_t bytes(int Mpad) {
+        return off_sc(Mpad) + (kMx4 ? (kGated ? 3u : 2u) * 1024u : 0u);
+    }
+};
+
+template <bool kMx4, bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_stream_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
+                      const __grid_constant__ CUtensorMap tmx, const StreamParams p) {
+    using L = StageLayout<kMx4, kGated>;
+    constexpr int kAcc = kGated ? 2 : 1;
+    extern __shared__ uint8_t fs_smem_raw[];
+    const uint32_t raw = smem_u32(fs_smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = fs_smem_raw + (base - raw);
+    const int S = p.stages;
+    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + static_cast<size_t>(S) * p.stage_bytes);
+    uint64_t *empty = full + S;
+    uint64_t *accf = empty + S;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accf + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int C = p.C;
+    const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int tile = static_cast<int>(blockIdx.x) / C;
+    const int m0 = static_cast<int>(blockIdx.y) * p.Mpad;
+    const int Mloc = min(p.M - m0, p.Mpad);
+    const int kb0 = static_cast<int>(static_cast<long long>(p.KB) * rank / C);
+    const int kb1 = static_cast<int>(static_cast<long long>(p.KB) * (rank + 1) / C);
+    const int n_st = kb1 - kb0;
+    const int pre = n_st < S ? n_st : S;
+    const uint32_t xbytes = static_cast<uint32_t>(p.Mpad) * 128;
+    constexpr int kCols = kMx4 ? 128 : 64;   // map columns (bytes or elements) per K block
+
+    // scale tiles that exist of K block kb (two but at the end of K)
+    auto sc_tiles = [&](int kb) { return min(2, p.kt_n - 2 * kb); };
+    auto issue_w = [&](int s, int stage) {
+        const uint64_t pol = policy_evict_first();
+        const int kb = kb0 + s;
+        const uint32_t st = base + stage * p.stage_bytes;
+        const uint32_t bar = smem_u32(full + stage);
+        uint32_t bytes = kAcc * kWBox + xbytes;
+        const uint32_t scb = kMx4 ? 512u * static_cast<uint32_t>(sc_tiles(kb)) : 0u;
+        bytes += scb * (kAcc + 1);
+        mbar_expect_tx(bar, bytes);
+        tma_load_2d(st, &tma, bar, kb * kCols, tile * kRows, pol);
+        if constexpr (kGated) tma_load_2d(st + kWBox, &tmb, bar, kb * kCols, tile * kRows, pol);
+        if constexpr (kMx4) {
+            const size_t off = (static_cast<size_t>(tile) * p.kt_n + 2 * kb) * 512;
+            const uint32_t sc = st + L::off_sc(p.Mpad);
+            bulk_load(sc, p.sa + off, scb, bar);
+            if constexpr (kGated) bulk_load(sc + 1024, p.sb + off, scb, bar);
+        }
+    };
+    auto issue_x = [&](int s, int stage) {
+        const int kb = kb0 + s;
+        const uint32_t st = base + stage * p.stage_bytes;
+        const uint32_t bar = smem_u32(full + stage);
+        tma_load_2d(st + L::off_x, &tmx, bar, kb * kCols, m0, policy_evict_last());
+        if constexpr (kMx4) {
+            const size_t off = (static_cast<size_t>(m0 >> 7) * p.kt_n + 2 * kb) * 512;
+            bulk_load(st + L::off_sc(p.Mpad) + kAcc * 1024, p.sx + off,
+                      512u * static_cast<uint32_t>(sc_tiles(kb)), bar);
+        }
+    };
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(full + s), 1);
+            mbar_init(smem_u32(empty + s), 1);
+        }
+        mbar_init(smem_u32(accf), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        // the weights do not depend on the kernel before: they start at once
+        for (int s = 0; s < pre; ++s) issue_w(s, s);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            pdl_wait();   // x (quantised by the kernel before, when there is one)
+            for (int s = 0; s < pre; ++s) issue_x(s, s);
+            for (int s = pre; s < n_st; ++s) {
+                const int stage = s % S;
+                mbar_wait_bounded(smem_u32(empty + stage), static_cast<uint32_t>(((s / S) - 1) & 1), abort_flag,
+                                  p.err, DEV_TIMEOUT_EMPTY);
+                issue_w(s, stage);
+                issue_x(s, stage);
+            }
+            if (*abort_flag)
+                for (int s = n_st > S ? n_st - S : 0; s < n_st; ++s)
+                    ffn_drain_wait(smem_u32(full + (s % S)), static_cast<uint32_t>((s / S) & 1));
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int s = 0; s < n_st; ++s) {
+                const int stage = s % S;
+                mbar_wait_bounded(smem_u32(full + stage), static_cast<uint32_t>((s / S) & 1), abort_flag, p.err,
+                                  DEV_TIMEOUT_FULL);
+                tc_fence_after();
+                const uint32_t st = base + stage * p.stage_bytes;
+                const uint64_t ad = desc_kmajor(st);
+                const uint64_t bd = desc_kmajor(st + L::off_x);
+                if constexpr (kMx4) {
+                    const int kb = kb0 + s;
+                    const uint32_t sf = tmem + p.sf_col + static_cast<uint32_t>(stage) * sf_cols_of(kMx4, kGated);
+                    const uint32_t sc = st + L::off_sc(p.Mpad);
+                    for (int j = 0; j < sc_tiles(kb); ++j)
+#pragma unroll
+                        for (int o = 0; o <= kAcc; ++o)   // gate, up, tokens
+                            tmem_cp_scales(sf + 8 * o + 4 * j, desc_scales(sc + 1024 * o + 512 * j));
+                    // 64 columns a step; steps past K are left out (their scales are not loaded)
+                    const int steps = min(4, (p.K - kb * 256 + 63) >> 6);
+                    for (int kk = 0; kk < steps; ++kk) {
+                        const uint32_t id = idesc_sf(p.idesc, (kk & 1) * 2);
+                        const uint32_t sfk = sf + 4 * (kk >> 1);
+#pragma unroll
+                        for (int a = 0; a < kAcc; ++a)
+                            umma_mxf4(tmem + a * p.Mpad, ad + (a * kWBox >> 4) + 2 * kk, bd + 2 * kk, id,
+                                      sfk + 8 * a, sfk + 8 * kAcc, (s > 0 || kk > 0) ? 1u : 0u);
+                    }
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                        for (int a = 0; a < kAcc; ++a)
+                            umma_bf16(tmem + a * p.Mpad, ad + (a * kWBox >> 4) + 2 * kk, bd + 2 * kk, p.idesc,
+                                      (s > 0 || kk > 0) ? 1u : 0u);
+                }
+                umma_commit(smem_u32(empty + stage));
+            }
+            umma_commit(smem_u32(accf));
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3;
+        const int row = q * 32 + lane;
+        const int n = tile * kRows + row;
+        mbar_wait_bounded(smem_u32(accf), 0, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
+        tc_fence_after();
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        float *part = p.ws + ((static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C + rank) *
+                                 static_cast<size_t>(kAcc * kRows) * p.Mpad;
+        for (int c0 = 0; c0 < p.Mpad; c0 += 16) {
+            uint32_t va[16], vb[16];
+            tmem_ld16(taddr + c0, va);
+            if constexpr (kGated) tmem_ld16(taddr + p.Mpad + c0, vb);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int m = c0 + i;
+                if (m >= Mloc) continue;
+                const float a = __uint_as_float(va[i]);
+                if (C > 1) {
+                    part[m * kRows + row] = a;
+                    if constexpr (kGated) part[(p.Mpad + m) * kRows + row] = __uint_as_float(vb[i]);
+                } else if (n < p.N) {
+                    const int64_t om = m0 + m;
+                    if constexpr (kGated) {
+                        const float b = __uint_as_float(vb[i]);
+                        p.y[om * p.ldy + n] = elem_round(ffn_act(a, p.act) * b, p.dtype);
+                        if (p.g) {
+                            p.g[om * p.N + n] = elem_round(a, p.dtype);
+                            p.u[om * p.N + n] = elem_round(b, p.dtype);
+                        }
+                    } else {
+                        p.y[om * p.ldy + n] = elem_round(a, p.dtype);
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    }
+
+    if (C > 1) {
+        __syncwarp();
+        cluster_sync_all();   // every partial tile of the cluster is written and visible
+        const size_t stride = static_cast<size_t>(kAcc * kRows) * p.Mpad;
+        const float *parts = p.ws + (static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C * stride;
+        // a warp takes a token, a lane four of its features
+        const int n = tile * kRows + 4 * lane;
+        for (int m = warp * C + rank; m < Mloc; m += (kThreads / 32) * C) {
+            float va[4] = {0.f, 0.f, 0.f, 0.f}, vb[4] = {0.f, 0.f, 0.f, 0.f};
+            const float *src = parts + static_cast<size_t>(m) * kRows + 4 * lane;
+            for (int r = 0; r < C; ++r) {
+                const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + r * stride));
+                va[0] += a.x, va[1] += a.y, va[2] += a.z, va[3] += a.w;
+                if constexpr (kGated) {
+                    const float4 b = __ldcg(reinterpret_cast<const float4 *>(
+                        src + r * stride + static_cast<size_t>(p.Mpad) * kRows));
+                    vb[0] += b.x, vb[1] += b.y, vb[2] += b.z, vb[3] += b.w;
+                }
+            }
+            const int64_t om = m0 + m;
+            auto put = [&](uint16_t *dst, int64_t ld, const float(&v)[4]) {
+                uint16_t *d = dst + om * ld + n;
+                if (p.vec4 && n + 4 <= p.N) {
+                    const uint32_t lo = elem_round(v[0], p.dtype) | static_cast<uint32_t>(elem_round(v[1], p.dtype)) << 16;
+                    const uint32_t hi = elem_round(v[2], p.dtype) | static_cast<uint32_t>(elem_round(v[3], p.dtype)) << 16;
+                    *reinterpret_cast<uint2 *>(d) = make_uint2(lo, hi);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n + i < p.N) d[i] = elem_round(v[i], p.dtype);
+                }
+            };
+            if constexpr (kGated) {
+                float h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = ffn_act(va[i], p.act) * vb[i];
+                put(p.y, p.ldy, h);
+                if (p.g) {
+                    put(p.g, p.N, va);
+                    put(p.u, p.N, vb);
+                }
+            } else {
+                put(p.y, p.ldy, va);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
+}
+
+// ---- launch plan ----------------------------------------------------------------
+
+struct Plan {
+    int Mpad, mt, tiles, KB, C, stages;
+    uint32_t stage_bytes, sf_cols, tmem_cols;
+};
+
+uint32_t stage_bytes_of(bool mx4, bool gated, int Mpad) {
+    if (mx4) return gated ? StageLayout<true, true>::bytes(Mpad) : StageLayout<true, false>::bytes(Mpad);
+    return gated ? StageLayout<false, true>::bytes(Mpad) : StageLayout<false, false>::bytes(Mpad);
+}
+
+Plan make_plan(bool mx4, bool gated, int M, int N, int K, int sms) {
+    Plan q;
+    q.Mpad = std::min((M + 15) / 16 * 16, kMaxTok);
+    q.mt = (M + q.Mpad - 1) / q.Mpad;
+    q.tiles = (N + kRows - 1) / kRows;
+    q.KB = mx4 ? (K + 255) / 256 : (K + 63) / 64;
+    // as many CTAs as there are SMs, while each keeps at least one K block
+    q.C = 1;
+    while (q.C < 8 && static_cast<int64_t>(q.tiles) * q.mt * q.C * 2 <= sms && q.C * 2 <= q.KB) q.C *= 2;
+    q.stage_bytes = stage_bytes_of(mx4, gated, q.Mpad);
+    q.sf_cols = sf_cols_of(mx4, gated);
+    const uint32_t acc = static_cast<uint32_t>(gated ? 2 : 1) * q.Mpad;
+    int st = static_cast<int>((kMaxSmem - 1024 - kBarBytes) / q.stage_bytes);
+    st = std::min(st, kMaxStages);
+    if (mx4) st = std::min(st, static_cast<int>((512 - acc) / q.sf_cols));
+    st = std::min(st, (q.KB + q.C - 1) / q.C);
+    q.stages = st;
+    q.tmem_cols = 32;
+    while (q.tmem_cols < acc + q.sf_cols * st) q.tmem_cols <<= 1;
+    return q;
+}
+
+std::mutex g_mu;
+std::map<int, bool> g_ready;   // devices whose kernels have their shared memory raised
+
+}  // namespace
+
+size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms) {
+    const Plan q = make_plan(mx4, gated, M, N, K, sms);
+    if (q.C == 1) return 0;
+    return static_cast<size_t>(q.mt) * q.tiles * q.C * (gated ? 2 : 1) * kRows * q.Mpad * sizeof(float);
+}
+
+cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s) {
+    const Plan q = make_plan(a.mx4, a.gated, a.M, a.N, a.K, d.sms);
+    if (q.C > 1 && !a.ws) return cudaErrorInvalidValue;
+    using Fn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, StreamParams);
+    static const Fn kernels[2][2] = {{ffn_stream_kernel<false, false>, ffn_stream_kernel<false, true>},
+                                     {ffn_stream_kernel<true, false>, ffn_stream_kernel<true, true>}};
+    cudaError_t e = cudaSuccess;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!g_ready[d.dev]) {
+            for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+                e = cudaFuncSetAttribute(kernels[i >> 1][i & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kMaxSmem));
+            if (e != cudaSuccess) return e;
+            g_ready[d.dev] = true;
+        }
+    }
+    StreamParams p = {};
+    p.sa = a.qa.scales;
+    p.sb = a.qb.scales;
+    p.sx = a.qx.scales;
+    p.kt_n = static_cast<int>(mx4_ktiles(a.K));
+    p.y = static_cast<uint16_t *>(a.y);
+    p.g = static_cast<uint16_t *>(a.g);
+    p.u = static_cast<uint16_t *>(a.u);
+    p.ldy = a.ldy;
+    p.ws = a.ws;
+    p.err = a.err;
+    p.M = a.M;
+    p.N = a.N;
+    p.K = a.K;
+    p.Mpad = q.Mpad;
+    p.KB = q.KB;
+    p.C = q.C;
+    p.stages = q.stages;
+    p.n_tiles = q.tiles;
+    p.act = a.act;
+    p.dtype = a.dtype;
+    // 8-byte stores: y's rows, and g and u's (stride N, 16-byte aligned bases)
+    p.vec4 = a.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && (!a.g || a.N % 4 == 0);
+    p.idesc = a.mx4 ? idesc_mxf4(kRows, q.Mpad) : idesc_f16(a.dtype, kRows, q.Mpad);
+    p.tmem_cols = q.tmem_cols;
+    p.stage_bytes = q.stage_bytes;
+    p.sf_col = static_cast<uint32_t>((a.gated ? 2 : 1) * q.Mpad);
+
+    CUtensorMap ma, mb, mx;
+    if (a.mx4) {
+        const int64_t pitch = mx4_pitch(a.K);
+        e = ffn_tensor_map(&ma, a.qa.codes, a.N, pitch, pitch, kRows, 128, kMapU8);
+        if (e == cudaSuccess && a.gated) e = ffn_tensor_map(&mb, a.qb.codes, a.N, pitch, pitch, kRows, 128, kMapU8);
+        if (e == cudaSuccess) e = ffn_tensor_map(&mx, a.qx.codes, a.M, pitch, pitch, q.Mpad, 128, kMapU8);
+    } else {
+        e = ffn_tensor_map(&ma, a.Wa, a.N, a.K, a.lda, kRows, 64, a.dtype);
+        if (e == cudaSuccess && a.gated) e = ffn_tensor_map(&mb, a.Wb, a.N, a.K, a.ldb, kRows, 64, a.dtype);
+        if (e == cudaSuccess) e = ffn_tensor_map(&mx, a.x, a.M, a.K, a.ldx, q.Mpad, 64, a.dtype);
+    }
+    if (e != cudaSuccess) return e;
+    if (!a.gated) mb = ma;
+
+    size_t smem = 0;
+    e = ffn_smem_for_tmem(d.dev, q.tmem_cols, static_cast<size_t>(q.stages) * q.stage_bytes + 1024 + kBarBytes, &smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(q.tiles * q.C), static_cast<unsigned>(q.mt), 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(q.C);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernels[a.mx4][a.gated], ma, mb, mx, p);
+}
+
+}  // namespace kp

@@ -94,10 +94,12 @@ enum kp_kind {
     KP_KIND_SMALLK = 3 /* CUDA-core small-K kernel (K <= 256), the F_B shape */
 };
 
-/* Element type of x, W, y and the residual in skinny_gemm_ex. */
+/* Element type of x, W, y and the residual in skinny_gemm_ex, and of the
+ * feed-forward operators' 16-bit operands. KP_FP32 only where it is named. */
 enum kp_dtype {
     KP_BF16 = 0,
-    KP_FP16 = 1
+    KP_FP16 = 1,
+    KP_FP32 = 2
 };
 
 enum kp_flags {
@@ -316,6 +318,82 @@ KP_API int kda_proj_run(const kda_plan *plan, const void *x, const void *W_packe
 
 /* Free the plan's scratch (synchronises the device first). NULL is a no-op. */
 KP_API int kda_proj_destroy(kda_plan *plan);
+
+/* ---------------------------------------------------------------------------
+ * Feed-forward operators: microscaled 4-bit quantisation and product, and the
+ * gated block in 16 and in 4 bits with its backward pass.
+ *
+ * Common to all of them: matrices are row-major with the given row stride in
+ * elements (ld* >= columns) and may be views into wider ones; work is enqueued
+ * on `stream` alone; sums are held in fp32 and rounded once to the output's
+ * type; the library allocates nothing and keeps nothing. `work` is the
+ * caller's, 256-byte aligned, of at least kp_ffn_workspace() bytes, and may be
+ * reused once the call's work has completed on its stream: calls in flight on
+ * different streams need workspaces of their own. They can be captured into
+ * CUDA graphs. Outputs must not overlap inputs or each other. Results do not
+ * vary from run to run. Returns KP_OK, KP_EINVAL, KP_EALIGN, KP_ESHAPE,
+ * KP_ENODEV, KP_ECUDA, KP_EDEVICE. */
+
+/* Gate activations: g / (1 + e^-g); g (1 + erf(g / sqrt 2)) / 2; and the tanh
+ * form of the latter, g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. */
+enum kp_act {
+    KP_ACT_SILU = 0,
+    KP_ACT_GELU = 1,
+    KP_ACT_GELU_TANH = 2
+};
+
+/* Operators that take a workspace. */
+enum kp_ffn_op {
+    KP_FFN_MX4_GEMM = 0,
+    KP_FFN_MX4_GATED = 1,
+    KP_FFN_GATED = 2
+};
+
+/* Bytes of `work` for M rows (tokens), N output features (F) and K columns, on
+ * the current device. */
+KP_API int kp_ffn_workspace(int op, int M, int N, int K, size_t *bytes);
+
+/* Microscaled 4-bit storage of a matrix [rows, cols]: blocks of 32 columns of a
+ * row share a power-of-two scale (one byte), elements are 4-bit codes with a
+ * sign, two exponent bits and one mantissa bit (0, .5, 1, 1.5, 2, 3, 4, 6). With
+ * m a block's largest magnitude its scale is 2^(floor(log2 m) - 2), at least
+ * 2^-127, and each element is rounded to the nearest code (ties to even, at most
+ * 6 scales); a block with a NaN or an infinity stands for NaN throughout.
+ *   codes   [rows][ceil(cols / 32) * 16] bytes, the lower column in the low
+ *           half of a byte; columns past the end are 0
+ *   scales  tiles of 128 rows x 4 blocks, 512 bytes each, row tiles outermost;
+ *           row r, block b of a tile at byte (r % 32) * 16 + (r / 32) * 4 + b
+ * kp_mx4_bytes gives both sizes (host only). Both pointers are 16-byte aligned. */
+KP_API int kp_mx4_bytes(int rows, int cols, size_t *code_bytes, size_t *scale_bytes);
+/* x [rows, cols] of dtype KP_BF16, KP_FP16 or KP_FP32, aligned to its elements. */
+KP_API int kp_mx4_quantize(const void *x, int64_t ldx, int rows, int cols, int dtype, void *codes,
+                           void *scales, kp_stream_t stream);
+/* The values the codes stand for, in y [rows, cols] of any of the three types
+ * (exact in bf16 and fp32; fp16 rounds, and overflows to infinity). */
+KP_API int kp_mx4_dequantize(const void *codes, const void *scales, int rows, int cols, void *y,
+                             int64_t ldy, int dtype, kp_stream_t stream);
+
+/* y[M, N] = round( Q(x) Q(W)^T ): the product of two microscaled matrices, W
+ * [N, K] quantised beforehand. x is either a 16-bit matrix [M, K] of y's dtype,
+ * which the call quantises into its workspace, or (x NULL) codes and scales.
+ * Any M >= 0, N, K >= 1. */
+KP_API int kp_mx4_gemm(const void *x, int64_t ldx, const void *x_codes, const void *x_scales,
+                       const void *W_codes, const void *W_scales, void *y, int64_t ldy, int M, int N,
+                       int K, int dtype, void *work, size_t work_bytes, kp_stream_t stream);
+/* h[T, F] = round( act(Q(x) Q(Wg)^T) * (Q(x) Q(Wu)^T) ), the same way. */
+KP_API int kp_mx4_gated_ffn(const void *x, int64_t ldx, const void *x_codes, const void *x_scales,
+                            const void *Wg_codes, const void *Wg_scales, const void *Wu_codes,
+                            const void *Wu_scales, void *h, int64_t ldh, int T, int F, int K, int act,
+                            int dtype, void *work, size_t work_bytes, kp_stream_t stream);
+
+/* Gated block h[T, F] = round( act(x Wg^T) * (x Wu^T) ), x [T, K], Wg and Wu
+ * [F, K], all of dtype KP_BF16 or KP_FP16; x, Wg and Wu 16-byte aligned with
+ * row strides and K multiples of 8. g and u (both or neither; contiguous
+ * [T, F], 16-byte aligned) receive the two products for the backward pass,
+ * rounded to dtype as the tensor cores that read them there need it. */
+KP_API int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg, const void *Wu,
+                        int64_t ldu, void *h, int64_t ldh, void *g, void *u, int T, int F, int K,
+                        int act, int dtype, void *work, size_t work_bytes, kp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics. */
