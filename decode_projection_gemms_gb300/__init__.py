@@ -8,7 +8,8 @@ from __future__ import annotations
 
 __all__ = ["KdaPlan", "KpCfg", "KdaProjError", "skinny_gemm", "select_config", "make_events",
            "table_load", "table_clear", "device_error", "check_device",
-           "Mx4Tensor", "mx4_quantize", "mx4_dequantize", "mx4_gemm", "mx4_gated_ffn", "gated_ffn"]
+           "Mx4Tensor", "mx4_quantize", "mx4_dequantize", "mx4_gemm", "mx4_gated_ffn", "gated_ffn",
+           "gated_ffn_backward"]
 
 
 def __getattr__(name):

@@ -32,7 +32,7 @@ FLAG_FUSE_FB = 2
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 # enum kp_act, enum kp_ffn_op
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
-FFN_MX4_GEMM, FFN_MX4_GATED, FFN_GATED = 0, 1, 2
+FFN_MX4_GEMM, FFN_MX4_GATED, FFN_GATED, FFN_GATED_BACKWARD = 0, 1, 2, 3
 BRANCH_QKVG, BRANCH_FAB, BRANCH_FB = 0, 1, 2
 
 # exported symbols (must match include/kdaproj.h)
@@ -43,7 +43,7 @@ EXPORTS = (
     "kp_device_error", "kp_scratch_bytes", "skinny_gemm_noalloc", "skinny_gemm_ex",
     "kp_selftest_timeout", "kp_pdl_consumer_checksum",
     "kp_ffn_workspace", "kp_mx4_bytes", "kp_mx4_quantize", "kp_mx4_dequantize", "kp_mx4_gemm",
-    "kp_mx4_gated_ffn", "kp_gated_ffn",
+    "kp_mx4_gated_ffn", "kp_gated_ffn", "kp_gated_ffn_backward",
 )
 DEV_SELFTEST = 5   # device error code of kp_selftest_timeout
 
@@ -117,6 +117,8 @@ def load(path: str | None = None):
             "kp_mx4_gemm": [vp, i64, vp, vp, vp, vp, vp, i64, ci, ci, ci, ci, vp, sz, vp],
             "kp_mx4_gated_ffn": [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, ci, ci, ci, ci, ci, vp, sz, vp],
             "kp_gated_ffn": [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp, sz, vp],
+            "kp_gated_ffn_backward": [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci,
+                                      vp, sz, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -558,6 +560,36 @@ def gated_ffn(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "s
                                    g.data_ptr() if save else None, u.data_ptr() if save else None, T, F, K, code,
                                    _DTYPES[x.dtype], *_work_args(work), on.handle))
     return (h, g, u) if save else h
+
+
+def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, g: torch.Tensor,
+                       u: torch.Tensor, act: str = "silu", stream=None):
+    """Gradients ``(dx, dWg, dWu)`` of ``gated_ffn`` for the gradient ``dh`` of its
+    output, from its operands and the ``g`` and ``u`` it saved. ``dG = dh u act'(g)``
+    and ``dU = dh act(g)`` are computed in fp32 and rounded to x's type as the
+    tensor cores' operands; the three products are summed in fp32. With no tokens
+    the weights' gradients are zero."""
+    code = _act_code(act)
+    T, F, K, ldx, ldg, ldu = _gated_operands(x, Wg, Wu)
+    dev = x.device
+    lddh = _rows(dh, "dh", x.dtype, dev)
+    for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
+        if t is not dh:
+            _rows(t, name, x.dtype, dev)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if tuple(t.shape) != (T, F):
+            raise ValueError(f"{name} must be {(T, F)}, got {tuple(t.shape)}")
+    with _On(dev, stream) as on:
+        dx = torch.empty((T, K), dtype=x.dtype, device=dev)
+        dWg = torch.empty((F, K), dtype=x.dtype, device=dev)
+        dWu = torch.empty((F, K), dtype=x.dtype, device=dev)
+        work = _work(FFN_GATED_BACKWARD, T, F, K, dev)
+        _check(load().kp_gated_ffn_backward(dh.data_ptr(), lddh, x.data_ptr(), ldx, Wg.data_ptr(), ldg,
+                                            Wu.data_ptr(), ldu, g.data_ptr(), u.data_ptr(), dx.data_ptr(),
+                                            dWg.data_ptr(), dWu.data_ptr(), T, F, K, code, _DTYPES[x.dtype],
+                                            *_work_args(work), on.handle))
+    return dx, dWg, dWu
 
 
 class KdaPlan:

@@ -35,6 +35,8 @@ SOURCES = [
     "kp_noalloc.cu",
     "kp_mx4.cu",
     "kp_ffn_stream.cu",
+    "kp_ffn_tile.cu",
+    "kp_ffn_bwd.cu",
     "kp_ffn_api.cu",
 ]
 HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh", "kp_ffn.cuh"]

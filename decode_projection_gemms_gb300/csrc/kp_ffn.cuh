@@ -31,6 +31,8 @@ int ffn_device(FfnDev *out);   // KP_OK, or a status with the message set (KP_ED
 constexpr int kMapU8 = 16;
 cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld,
                            int box_rows, int box_cols, int dtype);
+// The scale tiles of a microscaled matrix, 512 bytes each, boxes of two.
+cudaError_t ffn_scale_map(CUtensorMap *map, const void *scales, int64_t tiles);
 // Shared memory to request for a CTA that holds `cols` TMEM columns: at least
 // cols/512 of the SM's, so CTAs that share an SM never need more than 512
 // columns together and no allocation can wait for a CTA that waits for it.
@@ -80,6 +82,41 @@ struct FfnArgs {
 size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms);   // bytes
 cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s);
 
+// One launch of the tile kernel (kp_ffn_tile.cu), for many tokens and for the
+// backward pass. D[m, n] = sum_k A[m, k] B[n, k], D row-major.
+enum FfnTileForm {
+    TILE_GATED,       // A = x, B = Wg and Wu side by side: h (and g, u)
+    TILE_MX4_GATED,   // the same over microscaled operands
+    TILE_MX4,         // A = x, B = W, microscaled: y
+    TILE_DX,          // D = A0 B0 + A1 B1, A = dG, dU [m, k], B = Wg, Wu stored [k, n]
+    TILE_DW           // D0 = A0 B0, D1 = A1 B0, A = dG, dU stored [k, m], B = x stored [k, n]
+};
+struct FfnTileArgs {
+    int form = TILE_GATED;
+    int act = 0, dtype = KP_BF16;
+    const void *A0 = nullptr, *A1 = nullptr, *B0 = nullptr, *B1 = nullptr;
+    int64_t lda = 0, ldb0 = 0, ldb1 = 0;
+    Mx4Mat qa, qb0, qb1;
+    void *y0 = nullptr, *y1 = nullptr;
+    int64_t ldy = 0;
+    void *g = nullptr, *u = nullptr;
+    int M = 0, N = 0, K = 0;     // D is M x N (gated: N = F); K per product
+    float *ws = nullptr;         // TILE_DX: split-K partial sums
+    bool pdl = false;
+    int *err = nullptr;
+};
+// Split-K partial sums of TILE_DX, bytes (0: it does not split).
+size_t ffn_tile_scratch(int form, int M, int N, int K, int sms);
+cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t s);
+
+// Whether a forward product takes the tile kernel or the weight-streaming one.
+bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms);
+
+// dG = dh u act'(g), dU = dh act(g): the gradients of both products, [T, F]
+// with row stride ld (kp_ffn_bwd.cu).
+cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const void *g, const void *u, void *dg, void *du,
+                                 int64_t ld, int T, int F, int act, int dtype, int sms, cudaStream_t s);
+
 }  // namespace kp
 
 #if defined(__CUDACC__)
@@ -94,6 +131,25 @@ __device__ __forceinline__ float ffn_act(float g, int act) {
     // 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)), z = sqrt(2/pi) (g + 0.044715 g^3)
     const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
     return __fdividef(g, 1.f + __expf(-z2));
+}
+
+// act(g) and act'(g), in fp32.
+__device__ __forceinline__ void ffn_act_grad(float g, int act, float &a, float &da) {
+    if (act == KP_ACT_SILU) {
+        const float s = __fdividef(1.f, 1.f + __expf(-g));
+        a = ffn_act(g, act);
+        da = s * (1.f + g * (1.f - s));
+    } else if (act == KP_ACT_GELU) {
+        const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
+        a = g * cdf;
+        da = cdf + g * 0.39894228040143268f * __expf(-0.5f * g * g);
+    } else {
+        // a = g s(w), s the logistic function, w = 2 sqrt(2/pi) (g + 0.044715 g^3)
+        const float w = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+        const float s = __fdividef(1.f, 1.f + __expf(-w));
+        a = ffn_act(g, act);
+        da = s + g * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * g * g);
+    }
 }
 
 // ---- shared-memory matrix descriptors ----------------------------------------

@@ -52,6 +52,20 @@ cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int6
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t ffn_scale_map(CUtensorMap *map, const void *scales, int64_t tiles) {
+    EncodeFn enc;
+    cudaError_t e = encoder(&enc);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(tiles)};   // 32-bit words
+    const cuuint64_t strides[1] = {512};
+    const cuuint32_t box[2] = {128, 2};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(scales), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t ffn_smem_for_tmem(int dev, uint32_t cols, size_t need, size_t *smem) {
     static std::mutex mu;
     static int known = -1, sm_smem = 0, reserved = 0;   // the last device asked about
@@ -111,6 +125,38 @@ static int check_workspace(const char *fn, const void *work, size_t have, size_t
 
 static size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
+// Which kernel a forward product takes: see ffn_use_tile.
+static size_t forward_scratch(bool mx4, bool gated, int M, int N, int K, int sms) {
+    return ffn_use_tile(mx4, gated, M, N, K, sms) ? 0 : ffn_stream_scratch(mx4, gated, M, N, K, sms);
+}
+
+static cudaError_t forward_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s) {
+    if (!ffn_use_tile(a.mx4, a.gated, a.M, a.N, a.K, d.sms)) return ffn_stream_launch(a, d, s);
+    FfnTileArgs t;
+    t.form = !a.mx4 ? TILE_GATED : a.gated ? TILE_MX4_GATED : TILE_MX4;
+    t.act = a.act;
+    t.dtype = a.dtype;
+    t.A0 = a.x;
+    t.B0 = a.Wa;
+    t.B1 = a.Wb;
+    t.lda = a.ldx;
+    t.ldb0 = a.lda;
+    t.ldb1 = a.ldb;
+    t.qa = a.qx;
+    t.qb0 = a.qa;
+    t.qb1 = a.qb;
+    t.y0 = a.y;
+    t.ldy = a.ldy;
+    t.g = a.g;
+    t.u = a.u;
+    t.M = a.M;
+    t.N = a.N;
+    t.K = a.K;
+    t.pdl = a.pdl;
+    t.err = a.err;
+    return ffn_tile_launch(t, d, s);
+}
+
 // 4-bit products: x's codes, x's scales, split-K partial tiles.
 struct Mx4Work {
     size_t scales, part, bytes;
@@ -119,7 +165,21 @@ static Mx4Work mx4_work(bool gated, int M, int N, int K, int sms) {
     Mx4Work w;
     w.scales = up256(mx4_code_bytes(M, K));
     w.part = w.scales + up256(mx4_scale_bytes(M, K));
-    w.bytes = w.part + ffn_stream_scratch(true, gated, M, N, K, sms);
+    w.bytes = w.part + forward_scratch(true, gated, M, N, K, sms);
+    return w;
+}
+
+// Backward: dG and dU [T][F rounded up to 8] in 16 bits, then dx's partial sums.
+struct BwdWork {
+    size_t du, part, bytes;
+    int64_t ld;
+};
+static BwdWork bwd_work(int T, int F, int K, int sms) {
+    BwdWork w;
+    w.ld = (static_cast<int64_t>(F) + 7) / 8 * 8;
+    w.du = up256(static_cast<size_t>(T) * w.ld * 2);
+    w.part = 2 * w.du;
+    w.bytes = w.part + ffn_tile_scratch(TILE_DX, T, K, F, sms);
     return w;
 }
 
@@ -164,7 +224,7 @@ static int mx4_product(const char *fn, FfnArgs a, const void *x, int64_t ldx, co
     } else {
         a.qx = {static_cast<const uint8_t *>(x_codes), static_cast<const uint8_t *>(x_scales)};
     }
-    e = ffn_stream_launch(a, d, s);
+    e = forward_launch(a, d, s);
     if (e != cudaSuccess) return cuda_failed(e, fn);
     return KP_OK;
 }
@@ -235,7 +295,10 @@ int kp_ffn_workspace(int op, int M, int N, int K, size_t *bytes) {
         if (M) *bytes = mx4_work(op == KP_FFN_MX4_GATED, M, N, K, d.sms).bytes;
         return KP_OK;
     case KP_FFN_GATED:
-        if (M) *bytes = ffn_stream_scratch(false, true, M, N, K, d.sms);
+        if (M) *bytes = forward_scratch(false, true, M, N, K, d.sms);
+        return KP_OK;
+    case KP_FFN_GATED_BACKWARD:
+        if (M) *bytes = bwd_work(M, N, K, d.sms).bytes;
         return KP_OK;
     default: return set_error(KP_EINVAL, "kp_ffn_workspace: unknown operator %d", op);
     }
@@ -291,7 +354,7 @@ int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg, const 
         return set_error(KP_EALIGN, "%s: g and u must be 16-byte aligned", fn);
     FfnDev d;
     if ((rc = ffn_device(&d))) return rc;
-    const size_t need = ffn_stream_scratch(false, true, T, F, K, d.sms);
+    const size_t need = forward_scratch(false, true, T, F, K, d.sms);
     if ((rc = check_workspace(fn, work, work_bytes, need))) return rc;
     FfnArgs a;
     a.gated = true;
@@ -312,8 +375,70 @@ int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg, const 
     a.K = K;
     a.ws = static_cast<float *>(work);
     a.err = d.err;
-    cudaError_t e = ffn_stream_launch(a, d, stream);
+    cudaError_t e = forward_launch(a, d, stream);
     return e == cudaSuccess ? KP_OK : cuda_failed(e, fn);
+}
+
+int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx, const void *Wg, int64_t ldg,
+                          const void *Wu, int64_t ldu, const void *g, const void *u, void *dx, void *dWg, void *dWu,
+                          int T, int F, int K, int act, int dtype, void *work, size_t work_bytes,
+                          kp_stream_t stream) {
+    const char *fn = "kp_gated_ffn_backward";
+    if (T < 0 || F < 1 || K < 1) return bad_sizes(fn, T, F, K);
+    if (!is16(dtype)) return set_error(KP_EINVAL, "%s: unknown element type %d", fn, dtype);
+    if (!is_act(act)) return set_error(KP_EINVAL, "%s: unknown activation %d", fn, act);
+    if (K & 7) return set_error(KP_ESHAPE, "%s: K=%d is not a multiple of 8", fn, K);
+    if (!dWg || !dWu) return set_error(KP_EINVAL, "%s: dWg or dWu is NULL", fn);
+    if (misaligned(dWg, 16) || misaligned(dWu, 16))
+        return set_error(KP_EALIGN, "%s: dWg and dWu must be 16-byte aligned", fn);
+    int rc;
+    FfnDev d;
+    if (T == 0) {   // no tokens: the weights' gradients are zero
+        if ((rc = ffn_device(&d))) return rc;
+        cudaError_t e = cudaMemsetAsync(dWg, 0, static_cast<size_t>(F) * K * 2, stream);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dWu, 0, static_cast<size_t>(F) * K * 2, stream);
+        return e == cudaSuccess ? KP_OK : cuda_failed(e, fn);
+    }
+    if ((rc = check_operand(fn, "x", x, ldx, K)) || (rc = check_operand(fn, "Wg", Wg, ldg, K)) ||
+        (rc = check_operand(fn, "Wu", Wu, ldu, K)) || (rc = check_output(fn, "dh", dh, lddh, F)))
+        return rc;
+    if (!g || !u || !dx) return set_error(KP_EINVAL, "%s: g, u or dx is NULL", fn);
+    if (misaligned(g, 16) || misaligned(u, 16) || misaligned(dx, 16))
+        return set_error(KP_EALIGN, "%s: g, u and dx must be 16-byte aligned", fn);
+    if ((rc = ffn_device(&d))) return rc;
+    const BwdWork w = bwd_work(T, F, K, d.sms);
+    if ((rc = check_workspace(fn, work, work_bytes, w.bytes))) return rc;
+    uint8_t *base = static_cast<uint8_t *>(work);
+    cudaError_t e = ffn_gate_grad_launch(dh, lddh, g, u, base, base + w.du, w.ld, T, F, act, dtype, d.sms, stream);
+    if (e != cudaSuccess) return cuda_failed(e, fn);
+    FfnTileArgs t;
+    t.form = TILE_DX;
+    t.dtype = dtype;
+    t.A0 = base;
+    t.A1 = base + w.du;
+    t.lda = w.ld;
+    t.B0 = Wg;
+    t.B1 = Wu;
+    t.ldb0 = ldg;
+    t.ldb1 = ldu;
+    t.y0 = dx;
+    t.ldy = K;
+    t.M = T;
+    t.N = K;
+    t.K = F;
+    t.ws = reinterpret_cast<float *>(base + w.part);
+    t.err = d.err;
+    if ((e = ffn_tile_launch(t, d, stream)) != cudaSuccess) return cuda_failed(e, fn);
+    t.form = TILE_DW;
+    t.B0 = x;
+    t.ldb0 = ldx;
+    t.y0 = dWg;
+    t.y1 = dWu;
+    t.M = F;
+    t.N = K;
+    t.K = T;
+    if ((e = ffn_tile_launch(t, d, stream)) != cudaSuccess) return cuda_failed(e, fn);
+    return KP_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,67 @@
+// Gradients of the gated block's two products, element by element:
+//     dU = dh act(g),   dG = dh u act'(g).
+// Three matrices read and two written, nothing reused: bound by HBM. They are
+// rounded to 16 bits because the tensor cores of the three products behind them
+// read 16-bit operands; everything before that rounding is fp32.
+#include "kp_ffn.cuh"
+
+namespace kp {
+
+namespace {
+
+__global__ void __launch_bounds__(256)
+    gate_grad_kernel(const uint16_t *__restrict__ dh, int64_t lddh, const uint16_t *__restrict__ g,
+                     const uint16_t *__restrict__ u, uint16_t *__restrict__ dg, uint16_t *__restrict__ du,
+                     int64_t ld, int T, int F, int act, int dtype, int vec) {
+    const int chunks = (F + 7) >> 3;
+    const int64_t total = static_cast<int64_t>(T) * chunks;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t t = i / chunks;
+        const int f = static_cast<int>(i - t * chunks) * 8;
+        union {
+            uint4 v;
+            uint16_t h[8];
+        } a, b, c, og, ou;
+        if (vec) {
+            a.v = __ldg(reinterpret_cast<const uint4 *>(dh + t * lddh + f));
+            b.v = __ldg(reinterpret_cast<const uint4 *>(g + t * F + f));
+            c.v = __ldg(reinterpret_cast<const uint4 *>(u + t * F + f));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const bool in = f + k < F;
+                a.h[k] = in ? dh[t * lddh + f + k] : 0;
+                b.h[k] = in ? g[t * F + f + k] : 0;
+                c.h[k] = in ? u[t * F + f + k] : 0;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float d = elem_widen(a.h[k], dtype);
+            float av, dav;
+            ffn_act_grad(elem_widen(b.h[k], dtype), act, av, dav);
+            ou.h[k] = elem_round(d * av, dtype);
+            og.h[k] = elem_round(d * elem_widen(c.h[k], dtype) * dav, dtype);
+        }
+        // ld is a multiple of 8 and both buffers have its padding
+        *reinterpret_cast<uint4 *>(dg + t * ld + f) = og.v;
+        *reinterpret_cast<uint4 *>(du + t * ld + f) = ou.v;
+    }
+}
+
+}  // namespace
+
+cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const void *g, const void *u, void *dg, void *du,
+                                 int64_t ld, int T, int F, int act, int dtype, int sms, cudaStream_t s) {
+    const int64_t total = static_cast<int64_t>(T) * ((F + 7) / 8);
+    const int64_t blocks = (total + 255) / 256;
+    const int grid = static_cast<int>(blocks < sms * 8LL ? blocks : sms * 8LL);
+    const bool vec = F % 8 == 0 && lddh % 8 == 0 && (reinterpret_cast<uintptr_t>(dh) & 15) == 0;
+    gate_grad_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(dh), lddh, static_cast<const uint16_t *>(g),
+                                          static_cast<const uint16_t *>(u), static_cast<uint16_t *>(dg),
+                                          static_cast<uint16_t *>(du), ld, T, F, act, dtype, vec);
+    return cudaGetLastError();
+}
+
+}  // namespace kp

@@ -1,0 +1,514 @@
+// Tile kernel of the feed-forward operators: D[m, n] = sum_k A[m, k] B[n, k] with
+// fp32 accumulation, for many tokens (forward) and for the backward pass, where
+// the tensor cores are the bound.
+//
+// Two CTAs of a cluster (an SM pair) compute one 256 x 256 tile with
+// tcgen05.mma.cta_group::2: each holds 128 rows of A, half of B's 256 rows, and
+// the accumulator rows of its own A, so an operand byte in shared memory feeds
+// twice the products that it would in a tile of one CTA. The leader's warp 1
+// issues every MMA; both CTAs' copies complete on the leader's barriers, and
+// tcgen05.commit returns stages and accumulators to both. Clusters are
+// persistent: a cluster takes items c, c + n, ... of the tile list, whose order
+// keeps a band of row tiles together so that their operands stay in L2.
+//
+// Forms:
+//   gated    B's halves are 128 rows of Wg (CTA 0) and the same 128 of Wu (CTA
+//            1): a thread of the epilogue finds the gate in accumulator column c
+//            and its factor in column 128 + c;
+//   dx       two products into one accumulator (dG Wg, then dU Wu), Wg and Wu
+//            read as they lie, N contiguous (the MMA's transposed operand). With
+//            few tokens the contraction is split over clusters, whose fp32
+//            partial sums a second kernel adds in order;
+//   dW       two outputs in one tile list (dG^T x and dU^T x), both operands
+//            with K (the tokens) strided;
+//   4-bit    kind::mxf4; scale tiles go to TMEM columns of their stage. The
+//            accumulator and the scales fill the tensor memory, so these have
+//            one accumulator, the 16-bit forms two.
+//
+// Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 5: epilogue.
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "kp_ffn.cuh"
+
+namespace kp {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kTile = 256;                // rows of D per cluster; columns too
+constexpr uint32_t kHalf = 128 * 128;     // bytes of 128 rows of a K block (128 bytes of K)
+constexpr int kBand = 8;                  // row tiles kept together in the tile order
+constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kBarBytes = 256;
+
+struct TileMaps {
+    CUtensorMap a0, a1, b0, b1, sa, sb0, sb1;
+};
+
+struct TileParams {
+    uint16_t *y0, *y1, *g, *u;
+    int64_t ldy;
+    float *ws;
+    int *err;
+    int M, N, K;
+    int tiles_m, tiles_n, items, splits;
+    int KB1, KB;         // K blocks of the first product, of all
+    int kt_n;            // 4-bit: scale tiles per row tile
+    int act, dtype, vec, nacc, stages;
+    uint32_t idesc;
+};
+
+// ---- cta_group::2 forms ----------------------------------------------------------
+__device__ __forceinline__ void pair_load(uint32_t dst, const void *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint32_t bar) {   // the same barrier in both CTAs
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                              uint32_t sb, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void pair_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {   // shared::cluster address
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Operand stored with M / N contiguous, 128-byte swizzle: 64-element groups
+// 8 KB apart (64 K rows of 128 bytes), 8 K rows 1 KB apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(8192 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
+    return elem_round(a, dtype) | static_cast<uint32_t>(elem_round(b, dtype)) << 16;
+}
+
+// 32 consecutive outputs of one row.
+__device__ __forceinline__ void put_row32(uint16_t *dst, const float (&v)[32], int left, bool vec, int dtype) {
+    if (vec && left >= 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] =
+                make_uint4(pack2(v[8 * i], v[8 * i + 1], dtype), pack2(v[8 * i + 2], v[8 * i + 3], dtype),
+                           pack2(v[8 * i + 4], v[8 * i + 5], dtype), pack2(v[8 * i + 6], v[8 * i + 7], dtype));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) dst[i] = elem_round(v[i], dtype);
+    }
+}
+
+template <int kForm>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    ffn_tile_kernel(const __grid_constant__ TileMaps tm, const TileParams p) {
+    constexpr bool kMx4 = kForm == TILE_MX4 || kForm == TILE_MX4_GATED;
+    constexpr bool kGated = kForm == TILE_GATED || kForm == TILE_MX4_GATED;
+    constexpr bool kAMn = kForm == TILE_DW;
+    constexpr bool kBMn = kForm == TILE_DW || kForm == TILE_DX;
+    constexpr uint32_t kStage = 2 * kHalf + (kMx4 ? 3 * 1024 : 0);
+    constexpr int kCols = kMx4 ? 128 : 64;      // map columns per K block, K-major operands
+    constexpr int kNt = kGated ? 128 : 256;     // outputs of a tile along N
+    constexpr uint32_t kSfCol = 256, kSfStage = 24;   // 4-bit: scale columns (A 8, B 16 a stage)
+
+    extern __shared__ uint8_t ft_smem_raw[];
+    const uint32_t raw = smem_u32(ft_smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = ft_smem_raw + (base - raw);
+    const int S = p.stages;
+    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + static_cast<size_t>(S) * kStage);
+    uint64_t *empty = full + S;
+    uint64_t *accf = empty + S;
+    uint64_t *acce = accf + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int cid = static_cast<int>(blockIdx.x) >> 1;
+    const int nclu = static_cast<int>(gridDim.x) >> 1;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(full + s), 1);
+            mbar_init(smem_u32(empty + s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(accf + i), 1);
+            mbar_init(smem_u32(acce + i), 8);   // four epilogue warps of each CTA
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync_all();   // barriers of both CTAs exist
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    struct Item {
+        int z, split, m0, n0, kb0, kb1;
+    };
+    const int tiles = p.tiles_m * p.tiles_n;
+    auto item_at = [&](int i) {
+        Item it;
+        const int per = tiles * p.splits;
+        it.z = i / per;
+        i -= it.z * per;
+        it.split = i / tiles;
+        i -= it.split * tiles;
+        // bands of kBand row tiles, column tiles within a band, rows innermost
+        const int band = i / (kBand * p.tiles_n);
+        const int r = i - band * kBand * p.tiles_n;
+        const int h = min(kBand, p.tiles_m - band * kBand);
+        it.m0 = (band * kBand + r % h) * kTile;
+        it.n0 = r / h * kNt;
+        it.kb0 = static_cast<int>(static_cast<long long>(p.KB) * it.split / p.splits);
+        it.kb1 = static_cast<int>(static_cast<long long>(p.KB) * (it.split + 1) / p.splits);
+        return it;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            pdl_wait();
+            int kc = 0;   // K blocks of this cluster so far
+            for (int i = cid; i < p.items; i += nclu) {
+                const Item it = item_at(i);
+                const int m = it.m0 + rank * 128;
+                for (int kb = it.kb0; kb < it.kb1; ++kb, ++kc) {
+                    const int stage = kc % S;
+                    if (kc >= S)
+                        mbar_wait_bounded(smem_u32(empty + stage), static_cast<uint32_t>((kc / S - 1) & 1),
+                                          abort_flag, p.err, DEV_TIMEOUT_EMPTY);
+                    const uint32_t st = base + stage * kStage;
+                    const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+                    if (rank == 0) mbar_expect_tx(smem_u32(full + stage), 2 * kStage);
+                    const bool second = kForm == TILE_DX && kb >= p.KB1;
+                    const int k = second ? kb - p.KB1 : kb;
+                    const CUtensorMap *ma = (kForm == TILE_DX && second) || (kForm == TILE_DW && it.z) ? &tm.a1 : &tm.a0;
+                    if constexpr (kAMn) {
+                        pair_load(st, ma, bar, m, k * 64);
+                        pair_load(st + 8192, ma, bar, m + 64, k * 64);
+                    } else {
+                        pair_load(st, ma, bar, k * kCols, m);
+                    }
+                    const CUtensorMap *mb = (kGated && rank) || second ? &tm.b1 : &tm.b0;
+                    const int n = it.n0 + (kGated ? 0 : rank * 128);
+                    if constexpr (kBMn) {
+                        pair_load(st + kHalf, mb, bar, n, k * 64);
+                        pair_load(st + kHalf + 8192, mb, bar, n + 64, k * 64);
+                    } else {
+                        pair_load(st + kHalf, mb, bar, k * kCols, n);
+                    }
+                    if constexpr (kMx4) {
+                        // the scales of this CTA's A rows and of all 256 B rows
+                        const uint32_t sc = st + 2 * kHalf;
+                        pair_load(sc, &tm.sa, bar, 0, (m >> 7) * p.kt_n + 2 * k);
+                        const int nt = it.n0 >> 7;
+                        pair_load(sc + 1024, &tm.sb0, bar, 0, nt * p.kt_n + 2 * k);
+                        if constexpr (kGated)
+                            pair_load(sc + 2048, &tm.sb1, bar, 0, nt * p.kt_n + 2 * k);
+                        else
+                            pair_load(sc + 2048, &tm.sb0, bar, 0, (nt + 1) * p.kt_n + 2 * k);
+                    }
+                }
+            }
+            // Every copy of this CTA has landed, and every MMA that reads its
+            // shared memory has completed, before it leaves.
+            for (int t = kc > S ? kc - S : 0; t < kc; ++t)
+                ffn_drain_wait(smem_u32(empty + (t % S)), static_cast<uint32_t>((t / S) & 1));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int kc = 0, n_it = 0;
+            for (int i = cid; i < p.items; i += nclu, ++n_it) {
+                const Item it = item_at(i);
+                const int as = n_it % p.nacc;
+                if (n_it >= p.nacc)
+                    mbar_wait_bounded(smem_u32(acce + as), static_cast<uint32_t>((n_it / p.nacc - 1) & 1), abort_flag,
+                                      p.err, DEV_TIMEOUT_ACC_EMPTY);
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(as) * 256;
+                for (int kb = it.kb0; kb < it.kb1; ++kb, ++kc) {
+                    const int stage = kc % S;
+                    mbar_wait_bounded(smem_u32(full + stage), static_cast<uint32_t>((kc / S) & 1), abort_flag, p.err,
+                                      DEV_TIMEOUT_FULL);
+                    tc_fence_after();
+                    const uint32_t st = base + stage * kStage;
+                    const uint64_t ad = kAMn ? desc_mn(st) : desc_kmajor(st);
+                    const uint64_t bd = kBMn ? desc_mn(st + kHalf) : desc_kmajor(st + kHalf);
+                    if constexpr (kMx4) {
+                        const uint32_t sf = tmem + kSfCol + static_cast<uint32_t>(stage) * kSfStage;
+                        const uint32_t sc = st + 2 * kHalf;
+                        // columns: A's tiles 0 and 1 of the block, then for each B's two row tiles
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            pair_cp_scales(sf + 4 * j, desc_scales(sc + 512 * j));
+                            pair_cp_scales(sf + 8 + 8 * j, desc_scales(sc + 1024 + 512 * j));
+                            pair_cp_scales(sf + 12 + 8 * j, desc_scales(sc + 2048 + 512 * j));
+                        }
+                        // steps past K are left out: their scales belong to other rows
+                        const int steps = min(4, (p.K - kb * 256 + 63) >> 6);
+                        for (int kk = 0; kk < steps; ++kk)
+                            pair_mma_mxf4(d, ad + 2 * kk, bd + 2 * kk, idesc_sf(p.idesc, (kk & 1) * 2),
+                                          sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (kb > it.kb0 || kk > 0) ? 1u : 0u);
+                    } else {
+                        // 16 K a step: 32 bytes of a row, or 16 rows of 128 bytes
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            pair_mma_f16(d, ad + kk * (kAMn ? 128 : 2), bd + kk * (kBMn ? 128 : 2), p.idesc,
+                                         (kb > it.kb0 || kk > 0) ? 1u : 0u);
+                    }
+                    pair_commit(smem_u32(empty + stage));
+                }
+                pair_commit(smem_u32(accf + as));
+            }
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3;
+        int n_it = 0;
+        for (int i = cid; i < p.items; i += nclu, ++n_it) {
+            const Item it = item_at(i);
+            const int as = n_it % p.nacc;
+            mbar_wait_bounded(smem_u32(accf + as), static_cast<uint32_t>((n_it / p.nacc) & 1), abort_flag, p.err,
+                              DEV_TIMEOUT_ACC_FULL);
+            tc_fence_after();
+            const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16);
+            const int64_t m = it.m0 + rank * 128 + q * 32 + lane;
+            for (int c = 0; c < kNt; c += 32) {
+                uint32_t va[32];
+                tmem_ld32(t + c, va);
+                const int n = it.n0 + c;
+                const int left = p.N - n;
+                if constexpr (kGated) {
+                    uint32_t vb[32];
+                    tmem_ld32(t + 128 + c, vb);
+                    tmem_ld_wait();
+                    if (m < p.M && left > 0) {
+                        float a[32], b[32], h[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            a[j] = __uint_as_float(va[j]);
+                            b[j] = __uint_as_float(vb[j]);
+                            h[j] = ffn_act(a[j], p.act) * b[j];
+                        }
+                        put_row32(p.y0 + m * p.ldy + n, h, left, p.vec != 0, p.dtype);
+                        if (!kMx4 && p.g) {
+                            put_row32(p.g + m * p.N + n, a, left, p.vec != 0, p.dtype);
+                            put_row32(p.u + m * p.N + n, b, left, p.vec != 0, p.dtype);
+                        }
+                    }
+                } else {
+                    tmem_ld_wait();
+                    if (m < p.M && left > 0) {
+                        float a[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(va[j]);
+                        if (kForm == TILE_DX && p.splits > 1) {
+                            float *dst = p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)   // N is a multiple of 8
+                                if (4 * j < left)
+                                    reinterpret_cast<float4 *>(dst)[j] =
+                                        make_float4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+                        } else {
+                            uint16_t *y = kForm == TILE_DW && it.z ? p.y1 : p.y0;
+                            put_row32(y + m * p.ldy + n, a, left, p.vec != 0, p.dtype);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) remote_arrive(mapa_shared(smem_u32(acce + as), 0));
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync_all();   // the peer is done with this CTA's barriers and memory
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Partial sums [S][M][N] added in order and rounded.
+__global__ void __launch_bounds__(256) join_kernel(const float *ws, int64_t n, int splits, uint16_t *y, int dtype) {
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 1024) {
+        float4 s = *reinterpret_cast<const float4 *>(ws + i);
+        for (int k = 1; k < splits; ++k) {
+            const float4 v = *reinterpret_cast<const float4 *>(ws + k * n + i);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        *reinterpret_cast<uint2 *>(y + i) = make_uint2(pack2(s.x, s.y, dtype), pack2(s.z, s.w, dtype));
+    }
+}
+
+int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// K splits of dx: enough that every SM pair has work, each with at least
+// eight K blocks (a partial tile costs about as much as four to write and add).
+int dx_splits(int M, int N, int KB, int sms) {
+    const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, kTile);
+    int s = 1;
+    while (tiles * (s + 1) <= sms / 2 && KB / (s + 1) >= 8) ++s;
+    return s;
+}
+
+std::mutex g_mu;
+std::map<int, bool> g_ready;
+
+}  // namespace
+
+bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms) {
+    (void)mx4, (void)K;
+    // enough tiles for half of the SM pairs
+    return 4ll * cdiv(M, kTile) * cdiv(N, gated ? 128 : 256) >= sms;
+}
+
+size_t ffn_tile_scratch(int form, int M, int N, int K, int sms) {
+    if (form != TILE_DX) return 0;
+    const int s = dx_splits(M, N, 2 * cdiv(K, 64), sms);
+    return s > 1 ? static_cast<size_t>(s) * M * N * sizeof(float) : 0;
+}
+
+cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t s) {
+    const bool mx4 = a.form == TILE_MX4 || a.form == TILE_MX4_GATED;
+    const bool gated = a.form == TILE_GATED || a.form == TILE_MX4_GATED;
+    using Fn = void (*)(TileMaps, TileParams);
+    static const Fn kernels[] = {ffn_tile_kernel<TILE_GATED>, ffn_tile_kernel<TILE_MX4_GATED>,
+                                 ffn_tile_kernel<TILE_MX4>, ffn_tile_kernel<TILE_DX>, ffn_tile_kernel<TILE_DW>};
+    cudaError_t e = cudaSuccess;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!g_ready[d.dev]) {
+            for (Fn f : kernels)
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
+            if (e != cudaSuccess) return e;
+            g_ready[d.dev] = true;
+        }
+    }
+    TileParams p = {};
+    p.y0 = static_cast<uint16_t *>(a.y0);
+    p.y1 = static_cast<uint16_t *>(a.y1);
+    p.g = static_cast<uint16_t *>(a.g);
+    p.u = static_cast<uint16_t *>(a.u);
+    p.ldy = a.ldy;
+    p.ws = a.ws;
+    p.err = a.err;
+    p.M = a.M;
+    p.N = a.N;
+    p.K = a.K;
+    p.tiles_m = cdiv(a.M, kTile);
+    p.tiles_n = cdiv(a.N, gated ? 128 : 256);
+    p.KB1 = mx4 ? cdiv(a.K, 256) : cdiv(a.K, 64);
+    p.KB = a.form == TILE_DX ? 2 * p.KB1 : p.KB1;
+    p.splits = a.form == TILE_DX ? dx_splits(a.M, a.N, p.KB, d.sms) : 1;
+    const int64_t items = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits * (a.form == TILE_DW ? 2 : 1);
+    if (items > 0x7FFFFFFF || (p.splits > 1 && !a.ws)) return cudaErrorInvalidValue;
+    p.items = static_cast<int>(items);
+    p.kt_n = static_cast<int>(mx4_ktiles(a.K));
+    p.act = a.act;
+    p.dtype = a.dtype;
+    // 16-byte stores: y's rows (and g and u's, stride N)
+    p.vec = a.ldy % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1)) & 15) == 0 &&
+            (!a.g || a.N % 8 == 0);
+    p.nacc = mx4 ? 1 : 2;
+    const size_t stage = 2 * kHalf + (mx4 ? 3 * 1024 : 0);
+    p.stages = static_cast<int>((kMaxSmem - 1024 - kBarBytes) / stage);
+    p.idesc = mx4 ? idesc_mxf4(256, 256)
+                  : idesc_f16(a.dtype, 256, 256, a.form == TILE_DW, a.form == TILE_DW || a.form == TILE_DX);
+
+    TileMaps tm = {};
+    auto map = [&](CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows, int box_cols,
+                   int type) {
+        if (e == cudaSuccess) e = ffn_tensor_map(m, ptr, rows, cols, ld, box_rows, box_cols, type);
+    };
+    if (mx4) {
+        const int64_t pitch = mx4_pitch(a.K);
+        map(&tm.a0, a.qa.codes, a.M, pitch, pitch, 128, 128, kMapU8);
+        map(&tm.b0, a.qb0.codes, a.N, pitch, pitch, 128, 128, kMapU8);
+        if (gated) map(&tm.b1, a.qb1.codes, a.N, pitch, pitch, 128, 128, kMapU8);
+        auto scales = [&](CUtensorMap *m, const Mx4Mat &q, int rows) {
+            if (e == cudaSuccess)
+                e = ffn_scale_map(m, q.scales, static_cast<int64_t>(cdiv(rows, 128)) * p.kt_n);
+        };
+        scales(&tm.sa, a.qa, a.M);
+        scales(&tm.sb0, a.qb0, a.N);
+        if (gated) scales(&tm.sb1, a.qb1, a.N);
+    } else if (a.form == TILE_GATED) {
+        map(&tm.a0, a.A0, a.M, a.K, a.lda, 128, 64, a.dtype);
+        map(&tm.b0, a.B0, a.N, a.K, a.ldb0, 128, 64, a.dtype);
+        map(&tm.b1, a.B1, a.N, a.K, a.ldb1, 128, 64, a.dtype);
+    } else if (a.form == TILE_DX) {
+        map(&tm.a0, a.A0, a.M, a.K, a.lda, 128, 64, a.dtype);
+        map(&tm.a1, a.A1, a.M, a.K, a.lda, 128, 64, a.dtype);
+        map(&tm.b0, a.B0, a.K, a.N, a.ldb0, 64, 64, a.dtype);
+        map(&tm.b1, a.B1, a.K, a.N, a.ldb1, 64, 64, a.dtype);
+    } else {
+        map(&tm.a0, a.A0, a.K, a.M, a.lda, 64, 64, a.dtype);
+        map(&tm.a1, a.A1, a.K, a.M, a.lda, 64, 64, a.dtype);
+        map(&tm.b0, a.B0, a.K, a.N, a.ldb0, 64, 64, a.dtype);
+    }
+    if (e != cudaSuccess) return e;
+
+    size_t smem = 0;
+    if ((e = ffn_smem_for_tmem(d.dev, 512, p.stages * stage + 1024 + kBarBytes, &smem)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u * static_cast<unsigned>(std::min(p.items, d.sms / 2)), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.pdl ? 1 : 0;
+    if ((e = cudaLaunchKernelEx(&cfg, kernels[a.form], tm, p)) != cudaSuccess) return e;
+    if (p.splits > 1) {
+        const int64_t n = static_cast<int64_t>(a.M) * a.N;
+        const int blocks = static_cast<int>(std::min<int64_t>((n / 4 + 255) / 256, static_cast<int64_t>(d.sms) * 8));
+        join_kernel<<<blocks, 256, 0, s>>>(a.ws, n, p.splits, p.y0, a.dtype);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace kp

@@ -346,7 +346,8 @@ enum kp_act {
 enum kp_ffn_op {
     KP_FFN_MX4_GEMM = 0,
     KP_FFN_MX4_GATED = 1,
-    KP_FFN_GATED = 2
+    KP_FFN_GATED = 2,
+    KP_FFN_GATED_BACKWARD = 3
 };
 
 /* Bytes of `work` for M rows (tokens), N output features (F) and K columns, on
@@ -394,6 +395,17 @@ KP_API int kp_mx4_gated_ffn(const void *x, int64_t ldx, const void *x_codes, con
 KP_API int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg, const void *Wu,
                         int64_t ldu, void *h, int64_t ldh, void *g, void *u, int T, int F, int K,
                         int act, int dtype, void *work, size_t work_bytes, kp_stream_t stream);
+
+/* Its gradients, from dh [T, F], x and the weights (as above, the same values as
+ * in the forward call) and its g and u:
+ *   dU = dh act(g), dG = dh u act'(g)   rounded to dtype, as the operands of
+ *   dx [T, K] = dG Wg + dU Wu, dWg [F, K] = dG^T x, dWu [F, K] = dU^T x.
+ * dx, dWg and dWu are contiguous, 16-byte aligned and written, not added to; with
+ * T = 0 the weights' gradients are set to zero. */
+KP_API int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx, const void *Wg,
+                                 int64_t ldg, const void *Wu, int64_t ldu, const void *g, const void *u,
+                                 void *dx, void *dWg, void *dWu, int T, int F, int K, int act, int dtype,
+                                 void *work, size_t work_bytes, kp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics. */

@@ -82,3 +82,30 @@ def gated(x, Wg, Wu, name):
     a, _ = act(g, name)
     ea = D1 * eg + ACT_EPS * g.abs()
     return a * u, ea * (u.abs() + eu) + a.abs() * eu + 2.0 ** -24 * (a * u).abs(), g, eg, u, eu
+
+
+def gated_grads(dh, x, Wg, Wu, name, unit):
+    """{name: (gradient, bound on its error before its own rounding)} of the gated
+    block. g and u reach the backward pass rounded to 16 bits (`unit`), and dG and
+    dU are rounded again as operands; both errors are carried through."""
+    g, eg = product_bounds(x, Wg)
+    u, eu = product_bounds(x, Wu)
+    eg = eg + unit * (g.abs() + eg)
+    eu = eu + unit * (u.abs() + eu)
+    a, da = act(g, name)
+    dg, du = dh * u * da, dh * a
+    d = dh.abs()
+    fp = 2.0 ** -19 * (1 + g.abs())       # act and act' in fp32
+    edg = d * (eu * D1 + (u.abs() + eu) * (D2 * eg + fp))
+    edg = edg + unit * (dg.abs() + edg)
+    edu = d * (D1 * eg + fp)
+    edu = edu + unit * (du.abs() + edu)
+    tiny = 2.0 ** -25                     # fp16 operands below its subnormals
+    edg, edu = edg + tiny, edu + tiny
+    F, T = g.shape[1], g.shape[0]
+    dx = dg @ Wg + du @ Wu
+    edx = edg @ Wg.abs() + edu @ Wu.abs() + acc_bound(dg.abs() + edg, Wg, 2 * F) + acc_bound(du.abs() + edu, Wu, 2 * F)
+    out = {"dx": (dx, edx)}
+    for key, v, e in (("dWg", dg, edg), ("dWu", du, edu)):
+        out[key] = (v.t() @ x, e.t() @ x.abs() + acc_bound((v.abs() + e).t(), x, T))
+    return out

@@ -7,7 +7,7 @@ import torch
 
 import decode_projection_gemms_gb300 as kda
 from decode_projection_gemms_gb300 import binding
-from ffn_ref import close, gated, mx4_values, product_bounds
+from ffn_ref import UNIT, act as act64, close, gated, gated_grads, mx4_values, product_bounds
 
 pytestmark = pytest.mark.gpu
 HALF = (torch.bfloat16, torch.float16)
@@ -105,7 +105,8 @@ def test_quantize_pads_are_zero_and_empty_is_nothing():
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 128, 32), (1, 64, 64), (2, 129, 65), (7, 100, 127), (16, 256, 256),
                                    (17, 300, 257), (33, 127, 384), (64, 513, 640), (100, 999, 1000),
                                    (128, 128, 2048), (129, 257, 513), (1, 4096, 7168), (300, 640, 2050),
-                                   (513, 1025, 777), (1100, 2050, 514)])
+                                   (513, 1025, 777), (1100, 2050, 514),
+                                   (1537, 1921, 1300), (2048, 1024, 256), (700, 3200, 100)])
 def test_mx4_gemm(M, N, K, dtype):
     x = normal(M, K, M + K, dtype)
     W = normal(N, K, N + 1, torch.bfloat16, std=0.02)
@@ -202,12 +203,79 @@ def test_gated_ffn_strided_views():
     assert torch.equal(wide[:, :F], ref) and (wide[:, F:] == 3.0).all()
 
 
+# ---- its backward pass ---------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("T,F,K", [(1, 1, 8), (1, 40, 64), (2, 264, 72), (7, 13, 16), (63, 128, 256), (64, 257, 320),
+                                   (65, 100, 1000), (255, 512, 264), (256, 256, 256), (300, 1000, 520),
+                                   (777, 264, 2056), (1, 2048, 2048), (1030, 1416, 600)])
+def test_gated_ffn_backward(T, F, K, dtype):
+    act = ACTS[(T + F) % 3]
+    x, dh = normal(T, K, T, dtype), normal(T, F, T + 1, dtype, std=0.05)
+    Wg, Wu = normal(F, K, 2, dtype, std=K ** -0.5 * 1.5), normal(F, K, 3, dtype, std=K ** -0.5)
+    _, g, u = kda.gated_ffn(x, Wg, Wu, act=act, save=True)
+    grads = kda.gated_ffn_backward(dh, x, Wg, Wu, g, u, act=act)
+    ref = gated_grads(dh.double(), x.double(), Wg.double(), Wu.double(), act, UNIT[dtype])
+    for got, name in zip(grads, ("dx", "dWg", "dWu")):
+        close(got, *ref[name], f"{name} {T}x{F}x{K}")
+    again = kda.gated_ffn_backward(dh, x, Wg, Wu, g, u, act=act)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    quiet()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_ffn_backward_against_differences(act):
+    """<gradient, direction> against central differences of the 64-bit forward
+    pass. With step e the difference is off by O(e^2) = 1e-8 of the loss's third
+    derivative, far below the operands' rounding, which the bound carries."""
+    T, F, K = 70, 96, 128
+    dt = torch.float16
+    x, dh = normal(T, K, 1, dt), normal(T, F, 2, dt, std=0.05)
+    Wg, Wu = normal(F, K, 3, dt, std=0.12), normal(F, K, 4, dt, std=0.09)
+    _, g, u = kda.gated_ffn(x, Wg, Wu, act=act, save=True)
+    grads = kda.gated_ffn_backward(dh, x, Wg, Wu, g, u, act=act)
+    p = [t.double() for t in (x, Wg, Wu)]
+    ref = gated_grads(dh.double(), *p, act, UNIT[dt])
+
+    def loss(a, b, c):
+        return ((act64(a @ b.t(), act)[0] * (a @ c.t())) * dh.double()).sum()
+
+    e = 1e-4
+    for i, (got, name) in enumerate(zip(grads, ("dx", "dWg", "dWu"))):
+        v = normal(*got.shape, 10 + i).double()
+        hi, lo = list(p), list(p)
+        hi[i], lo[i] = p[i] + e * v, p[i] - e * v
+        diff = (loss(*hi) - loss(*lo)) / (2 * e)
+        tol = ((ref[name][1] + UNIT[dt] * ref[name][0].abs()) * v.abs()).sum() + 1e-5 * diff.abs()
+        assert ((got.double() * v).sum() - diff).abs() <= tol
+
+
+def test_gated_ffn_backward_strided_and_empty():
+    T, F, K = 45, 88, 192
+    x, Wp, dh = normal(T, K, 1, torch.bfloat16), normal(2 * F, K, 2, torch.bfloat16, std=0.1), normal(T, F, 3, torch.bfloat16)
+    _, g, u = kda.gated_ffn(x, Wp[:F], Wp[F:], save=True)
+    ref = kda.gated_ffn_backward(dh, x, Wp[:F], Wp[F:], g, u)
+    for extra, offset in ((8, 0), (1, 2), (3, 0)):
+        got = kda.gated_ffn_backward(strided(dh, extra, offset), strided(x, 8), strided(Wp[:F], 16),
+                                     strided(Wp[F:], 24, 8), g, u)
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    e = torch.empty((0, K), dtype=torch.bfloat16, device="cuda")
+    ef = torch.empty((0, F), dtype=torch.bfloat16, device="cuda")
+    dx, dWg, dWu = kda.gated_ffn_backward(ef, e, Wp[:F], Wp[F:], ef, ef)
+    assert dx.shape == (0, K) and (dWg == 0).all() and (dWu == 0).all() and dWg.shape == (F, K)
+    with pytest.raises(ValueError):
+        kda.gated_ffn_backward(dh[:, :80], x, Wp[:F], Wp[F:], g, u)
+    with pytest.raises(ValueError):
+        kda.gated_ffn_backward(dh, x, Wp[:F], Wp[F:], g.t(), u)
+    quiet()
+
+
 # ---- gated block over 4-bit weights ------------------------------------------------
 
 @pytest.mark.parametrize("dtype", HALF)
 @pytest.mark.parametrize("T,F,K", [(1, 1, 1), (1, 128, 256), (3, 130, 100), (16, 256, 257), (64, 384, 1000),
                                    (100, 127, 64), (128, 128, 640), (129, 500, 513), (8, 2048, 7168),
-                                   (700, 900, 1111)])
+                                   (700, 900, 1111), (1025, 1300, 390), (1300, 1030, 1024)])
 def test_mx4_gated_ffn(T, F, K, dtype):
     act = ACTS[(T + F) % 3]
     x = normal(T, K, T, dtype)
