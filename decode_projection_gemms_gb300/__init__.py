@@ -15,5 +15,6 @@ __all__ = ["KdaPlan", "KpCfg", "KdaProjError", "skinny_gemm", "select_config", "
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)   # looked up once
+        return value
     raise AttributeError(name)

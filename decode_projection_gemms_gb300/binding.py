@@ -8,6 +8,7 @@ built, importing the functions below raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -80,6 +81,8 @@ _lib = None
 def load(path: str | None = None):
     """Load the library (once) and declare its signatures. Raises if absent."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -124,11 +127,10 @@ def load(path: str | None = None):
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = ctypes.c_char_p if name == "kp_last_error" else ci
-        _lib = lib
-        if os.path.exists(TABLE_PATH):
-            rc = lib.kp_table_load(TABLE_PATH.encode())
-            if rc:
-                raise KdaProjError(rc, lib.kp_last_error().decode())
+        rc = lib.kp_table_load(TABLE_PATH.encode()) if os.path.exists(TABLE_PATH) else KP_OK
+        _lib = lib   # seen without the lock: only once the table is in
+        if rc:
+            raise KdaProjError(rc, lib.kp_last_error().decode())
         return _lib
 
 
@@ -305,37 +307,77 @@ def skinny_gemm_noalloc(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor,
 
 
 # ---- feed-forward operators ---------------------------------------------------
+#
+# Every function below runs on the current device and stream: when a stream or a
+# tensor of another device is given, it calls itself with those made current, so
+# that what it allocates is handed out in that stream's order. Single-token calls
+# take a few microseconds on the device, so the checks on the common path are few.
 
 _FFN_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
 _FFN_WORK: dict = {}   # workspace bytes by (device, operator, sizes): host arithmetic only
+_current_device = torch.cuda.current_device
+try:
+    _raw_stream = torch._C._cuda_getCurrentRawStream    # the handle alone, without a Stream object
+except AttributeError:   # pragma: no cover
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
-def _rows(t, name: str, dtype=None, device=None) -> int:
-    """Check a 2-D row-major CUDA matrix (rows may be strided); returns the row
-    stride in elements."""
+_DEVICES: dict = {}
+
+
+def _device(index: int):
+    d = _DEVICES.get(index)
+    if d is None:
+        d = _DEVICES[index] = torch.device("cuda", index)
+    return d
+
+
+def _elsewhere(t, name: str, stream) -> bool:
+    """Whether the call has to move to another device or stream first."""
+    try:
+        index = t.device.index
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
+    if index is None:
+        raise ValueError(f"{name} must be on a CUDA device, is on {t.device}")
+    return stream is not None or index != _current_device()
+
+
+@contextlib.contextmanager
+def _on(device, stream, *inputs):
+    """Make device and stream current. The inputs are marked as used on the
+    stream, so memory that is freed meanwhile is not handed out under it."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        for t in inputs:
+            for part in ((t._buf, t._scales) if isinstance(t, Mx4Tensor) else (t,)):
+                if isinstance(part, torch.Tensor) and part.is_cuda:
+                    part.record_stream(stream)
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _rows(t, name: str, dtype, index: int) -> int:
+    """Check a 2-D row-major CUDA matrix of `dtype` (None: any) whose rows may be
+    strided; returns the row stride in elements."""
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_cuda or t.device.index != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, is on {t.device}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
     rows, cols = t.shape
     ld, inner = t.stride()
-    if rows <= 1:   # a stride of one row (or none) says nothing
-        ld = max(cols, (cols + 7) // 8 * 8 if rows else cols)
-    if (inner != 1 and cols > 1) or ld < cols:
+    if rows <= 1:   # the stride of a single row says nothing
+        ld = (cols + 7) // 8 * 8
+    if ld < cols or (inner != 1 and cols > 1):
         raise ValueError(f"{name} must have contiguous rows (strides {tuple(t.stride())})")
     return ld
-
-
-def _half_rows(t, name: str, dtype=None, device=None) -> int:
-    if isinstance(t, torch.Tensor) and t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    return _rows(t, name, dtype, device)
 
 
 def _act_code(act: str) -> int:
@@ -345,36 +387,9 @@ def _act_code(act: str) -> int:
         raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}") from None
 
 
-class _On:
-    """The call's device and stream: current while the call's buffers are
-    allocated (so the allocator hands them out in that stream's order) and its
-    kernels launched."""
-
-    __slots__ = ("dev", "stream", "handle", "_ctx")
-
-    def __init__(self, device, stream):
-        cur = torch.cuda.current_device()
-        self._ctx = []
-        if device.index is not None and device.index != cur:
-            self._ctx.append(torch.cuda.device(device))
-        if stream is not None:
-            self._ctx.append(torch.cuda.stream(stream))
-        self.dev, self.stream = device, stream
-
-    def __enter__(self):
-        for c in self._ctx:
-            c.__enter__()
-        self.handle = torch.cuda.current_stream().cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        for c in reversed(self._ctx):
-            c.__exit__(*exc)
-
-
-def _work(op: int, M: int, N: int, K: int, device):
-    """A workspace for this call, or None when it needs none."""
-    key = (device.index, op, M, N, K)
+def _work(op: int, M: int, N: int, K: int, index: int):
+    """(tensor or None, pointer, bytes) of this call's workspace."""
+    key = (index, op, M, N, K)
     n = _FFN_WORK.get(key)
     if n is None:
         b = ctypes.c_size_t()
@@ -382,58 +397,93 @@ def _work(op: int, M: int, N: int, K: int, device):
         if len(_FFN_WORK) > 4096:
             _FFN_WORK.clear()
         n = _FFN_WORK[key] = int(b.value)
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    if not n:
+        return None, None, 0
+    t = torch.empty(n, dtype=torch.uint8, device=_device(index))
+    return t, t.data_ptr(), n
 
 
-def _out(t, name: str, shape, dtype, device, contiguous=False):
+def _out(t, name: str, rows: int, cols: int, dtype, index: int):
     """The caller's output, checked, or a new one; returns (tensor, row stride)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device), shape[1]
-    ld = _rows(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+        return torch.empty((rows, cols), dtype=dtype, device=_device(index)), cols
+    ld = _rows(t, name, dtype, index)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
     return t, ld
 
 
 class Mx4Tensor:
     """A matrix ``[rows, cols]`` held in microscaled 4-bit floating point: 4-bit
     codes and one power-of-two scale per 32 columns (4.25 bits an element), in
-    the layout that ``include/kdaproj.h`` describes. Made by ``mx4_quantize``."""
+    the layout that ``include/kdaproj.h`` describes. Made by ``mx4_quantize``, or
+    from stored ``codes`` and ``scales`` (uint8, of the sizes that
+    ``Mx4Tensor.sizes`` gives, 16-byte aligned)."""
 
-    __slots__ = ("codes", "scales", "shape")
+    __slots__ = ("_buf", "_scales", "_code_bytes", "_scale_bytes", "shape", "device", "code_ptr", "scale_ptr")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
-        nb = (cols + 31) // 32
+        nc, ns = self.sizes(rows, cols)
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("codes and scales must be uint8")
-        if rows < 0 or cols < 1 or not codes.is_contiguous() or not scales.is_contiguous() \
-                or codes.numel() != rows * nb * 16 \
-                or scales.numel() != (rows + 127) // 128 * ((nb + 3) // 4) * 512 \
-                or codes.device != scales.device:
-            raise ValueError(f"codes and scales do not hold a {rows} x {cols} matrix")
-        self.codes, self.scales, self.shape = codes, scales, (rows, cols)
+        if codes.numel() != nc or scales.numel() != ns or not codes.is_contiguous() \
+                or not scales.is_contiguous() or codes.device != scales.device:
+            raise ValueError(f"codes and scales do not hold a {rows} x {cols} matrix "
+                             f"({nc} and {ns} contiguous bytes on one device)")
+        self._set(codes, scales, nc, ns, rows, cols, codes.data_ptr(), scales.data_ptr())
+
+    def _set(self, buf, scales, nc, ns, rows, cols, code_ptr, scale_ptr):
+        self._buf, self._scales, self._code_bytes, self._scale_bytes = buf, scales, nc, ns
+        self.shape, self.device = (rows, cols), buf.device
+        self.code_ptr, self.scale_ptr = code_ptr, scale_ptr
+
+    @classmethod
+    def _new(cls, rows: int, cols: int, device) -> "Mx4Tensor":
+        """Uninitialised: both parts in one allocation."""
+        nb = (cols + 31) >> 5
+        nc = rows * nb * 16
+        ns = ((rows + 127) >> 7) * ((nb + 3) >> 2) * 512
+        off = (nc + 255) & ~255
+        buf = torch.empty(off + ns, dtype=torch.uint8, device=device)
+        q = cls.__new__(cls)
+        ptr = buf.data_ptr()
+        q._set(buf, None, nc, ns, rows, cols, ptr, ptr + off)
+        return q
+
+    @staticmethod
+    def sizes(rows: int, cols: int):
+        """Bytes of the codes and of the scales of a rows x cols matrix."""
+        a, b = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(load().kp_mx4_bytes(rows, cols, ctypes.byref(a), ctypes.byref(b)))
+        return int(a.value), int(b.value)
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self) -> torch.Tensor:
+        """[rows, ceil(cols / 32) * 16] bytes, two codes each."""
+        rows, cols = self.shape
+        return self._buf.view(-1)[:self._code_bytes].view(rows, (cols + 31) // 32 * 16)
+
+    @property
+    def scales(self) -> torch.Tensor:
+        """The scale bytes, in tiles of 512."""
+        if self._scales is not None:
+            return self._scales
+        off = self.scale_ptr - self.code_ptr
+        return self._buf[off:off + self._scale_bytes]
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        return self._code_bytes + self._scale_bytes
 
     def __repr__(self):
         return f"Mx4Tensor({self.shape[0]} x {self.shape[1]}, {self.device})"
 
 
-def _mx4(q, name: str, device=None) -> Mx4Tensor:
+def _mx4(q, name: str, index: int) -> Mx4Tensor:
     if not isinstance(q, Mx4Tensor):
         raise TypeError(f"{name} must be an Mx4Tensor (mx4_quantize), got {type(q).__name__}")
-    if not q.codes.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if device is not None and q.device != device:
-        raise ValueError(f"{name} is on {q.device}, expected {device}")
+    if q.device.type != "cuda" or q.device.index != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, is on {q.device}")
     return q
 
 
@@ -442,46 +492,59 @@ def mx4_quantize(x: torch.Tensor, stream=None) -> Mx4Tensor:
     may be strided) to microscaled 4 bits: per 32 columns the scale
     ``2^(floor(log2 max|x|) - 2)``, elements to the nearest of 0, .5, 1, 1.5, 2,
     3, 4, 6 scales, ties to even. A block with a NaN or an infinity becomes NaN."""
-    ld = _rows(x, "x")
+    if _elsewhere(x, "x", stream):
+        with _on(x.device, stream, x):
+            return mx4_quantize(x)
+    index = x.device.index
+    ld = _rows(x, "x", None, index)
     dt = _FFN_DTYPES.get(x.dtype)
     if dt is None:
         raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
     rows, cols = x.shape
-    nb = (cols + 31) // 32
-    with _On(x.device, stream) as on:
-        codes = torch.empty((rows, nb * 16), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((rows + 127) // 128 * ((nb + 3) // 4) * 512, dtype=torch.uint8, device=x.device)
-        _check(load().kp_mx4_quantize(x.data_ptr(), ld, rows, cols, dt, codes.data_ptr(), scales.data_ptr(),
-                                      on.handle))
-    return Mx4Tensor(codes, scales, rows, cols)
+    q = Mx4Tensor._new(rows, cols, x.device)
+    rc = load().kp_mx4_quantize(x.data_ptr(), ld, rows, cols, dt, q.code_ptr, q.scale_ptr, _raw_stream(index))
+    if rc:
+        _check(rc)
+    return q
 
 
 def mx4_dequantize(q: Mx4Tensor, dtype=torch.bfloat16, y: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
-    """The values that ``q`` stands for: exact in bfloat16 and float32."""
-    _mx4(q, "q")
-    if dtype not in _FFN_DTYPES:
+    """The values that ``q`` stands for: exact in bfloat16 and float32 (float16
+    rounds, and overflows to infinity)."""
+    if _elsewhere(q, "q", stream):
+        with _on(q.device, stream, q, y):
+            return mx4_dequantize(q, dtype, y)
+    index = q.device.index
+    _mx4(q, "q", index)
+    dt = _FFN_DTYPES.get(dtype)
+    if dt is None:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    with _On(q.device, stream) as on:
-        y, ld = _out(y, "y", q.shape, dtype, q.device)
-        _check(load().kp_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.shape[0], q.shape[1],
-                                        y.data_ptr(), ld, _FFN_DTYPES[dtype], on.handle))
+    rows, cols = q.shape
+    y, ld = _out(y, "y", rows, cols, dtype, index)
+    rc = load().kp_mx4_dequantize(q.code_ptr, q.scale_ptr, rows, cols, y.data_ptr(), ld, dt, _raw_stream(index))
+    if rc:
+        _check(rc)
     return y
 
 
-def _mx4_x(x, dtype):
-    """(rows, cols, device, element type, x arguments) of a 4-bit product's
-    left side: a 16-bit matrix, quantised within the call, or an Mx4Tensor."""
+def _mx4_left(x, dtype, index: int):
+    """(rows, cols, element type, x's arguments) of a 4-bit product's left side: a
+    16-bit matrix, quantised within the call, or an Mx4Tensor."""
     if isinstance(x, Mx4Tensor):
-        _mx4(x, "x")
         dt = torch.bfloat16 if dtype is None else dtype
         if dt not in _DTYPES:
             raise TypeError(f"dtype must be bfloat16 or float16, got {dt}")
-        return x.shape[0], x.shape[1], x.device, dt, (None, 0, x.codes.data_ptr(), x.scales.data_ptr())
-    ld = _half_rows(x, "x")
-    if dtype is not None and dtype is not x.dtype:
-        raise TypeError(f"the output has x's type {x.dtype}")
-    return x.shape[0], x.shape[1], x.device, x.dtype, (x.data_ptr(), ld, None, None)
+        rows, cols = _mx4(x, "x", index).shape
+        return rows, cols, dt, (None, 0, x.code_ptr, x.scale_ptr)
+    ld = _rows(x, "x", None, index)
+    dt = x.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"x must be bfloat16, float16 or an Mx4Tensor, got {dt}")
+    if dtype is not None and dtype is not dt:
+        raise TypeError(f"the output has x's type {dt}")
+    rows, cols = x.shape
+    return rows, cols, dt, (x.data_ptr(), ld, None, None)
 
 
 def mx4_gemm(x, W: Mx4Tensor, y: torch.Tensor | None = None, dtype=None, stream=None) -> torch.Tensor:
@@ -489,21 +552,21 @@ def mx4_gemm(x, W: Mx4Tensor, y: torch.Tensor | None = None, dtype=None, stream=
     [M, K] is bfloat16 or float16 (quantised within the call; y has its type) or
     an ``Mx4Tensor`` (y has ``dtype``, bfloat16 unless given). ``W`` [N, K]. Any
     sizes; with ``x`` empty nothing runs."""
-    M, K, dev, dt, xargs = _mx4_x(x, dtype)
-    _mx4(W, "W", dev)
-    N = W.shape[0]
-    if W.shape[1] != K:
-        raise ValueError(f"W has K={W.shape[1]}, x has K={K}")
-    with _On(dev, stream) as on:
-        y, ld = _out(y, "y", (M, N), dt, dev)
-        work = _work(FFN_MX4_GEMM, M, N, K, dev)
-        _check(load().kp_mx4_gemm(*xargs, W.codes.data_ptr(), W.scales.data_ptr(), y.data_ptr(), ld, M, N, K,
-                                  _DTYPES[dt], *_work_args(work), on.handle))
+    if _elsewhere(x, "x", stream):
+        with _on(x.device, stream, x, W, y):
+            return mx4_gemm(x, W, y, dtype)
+    index = x.device.index
+    M, K, dt, xargs = _mx4_left(x, dtype, index)
+    N, Kw = _mx4(W, "W", index).shape
+    if Kw != K:
+        raise ValueError(f"W has K={Kw}, x has K={K}")
+    y, ld = _out(y, "y", M, N, dt, index)
+    work, wp, wn = _work(FFN_MX4_GEMM, M, N, K, index)
+    rc = load().kp_mx4_gemm(*xargs, W.code_ptr, W.scale_ptr, y.data_ptr(), ld, M, N, K, _DTYPES[dt], wp, wn,
+                            _raw_stream(index))
+    if rc:
+        _check(rc)
     return y
-
-
-def _work_args(work):
-    return (None, 0) if work is None else (work.data_ptr(), work.numel())
 
 
 def mx4_gated_ffn(x, Wg: Mx4Tensor, Wu: Mx4Tensor, act: str = "silu", h: torch.Tensor | None = None,
@@ -511,31 +574,37 @@ def mx4_gated_ffn(x, Wg: Mx4Tensor, Wu: Mx4Tensor, act: str = "silu", h: torch.T
     """``h = round(act(Q(x) @ Q(Wg).T) * (Q(x) @ Q(Wu).T))``: the gated block over
     4-bit weights [F, K] and activations, in one product kernel. ``x`` as for
     ``mx4_gemm``; ``act`` as for ``gated_ffn``."""
+    if _elsewhere(x, "x", stream):
+        with _on(x.device, stream, x, Wg, Wu, h):
+            return mx4_gated_ffn(x, Wg, Wu, act, h, dtype)
+    index = x.device.index
     code = _act_code(act)
-    T, K, dev, dt, xargs = _mx4_x(x, dtype)
-    _mx4(Wg, "Wg", dev)
-    _mx4(Wu, "Wu", dev)
-    F = Wg.shape[0]
-    if Wg.shape != Wu.shape or Wg.shape[1] != K:
+    T, K, dt, xargs = _mx4_left(x, dtype, index)
+    shape = _mx4(Wg, "Wg", index).shape
+    if _mx4(Wu, "Wu", index).shape != shape or shape[1] != K:
         raise ValueError(f"Wg {Wg.shape} and Wu {Wu.shape} must both be [F, {K}]")
-    with _On(dev, stream) as on:
-        h, ld = _out(h, "h", (T, F), dt, dev)
-        work = _work(FFN_MX4_GATED, T, F, K, dev)
-        _check(load().kp_mx4_gated_ffn(*xargs, Wg.codes.data_ptr(), Wg.scales.data_ptr(), Wu.codes.data_ptr(),
-                                       Wu.scales.data_ptr(), h.data_ptr(), ld, T, F, K, code, _DTYPES[dt],
-                                       *_work_args(work), on.handle))
+    F = shape[0]
+    h, ld = _out(h, "h", T, F, dt, index)
+    work, wp, wn = _work(FFN_MX4_GATED, T, F, K, index)
+    rc = load().kp_mx4_gated_ffn(*xargs, Wg.code_ptr, Wg.scale_ptr, Wu.code_ptr, Wu.scale_ptr, h.data_ptr(), ld,
+                                 T, F, K, code, _DTYPES[dt], wp, wn, _raw_stream(index))
+    if rc:
+        _check(rc)
     return h
 
 
-def _gated_operands(x, Wg, Wu):
-    ldx = _half_rows(x, "x")
-    ldg = _rows(Wg, "Wg", x.dtype, x.device)
-    ldu = _rows(Wu, "Wu", x.dtype, x.device)
+def _gated_operands(x, Wg, Wu, index: int):
+    dt = x.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"x must be bfloat16 or float16, got {dt}")
+    ldx = _rows(x, "x", None, index)
+    ldg = _rows(Wg, "Wg", dt, index)
+    ldu = _rows(Wu, "Wu", dt, index)
     T, K = x.shape
-    F = Wg.shape[0]
-    if Wg.shape != Wu.shape or Wg.shape[1] != K:
+    shape = Wg.shape
+    if shape != Wu.shape or shape[1] != K:
         raise ValueError(f"Wg {tuple(Wg.shape)} and Wu {tuple(Wu.shape)} must both be [F, {K}]")
-    return T, F, K, ldx, ldg, ldu
+    return T, shape[0], K, ldx, ldg, ldu, dt
 
 
 def gated_ffn(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu",
@@ -546,19 +615,22 @@ def gated_ffn(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "s
     may be strided (strides and K multiples of 8, 16-byte aligned). ``act``:
     "silu", "gelu" (erf) or "gelu_tanh". With ``save`` returns ``(h, g, u)``, the
     two products rounded to x's type, for ``gated_ffn_backward``."""
+    if _elsewhere(x, "x", stream):
+        with _on(x.device, stream, x, Wg, Wu, h):
+            return gated_ffn(x, Wg, Wu, act, h, save)
+    index = x.device.index
     code = _act_code(act)
-    T, F, K, ldx, ldg, ldu = _gated_operands(x, Wg, Wu)
-    dev = x.device
-    with _On(dev, stream) as on:
-        h, ldh = _out(h, "h", (T, F), x.dtype, dev)
-        g = u = None
-        if save:
-            g = torch.empty((T, F), dtype=x.dtype, device=dev)
-            u = torch.empty((T, F), dtype=x.dtype, device=dev)
-        work = _work(FFN_GATED, T, F, K, dev)
-        _check(load().kp_gated_ffn(x.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu, h.data_ptr(), ldh,
-                                   g.data_ptr() if save else None, u.data_ptr() if save else None, T, F, K, code,
-                                   _DTYPES[x.dtype], *_work_args(work), on.handle))
+    T, F, K, ldx, ldg, ldu, dt = _gated_operands(x, Wg, Wu, index)
+    h, ldh = _out(h, "h", T, F, dt, index)
+    g = u = gp = up = None
+    if save:
+        g, u = x.new_empty((T, F)), x.new_empty((T, F))
+        gp, up = g.data_ptr(), u.data_ptr()
+    work, wp, wn = _work(FFN_GATED, T, F, K, index)
+    rc = load().kp_gated_ffn(x.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu, h.data_ptr(), ldh, gp, up,
+                             T, F, K, code, _DTYPES[dt], wp, wn, _raw_stream(index))
+    if rc:
+        _check(rc)
     return (h, g, u) if save else h
 
 
@@ -569,26 +641,27 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu: 
     and ``dU = dh act(g)`` are computed in fp32 and rounded to x's type as the
     tensor cores' operands; the three products are summed in fp32. With no tokens
     the weights' gradients are zero."""
+    if _elsewhere(x, "x", stream):
+        with _on(x.device, stream, dh, x, Wg, Wu, g, u):
+            return gated_ffn_backward(dh, x, Wg, Wu, g, u, act)
+    index = x.device.index
     code = _act_code(act)
-    T, F, K, ldx, ldg, ldu = _gated_operands(x, Wg, Wu)
-    dev = x.device
-    lddh = _rows(dh, "dh", x.dtype, dev)
+    T, F, K, ldx, ldg, ldu, dt = _gated_operands(x, Wg, Wu, index)
+    lddh = _rows(dh, "dh", dt, index)
     for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
         if t is not dh:
-            _rows(t, name, x.dtype, dev)
+            _rows(t, name, dt, index)
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-        if tuple(t.shape) != (T, F):
+        if t.shape != (T, F):
             raise ValueError(f"{name} must be {(T, F)}, got {tuple(t.shape)}")
-    with _On(dev, stream) as on:
-        dx = torch.empty((T, K), dtype=x.dtype, device=dev)
-        dWg = torch.empty((F, K), dtype=x.dtype, device=dev)
-        dWu = torch.empty((F, K), dtype=x.dtype, device=dev)
-        work = _work(FFN_GATED_BACKWARD, T, F, K, dev)
-        _check(load().kp_gated_ffn_backward(dh.data_ptr(), lddh, x.data_ptr(), ldx, Wg.data_ptr(), ldg,
-                                            Wu.data_ptr(), ldu, g.data_ptr(), u.data_ptr(), dx.data_ptr(),
-                                            dWg.data_ptr(), dWu.data_ptr(), T, F, K, code, _DTYPES[x.dtype],
-                                            *_work_args(work), on.handle))
+    dx, dWg, dWu = x.new_empty((T, K)), x.new_empty((F, K)), x.new_empty((F, K))
+    work, wp, wn = _work(FFN_GATED_BACKWARD, T, F, K, index)
+    rc = load().kp_gated_ffn_backward(dh.data_ptr(), lddh, x.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(),
+                                      ldu, g.data_ptr(), u.data_ptr(), dx.data_ptr(), dWg.data_ptr(),
+                                      dWu.data_ptr(), T, F, K, code, _DTYPES[dt], wp, wn, _raw_stream(index))
+    if rc:
+        _check(rc)
     return dx, dWg, dWu
 
 

@@ -106,6 +106,14 @@ static int check_mx4(const char *fn, const char *name, const void *codes, const 
         return set_error(KP_EALIGN, "%s: %s's codes and scales must be 16-byte aligned", fn, name);
     return KP_OK;
 }
+// The 4-bit kernels count segments of 256 columns in 32 bits (that many hold
+// half a terabyte of codes).
+static int check_mx4_size(const char *fn, int64_t rows, int64_t cols) {
+    if ((rows + 127) * ((cols + 255) / 256) >= (1ll << 32) || cols > (1 << 30))
+        return set_error(KP_ESHAPE, "%s: %lld x %lld is too large", fn, static_cast<long long>(rows),
+                         static_cast<long long>(cols));
+    return KP_OK;
+}
 static int check_output(const char *fn, const char *name, const void *p, int64_t ld, int cols) {
     if (!p) return set_error(KP_EINVAL, "%s: %s is NULL", fn, name);
     if (misaligned(p, 2)) return set_error(KP_EALIGN, "%s: %s must be 2-byte aligned", fn, name);
@@ -192,7 +200,8 @@ static int mx4_product(const char *fn, FfnArgs a, const void *x, int64_t ldx, co
     if (a.M < 0 || a.N < 1 || a.K < 1) return bad_sizes(fn, a.M, a.N, a.K);
     if (!is16(a.dtype)) return set_error(KP_EINVAL, "%s: unknown element type %d", fn, a.dtype);
     if (a.M == 0) return KP_OK;
-    int rc;
+    int rc = check_mx4_size(fn, a.M, a.K);
+    if (rc) return rc;
     if ((x != nullptr) == (x_codes != nullptr))
         return set_error(KP_EINVAL, "%s: give x or its codes and scales, not both", fn);
     if (x) {
@@ -254,8 +263,8 @@ int kp_mx4_quantize(const void *x, int64_t ldx, int rows, int cols, int dtype, v
         return set_error(KP_EALIGN, "%s: x must be aligned to its element size", fn);
     if (ldx < cols) return set_error(KP_EINVAL, "%s: x's row stride %lld is below its %d columns", fn,
                                      static_cast<long long>(ldx), cols);
-    int rc = check_mx4(fn, "the output", codes, scales);
-    if (rc) return rc;
+    int rc = check_mx4_size(fn, rows, cols);
+    if (rc || (rc = check_mx4(fn, "the output", codes, scales))) return rc;
     FfnDev d;
     if ((rc = ffn_device(&d))) return rc;
     cudaError_t e = mx4_quantize_launch(x, ldx, rows, cols, dtype, static_cast<uint8_t *>(codes),
@@ -269,8 +278,8 @@ int kp_mx4_dequantize(const void *codes, const void *scales, int rows, int cols,
     if (rows < 0 || cols < 1) return set_error(KP_EINVAL, "%s: bad sizes: %d rows, %d columns", fn, rows, cols);
     if (!is16(dtype) && dtype != KP_FP32) return set_error(KP_EINVAL, "%s: unknown element type %d", fn, dtype);
     if (rows == 0) return KP_OK;
-    int rc = check_mx4(fn, "the input", codes, scales);
-    if (rc) return rc;
+    int rc = check_mx4_size(fn, rows, cols);
+    if (rc || (rc = check_mx4(fn, "the input", codes, scales))) return rc;
     if (!y) return set_error(KP_EINVAL, "%s: y is NULL", fn);
     if (misaligned(y, dtype == KP_FP32 ? 4 : 2))
         return set_error(KP_EALIGN, "%s: y must be aligned to its element size", fn);

@@ -3,14 +3,14 @@
 //     h[m, n] = round( act(sum_k x[m, k] Wg[n, k]) * sum_k x[m, k] Wu[n, k] )   (gated)
 // over bf16 / fp16 operands or over microscaled 4-bit ones.
 //
-// The MMA's 128 rows are output features, its columns the tokens (16 .. 128 a
+// The MMA's 128 rows are rows of the weights, its columns the tokens (16 .. 128 a
 // tile, further tiles along the grid's y axis read the weights from L2). The
-// gated form keeps two accumulators, gate and up, over the same token operand,
-// so a thread of the epilogue holds both factors of its outputs. A feature
-// tile's K range is split over the C CTAs of a cluster; their fp32 partial
-// tiles go through L2 and the cluster sums them in rank order, so the result
-// does not depend on timing. A K block is 128 bytes of a row (64 16-bit or 256
-// 4-bit columns), one 16 KB TMA box per weight; a 4-bit stage also brings its
+// 16-bit gated form has 64 rows of Wg and the same 64 of Wu in one MMA, the 4-bit
+// one 128 of each in two accumulators. A feature tile's K range is split over the
+// C CTAs of a cluster; their fp32 partial tiles go through L2 and the cluster sums
+// them in rank order, so the result does not depend on timing; the sums of a gate
+// and of its factor meet in one thread there. A K block is 128 bytes of a row (64 16-bit or 256
+// 4-bit columns), 8 or 16 KB TMA boxes; a 4-bit stage also brings its
 // scale tiles, which tcgen05.cp lays into the stage's own TMEM columns (their
 // last readers finished before the stage was refilled).
 //
@@ -26,12 +26,15 @@ namespace kp {
 namespace {
 
 constexpr int kThreads = 192;
-constexpr int kRows = 128;                 // features per tile
-constexpr uint32_t kWBox = kRows * 128;    // one K block of one weight
+constexpr int kRows = 128;                 // rows of an MMA
 constexpr int kMaxTok = 128;               // tokens per tile
 constexpr int kMaxStages = 10;
 constexpr size_t kBarBytes = 256;
 constexpr size_t kMaxSmem = 227 * 1024;
+// What a CTA takes for its stages: half an SM, so that clusters of eight fill the
+// GPU. With all of an SM's shared memory each, 15 such clusters fit where two to
+// an SM makes 36 (T = 1, F = 2048, K = 7168: 16.1 us against 13.8).
+constexpr size_t kSmem = 113 * 1024;
 
 struct StreamParams {
     const uint8_t *sa, *sb, *sx;   // 4-bit: scale tiles
@@ -44,24 +47,27 @@ struct StreamParams {
     uint32_t idesc, tmem_cols, stage_bytes, sf_col;
 };
 
-// TMEM columns of one stage's scales: 8 for each operand.
-constexpr uint32_t sf_cols_of(bool mx4, bool gated) { return mx4 ? (gated ? 24 : 16) : 0; }
-
+// What a CTA holds of the weights: 128 rows of W (plain); 64 rows of Wg and the
+// same 64 of Wu in one MMA (16-bit gated); 128 and 128 with an accumulator each
+// (4-bit gated: a scale tile is 128 rows of one matrix).
 template <bool kMx4, bool kGated>
-struct StageLayout {
-    static constexpr uint32_t off_x = kGated ? 2 * kWBox : kWBox;
-    static __host__ __device__ uint32_t off_sc(int Mpad) { return off_x + static_cast<uint32_t>(Mpad) * 128; }
-    static __host__ __device__ uint32_t bytes(int Mpad) {
-        return off_sc(Mpad) + (kMx4 ? (kGated ? 3u : 2u) * 1024u : 0u);
-    }
+struct Shape {
+    static constexpr int acc = kMx4 && kGated ? 2 : 1;            // accumulators
+    static constexpr int feat = kGated && !kMx4 ? 64 : 128;       // features per tile
+    static constexpr uint32_t w_bytes = acc * kRows * 128;        // a K block of the weights
+    static constexpr uint32_t sc_bytes = kMx4 ? (acc + 1) * 1024 : 0;
+    static constexpr uint32_t sf_cols = kMx4 ? 8 * (acc + 1) : 0; // TMEM columns of a stage's scales
+    static __host__ __device__ uint32_t off_sc(int Mpad) { return w_bytes + static_cast<uint32_t>(Mpad) * 128; }
+    static __host__ __device__ uint32_t stage_bytes(int Mpad) { return off_sc(Mpad) + sc_bytes; }
 };
 
 template <bool kMx4, bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_stream_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                       const __grid_constant__ CUtensorMap tmx, const StreamParams p) {
-    using L = StageLayout<kMx4, kGated>;
-    constexpr int kAcc = kGated ? 2 : 1;
+    using L = Shape<kMx4, kGated>;
+    constexpr int kAcc = L::acc;
+    constexpr int kPart = kAcc * kRows;   // fp32 sums per token of a partial tile
     extern __shared__ uint8_t fs_smem_raw[];
     const uint32_t raw = smem_u32(fs_smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -94,24 +100,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kb = kb0 + s;
         const uint32_t st = base + stage * p.stage_bytes;
         const uint32_t bar = smem_u32(full + stage);
-        uint32_t bytes = kAcc * kWBox + xbytes;
         const uint32_t scb = kMx4 ? 512u * static_cast<uint32_t>(sc_tiles(kb)) : 0u;
-        bytes += scb * (kAcc + 1);
-        mbar_expect_tx(bar, bytes);
-        tma_load_2d(st, &tma, bar, kb * kCols, tile * kRows, pol);
-        if constexpr (kGated) tma_load_2d(st + kWBox, &tmb, bar, kb * kCols, tile * kRows, pol);
+        mbar_expect_tx(bar, L::w_bytes + xbytes + scb * (kAcc + 1));
+        tma_load_2d(st, &tma, bar, kb * kCols, tile * L::feat, pol);
+        if constexpr (kGated) tma_load_2d(st + L::w_bytes / 2, &tmb, bar, kb * kCols, tile * L::feat, pol);
         if constexpr (kMx4) {
             const size_t off = (static_cast<size_t>(tile) * p.kt_n + 2 * kb) * 512;
             const uint32_t sc = st + L::off_sc(p.Mpad);
             bulk_load(sc, p.sa + off, scb, bar);
-            if constexpr (kGated) bulk_load(sc + 1024, p.sb + off, scb, bar);
+            if constexpr (kAcc == 2) bulk_load(sc + 1024, p.sb + off, scb, bar);
         }
     };
     auto issue_x = [&](int s, int stage) {
         const int kb = kb0 + s;
         const uint32_t st = base + stage * p.stage_bytes;
         const uint32_t bar = smem_u32(full + stage);
-        tma_load_2d(st + L::off_x, &tmx, bar, kb * kCols, m0, policy_evict_last());
+        tma_load_2d(st + L::w_bytes, &tmx, bar, kb * kCols, m0, policy_evict_last());
         if constexpr (kMx4) {
             const size_t off = (static_cast<size_t>(m0 >> 7) * p.kt_n + 2 * kb) * 512;
             bulk_load(st + L::off_sc(p.Mpad) + kAcc * 1024, p.sx + off,
@@ -163,10 +167,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t st = base + stage * p.stage_bytes;
                 const uint64_t ad = desc_kmajor(st);
-                const uint64_t bd = desc_kmajor(st + L::off_x);
+                const uint64_t bd = desc_kmajor(st + L::w_bytes);
                 if constexpr (kMx4) {
                     const int kb = kb0 + s;
-                    const uint32_t sf = tmem + p.sf_col + static_cast<uint32_t>(stage) * sf_cols_of(kMx4, kGated);
+                    const uint32_t sf = tmem + p.sf_col + static_cast<uint32_t>(stage) * L::sf_cols;
                     const uint32_t sc = st + L::off_sc(p.Mpad);
                     for (int j = 0; j < sc_tiles(kb); ++j)
 #pragma unroll
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t sfk = sf + 4 * (kk >> 1);
 #pragma unroll
                         for (int a = 0; a < kAcc; ++a)
-                            umma_mxf4(tmem + a * p.Mpad, ad + (a * kWBox >> 4) + 2 * kk, bd + 2 * kk, id,
+                            umma_mxf4(tmem + a * p.Mpad, ad + (a * kRows * 128 >> 4) + 2 * kk, bd + 2 * kk, id,
                                       sfk + 8 * a, sfk + 8 * kAcc, (s > 0 || kk > 0) ? 1u : 0u);
                     }
                 } else {
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int a = 0; a < kAcc; ++a)
-                            umma_bf16(tmem + a * p.Mpad, ad + (a * kWBox >> 4) + 2 * kk, bd + 2 * kk, p.idesc,
+                            umma_bf16(tmem + a * p.Mpad, ad + (a * kRows * 128 >> 4) + 2 * kk, bd + 2 * kk, p.idesc,
                                       (s > 0 || kk > 0) ? 1u : 0u);
                 }
                 umma_commit(smem_u32(empty + stage));
@@ -196,63 +200,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
+        // accumulators -> this CTA's partial tile [token][kPart], 128 bytes a warp
+        // and token: in L2, or with one CTA in the stage memory, which is free
+        // once the last MMA has completed
         const int q = warp & 3;
         const int row = q * 32 + lane;
-        const int n = tile * kRows + row;
         mbar_wait_bounded(smem_u32(accf), 0, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
         tc_fence_after();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        float *part = p.ws + ((static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C + rank) *
-                                 static_cast<size_t>(kAcc * kRows) * p.Mpad;
-        for (int c0 = 0; c0 < p.Mpad; c0 += 16) {
-            uint32_t va[16], vb[16];
-            tmem_ld16(taddr + c0, va);
-            if constexpr (kGated) tmem_ld16(taddr + p.Mpad + c0, vb);
+        float *part = C > 1 ? p.ws + ((static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C + rank) *
+                                         static_cast<size_t>(kPart) * p.Mpad
+                            : reinterpret_cast<float *>(gbase);
+        for (int c0 = 0; c0 < Mloc; c0 += 16) {
+            uint32_t v[kAcc][16];
+#pragma unroll
+            for (int a = 0; a < kAcc; ++a) tmem_ld16(taddr + a * p.Mpad + c0, v[a]);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int m = c0 + i;
-                if (m >= Mloc) continue;
-                const float a = __uint_as_float(va[i]);
-                if (C > 1) {
-                    part[m * kRows + row] = a;
-                    if constexpr (kGated) part[(p.Mpad + m) * kRows + row] = __uint_as_float(vb[i]);
-                } else if (n < p.N) {
-                    const int64_t om = m0 + m;
-                    if constexpr (kGated) {
-                        const float b = __uint_as_float(vb[i]);
-                        p.y[om * p.ldy + n] = elem_round(ffn_act(a, p.act) * b, p.dtype);
-                        if (p.g) {
-                            p.g[om * p.N + n] = elem_round(a, p.dtype);
-                            p.u[om * p.N + n] = elem_round(b, p.dtype);
-                        }
-                    } else {
-                        p.y[om * p.ldy + n] = elem_round(a, p.dtype);
-                    }
-                }
-            }
+            for (int i = 0; i < 16; ++i)
+                if (c0 + i < Mloc)
+#pragma unroll
+                    for (int a = 0; a < kAcc; ++a)
+                        part[(c0 + i) * kPart + a * kRows + row] = __uint_as_float(v[a][i]);
         }
         tc_fence_before();
     }
 
-    if (C > 1) {
-        __syncwarp();
-        cluster_sync_all();   // every partial tile of the cluster is written and visible
-        const size_t stride = static_cast<size_t>(kAcc * kRows) * p.Mpad;
-        const float *parts = p.ws + (static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C * stride;
-        // a warp takes a token, a lane four of its features
-        const int n = tile * kRows + 4 * lane;
-        for (int m = warp * C + rank; m < Mloc; m += (kThreads / 32) * C) {
+    // every partial tile of the cluster is written and visible after this
+    __syncwarp();
+    if (C > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    {
+        const size_t stride = static_cast<size_t>(kPart) * p.Mpad;
+        const float *parts = C > 1 ? p.ws + (static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C * stride
+                                   : reinterpret_cast<const float *>(gbase);
+        // a lane takes four features of a token; CTA r of the cluster every C-th
+        // group of tokens
+        constexpr int kLanes = L::feat / 4;              // lanes per token: 16 or 32
+        constexpr int kTok = kThreads / kLanes;          // tokens at a time
+        const int f = 4 * (threadIdx.x % kLanes);
+        const int n = tile * L::feat + f;
+        for (int m = rank * kTok + threadIdx.x / kLanes; m < Mloc; m += kTok * C) {
             float va[4] = {0.f, 0.f, 0.f, 0.f}, vb[4] = {0.f, 0.f, 0.f, 0.f};
-            const float *src = parts + static_cast<size_t>(m) * kRows + 4 * lane;
-            for (int r = 0; r < C; ++r) {
-                const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + r * stride));
-                va[0] += a.x, va[1] += a.y, va[2] += a.z, va[3] += a.w;
-                if constexpr (kGated) {
-                    const float4 b = __ldcg(reinterpret_cast<const float4 *>(
-                        src + r * stride + static_cast<size_t>(p.Mpad) * kRows));
-                    vb[0] += b.x, vb[1] += b.y, vb[2] += b.z, vb[3] += b.w;
-                }
+            const float *src = parts + static_cast<size_t>(m) * kPart + f;
+            auto add = [&](const float *at, float(&v)[4]) {
+                const float4 a = C > 1 ? __ldcg(reinterpret_cast<const float4 *>(at)) : *reinterpret_cast<const float4 *>(at);
+                v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            };
+#pragma unroll 4
+            for (int r = 0; r < C; ++r) {   // in rank order
+                add(src + r * stride, va);
+                if constexpr (kGated) add(src + r * stride + L::feat, vb);
             }
             const int64_t om = m0 + m;
             auto put = [&](uint16_t *dst, int64_t ld, const float(&v)[4]) {
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = ffn_act(va[i], p.act) * vb[i];
                 put(p.y, p.ldy, h);
-                if (p.g) {
+                if (!kMx4 && p.g) {
                     put(p.g, p.N, va);
                     put(p.u, p.N, vb);
                 }
@@ -291,30 +291,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 struct Plan {
     int Mpad, mt, tiles, KB, C, stages;
+    int acc, feat;
     uint32_t stage_bytes, sf_cols, tmem_cols;
 };
 
-uint32_t stage_bytes_of(bool mx4, bool gated, int Mpad) {
-    if (mx4) return gated ? StageLayout<true, true>::bytes(Mpad) : StageLayout<true, false>::bytes(Mpad);
-    return gated ? StageLayout<false, true>::bytes(Mpad) : StageLayout<false, false>::bytes(Mpad);
+template <bool kMx4, bool kGated>
+void shape_of(Plan &q) {
+    using L = Shape<kMx4, kGated>;
+    q.acc = L::acc;
+    q.feat = L::feat;
+    q.sf_cols = L::sf_cols;
+    q.stage_bytes = L::stage_bytes(q.Mpad);
 }
 
 Plan make_plan(bool mx4, bool gated, int M, int N, int K, int sms) {
     Plan q;
     q.Mpad = std::min((M + 15) / 16 * 16, kMaxTok);
+    if (mx4)
+        gated ? shape_of<true, true>(q) : shape_of<true, false>(q);
+    else
+        shape_of<false, true>(q);
     q.mt = (M + q.Mpad - 1) / q.Mpad;
-    q.tiles = (N + kRows - 1) / kRows;
+    q.tiles = (N + q.feat - 1) / q.feat;
     q.KB = mx4 ? (K + 255) / 256 : (K + 63) / 64;
-    // as many CTAs as there are SMs, while each keeps at least one K block
+    // Up to two CTAs per SM, while each keeps at least two K blocks. T = 1, F = 2048,
+    // K = 7168, 16-bit gated: C = 8 13.8 us, 4 15.1, 2 24; 77 x 4099 x 2050 in 4 bits
+    // (nine K blocks): C = 8 9.4 us, 4 8.0, 2 11.2.
     q.C = 1;
-    while (q.C < 8 && static_cast<int64_t>(q.tiles) * q.mt * q.C * 2 <= sms && q.C * 2 <= q.KB) q.C *= 2;
-    q.stage_bytes = stage_bytes_of(mx4, gated, q.Mpad);
-    q.sf_cols = sf_cols_of(mx4, gated);
-    const uint32_t acc = static_cast<uint32_t>(gated ? 2 : 1) * q.Mpad;
-    int st = static_cast<int>((kMaxSmem - 1024 - kBarBytes) / q.stage_bytes);
+    while (q.C < 8 && static_cast<int64_t>(q.tiles) * q.mt * q.C <= sms && q.C * 4 <= q.KB) q.C *= 2;
+    const uint32_t acc = static_cast<uint32_t>(q.acc) * q.Mpad;
+    int st = static_cast<int>((kSmem - 1024 - kBarBytes) / q.stage_bytes);
     st = std::min(st, kMaxStages);
     if (mx4) st = std::min(st, static_cast<int>((512 - acc) / q.sf_cols));
     st = std::min(st, (q.KB + q.C - 1) / q.C);
+    // one CTA: its partial tile needs the stage memory
+    if (q.C == 1)
+        st = std::max<int>(st, (static_cast<size_t>(q.acc) * kRows * 4 * q.Mpad + q.stage_bytes - 1) / q.stage_bytes);
     q.stages = st;
     q.tmem_cols = 32;
     while (q.tmem_cols < acc + q.sf_cols * st) q.tmem_cols <<= 1;
@@ -329,22 +341,23 @@ std::map<int, bool> g_ready;   // devices whose kernels have their shared memory
 size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms) {
     const Plan q = make_plan(mx4, gated, M, N, K, sms);
     if (q.C == 1) return 0;
-    return static_cast<size_t>(q.mt) * q.tiles * q.C * (gated ? 2 : 1) * kRows * q.Mpad * sizeof(float);
+    return static_cast<size_t>(q.mt) * q.tiles * q.C * q.acc * kRows * q.Mpad * sizeof(float);
 }
 
 cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s) {
     const Plan q = make_plan(a.mx4, a.gated, a.M, a.N, a.K, d.sms);
     if (q.C > 1 && !a.ws) return cudaErrorInvalidValue;
     using Fn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, StreamParams);
-    static const Fn kernels[2][2] = {{ffn_stream_kernel<false, false>, ffn_stream_kernel<false, true>},
-                                     {ffn_stream_kernel<true, false>, ffn_stream_kernel<true, true>}};
+    static const Fn kernels[] = {ffn_stream_kernel<false, true>, ffn_stream_kernel<true, false>,
+                                 ffn_stream_kernel<true, true>};   // 16-bit gated, 4-bit, 4-bit gated
+    if (!a.mx4 && !a.gated) return cudaErrorInvalidValue;          // skinny_gemm's work
     cudaError_t e = cudaSuccess;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!g_ready[d.dev]) {
-            for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-                e = cudaFuncSetAttribute(kernels[i >> 1][i & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kMaxSmem));
+            for (Fn f : kernels)
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
             if (e != cudaSuccess) return e;
             g_ready[d.dev] = true;
         }
@@ -375,7 +388,7 @@ cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s)
     p.idesc = a.mx4 ? idesc_mxf4(kRows, q.Mpad) : idesc_f16(a.dtype, kRows, q.Mpad);
     p.tmem_cols = q.tmem_cols;
     p.stage_bytes = q.stage_bytes;
-    p.sf_col = static_cast<uint32_t>((a.gated ? 2 : 1) * q.Mpad);
+    p.sf_col = static_cast<uint32_t>(q.acc * q.Mpad);
 
     CUtensorMap ma, mb, mx;
     if (a.mx4) {
@@ -384,8 +397,8 @@ cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s)
         if (e == cudaSuccess && a.gated) e = ffn_tensor_map(&mb, a.qb.codes, a.N, pitch, pitch, kRows, 128, kMapU8);
         if (e == cudaSuccess) e = ffn_tensor_map(&mx, a.qx.codes, a.M, pitch, pitch, q.Mpad, 128, kMapU8);
     } else {
-        e = ffn_tensor_map(&ma, a.Wa, a.N, a.K, a.lda, kRows, 64, a.dtype);
-        if (e == cudaSuccess && a.gated) e = ffn_tensor_map(&mb, a.Wb, a.N, a.K, a.ldb, kRows, 64, a.dtype);
+        e = ffn_tensor_map(&ma, a.Wa, a.N, a.K, a.lda, q.feat, 64, a.dtype);
+        if (e == cudaSuccess && a.gated) e = ffn_tensor_map(&mb, a.Wb, a.N, a.K, a.ldb, q.feat, 64, a.dtype);
         if (e == cudaSuccess) e = ffn_tensor_map(&mx, a.x, a.M, a.K, a.ldx, q.Mpad, 64, a.dtype);
     }
     if (e != cudaSuccess) return e;
@@ -408,7 +421,7 @@ cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernels[a.mx4][a.gated], ma, mb, mx, p);
+    return cudaLaunchKernelEx(&cfg, kernels[a.mx4 ? 1 + a.gated : 0], ma, mb, mx, p);
 }
 
 }  // namespace kp
