@@ -43,6 +43,10 @@ constexpr int kBand = 8;                  // row tiles kept together in the tile
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kBarBytes = 256;
 
+// Operand halves and, in 4 bits, three pairs of scale tiles; as many as fit.
+constexpr uint32_t stage_bytes(bool mx4) { return 2 * kHalf + (mx4 ? 3 * 1024 : 0); }
+constexpr int stages(bool mx4) { return static_cast<int>((kMaxSmem - 1024 - kBarBytes) / stage_bytes(mx4)); }
+
 struct TileMaps {
     CUtensorMap a0, a1, b0, b1, sa, sb0, sb1;
 };
@@ -56,7 +60,7 @@ struct TileParams {
     int tiles_m, tiles_n, items, splits;
     int KB1, KB;         // K blocks of the first product, of all
     int kt_n;            // 4-bit: scale tiles per row tile
-    int act, dtype, vec, nacc, stages;
+    int act, dtype, vec;
     uint32_t idesc;
 };
 
@@ -131,7 +135,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     constexpr bool kGated = kForm == TILE_GATED || kForm == TILE_MX4_GATED;
     constexpr bool kAMn = kForm == TILE_DW;
     constexpr bool kBMn = kForm == TILE_DW || kForm == TILE_DX;
-    constexpr uint32_t kStage = 2 * kHalf + (kMx4 ? 3 * 1024 : 0);
+    constexpr uint32_t kStage = stage_bytes(kMx4);
+    constexpr int kStages = stages(kMx4);
+    constexpr int kAccs = kMx4 ? 1 : 2;
     constexpr int kCols = kMx4 ? 128 : 64;      // map columns per K block, K-major operands
     constexpr int kNt = kGated ? 128 : 256;     // outputs of a tile along N
     constexpr uint32_t kSfCol = 256, kSfStage = 24;   // 4-bit: scale columns (A 8, B 16 a stage)
@@ -140,10 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t raw = smem_u32(ft_smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = ft_smem_raw + (base - raw);
-    const int S = p.stages;
-    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + static_cast<size_t>(S) * kStage);
-    uint64_t *empty = full + S;
-    uint64_t *accf = empty + S;
+    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + kStages * kStage);
+    uint64_t *empty = full + kStages;
+    uint64_t *accf = empty + kStages;
     uint64_t *acce = accf + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int nclu = static_cast<int>(gridDim.x) >> 1;
 
     if (warp == 0 && lane == 0) {
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(full + s), 1);
             mbar_init(smem_u32(empty + s), 1);
         }
@@ -203,18 +208,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (warp == 0) {
         if (lane == 0) {
             pdl_wait();
-            int kc = 0;   // K blocks of this cluster so far
+            const uint32_t full0 = mapa_shared(smem_u32(full), 0);   // the leader's barriers
+            int stage = 0;
+            uint32_t phase = 1;   // a fresh barrier passes a wait for the phase before its first
             for (int i = cid; i < p.items; i += nclu) {
                 const Item it = item_at(i);
                 const int m = it.m0 + rank * 128;
-                for (int kb = it.kb0; kb < it.kb1; ++kb, ++kc) {
-                    const int stage = kc % S;
-                    if (kc >= S)
-                        mbar_wait_bounded(smem_u32(empty + stage), static_cast<uint32_t>((kc / S - 1) & 1),
-                                          abort_flag, p.err, DEV_TIMEOUT_EMPTY);
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
                     const uint32_t st = base + stage * kStage;
-                    const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+                    const uint32_t bar = full0 + 8 * stage;
                     if (rank == 0) mbar_expect_tx(smem_u32(full + stage), 2 * kStage);
+                    if (++stage == kStages) stage = 0, phase ^= 1;
                     const bool second = kForm == TILE_DX && kb >= p.KB1;
                     const int k = second ? kb - p.KB1 : kb;
                     const CUtensorMap *ma = (kForm == TILE_DX && second) || (kForm == TILE_DW && it.z) ? &tm.a1 : &tm.a0;
@@ -246,26 +251,29 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
             }
             // Every copy of this CTA has landed, and every MMA that reads its
-            // shared memory has completed, before it leaves.
-            for (int t = kc > S ? kc - S : 0; t < kc; ++t)
-                ffn_drain_wait(smem_u32(empty + (t % S)), static_cast<uint32_t>((t / S) & 1));
+            // shared memory has completed, before it leaves: each stage's last
+            // round was returned (a stage without a round passes at once).
+            for (int t = 0; t < kStages; ++t) {
+                ffn_drain_wait(smem_u32(empty + stage), phase);
+                if (++stage == kStages) stage = 0, phase ^= 1;
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
-            int kc = 0, n_it = 0;
-            for (int i = cid; i < p.items; i += nclu, ++n_it) {
+            // The tensor cores take one MMA at a time and keep next to none
+            // queued, so what this thread does between two stages is time lost:
+            // no divisions here (stage and phase counted on), the descriptors
+            // ready beforehand.
+            int stage = 0, as = 0;
+            uint32_t phase = 0, aphase = 1;
+            for (int i = cid; i < p.items; i += nclu) {
                 const Item it = item_at(i);
-                const int as = n_it % p.nacc;
-                if (n_it >= p.nacc)
-                    mbar_wait_bounded(smem_u32(acce + as), static_cast<uint32_t>((n_it / p.nacc - 1) & 1), abort_flag,
-                                      p.err, DEV_TIMEOUT_ACC_EMPTY);
+                mbar_wait_bounded(smem_u32(acce + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
                 tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(as) * 256;
-                for (int kb = it.kb0; kb < it.kb1; ++kb, ++kc) {
-                    const int stage = kc % S;
-                    mbar_wait_bounded(smem_u32(full + stage), static_cast<uint32_t>((kc / S) & 1), abort_flag, p.err,
-                                      DEV_TIMEOUT_FULL);
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    mbar_wait_bounded(smem_u32(full + stage), phase, abort_flag, p.err, DEV_TIMEOUT_FULL);
                     tc_fence_after();
                     const uint32_t st = base + stage * kStage;
                     const uint64_t ad = kAMn ? desc_mn(st) : desc_kmajor(st);
@@ -293,19 +301,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                          (kb > it.kb0 || kk > 0) ? 1u : 0u);
                     }
                     pair_commit(smem_u32(empty + stage));
+                    if (++stage == kStages) stage = 0, phase ^= 1;
                 }
                 pair_commit(smem_u32(accf + as));
+                if (++as == kAccs) as = 0, aphase ^= 1;
             }
         }
         __syncwarp();
     } else {
         const int q = warp & 3;
-        int n_it = 0;
-        for (int i = cid; i < p.items; i += nclu, ++n_it) {
+        int as = 0;
+        uint32_t aphase = 0;
+        for (int i = cid; i < p.items; i += nclu) {
             const Item it = item_at(i);
-            const int as = n_it % p.nacc;
-            mbar_wait_bounded(smem_u32(accf + as), static_cast<uint32_t>((n_it / p.nacc) & 1), abort_flag, p.err,
-                              DEV_TIMEOUT_ACC_FULL);
+            mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
             tc_fence_after();
             const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16);
             const int64_t m = it.m0 + rank * 128 + q * 32 + lane;
@@ -355,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) remote_arrive(mapa_shared(smem_u32(acce + as), 0));
+            if (++as == kAccs) as = 0, aphase ^= 1;
         }
         __syncwarp();
     }
@@ -450,9 +460,6 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     // 16-byte stores: y's rows (and g and u's, stride N)
     p.vec = a.ldy % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1)) & 15) == 0 &&
             (!a.g || a.N % 8 == 0);
-    p.nacc = mx4 ? 1 : 2;
-    const size_t stage = 2 * kHalf + (mx4 ? 3 * 1024 : 0);
-    p.stages = static_cast<int>((kMaxSmem - 1024 - kBarBytes) / stage);
     p.idesc = mx4 ? idesc_mxf4(256, 256)
                   : idesc_f16(a.dtype, 256, 256, a.form == TILE_DW, a.form == TILE_DW || a.form == TILE_DX);
 
@@ -490,7 +497,7 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     if (e != cudaSuccess) return e;
 
     size_t smem = 0;
-    if ((e = ffn_smem_for_tmem(d.dev, 512, p.stages * stage + 1024 + kBarBytes, &smem)) != cudaSuccess) return e;
+    if ((e = ffn_smem_for_tmem(d.dev, 512, stages(mx4) * stage_bytes(mx4) + 1024 + kBarBytes, &smem)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2u * static_cast<unsigned>(std::min(p.items, d.sms / 2)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
