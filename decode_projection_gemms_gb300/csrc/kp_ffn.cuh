@@ -213,6 +213,21 @@ __device__ __forceinline__ uint32_t idesc_sf(uint32_t idesc, uint32_t byte) {
     return idesc | (byte << 29) | (byte << 4);
 }
 
+// One lane of a converged warp, the same one at every later call. Loops that issue
+// MMAs or copies run with all 32 lanes and only their instructions are this
+// lane's: operands then stay in the warp's uniform registers. In a branch taken by
+// one lane each MMA is preceded by moves into them, which its queue does not hide
+// (4-bit product 4096 x 4096 x 7168: 81 us against 58).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Wait (bounded by time only) for a barrier phase; used to drain copies.
 __device__ __forceinline__ void ffn_drain_wait(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();

@@ -25,7 +25,7 @@
 //            accumulator and the scales fill the tensor memory, so these have
 //            one accumulator, the 16-bit forms two.
 //
-// Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 5: epilogue.
+// Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 9: epilogue.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -36,7 +36,7 @@ namespace kp {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kTile = 256;                // rows of D per cluster; columns too
 constexpr uint32_t kHalf = 128 * 128;     // bytes of 128 rows of a K block (128 bytes of K)
 constexpr int kBand = 8;                  // row tiles kept together in the tile order
@@ -113,14 +113,24 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
     return elem_round(a, dtype) | static_cast<uint32_t>(elem_round(b, dtype)) << 16;
 }
 
-// 32 consecutive outputs of one row.
-__device__ __forceinline__ void put_row32(uint16_t *dst, const float (&v)[32], int left, bool vec, int dtype) {
+// 32 consecutive outputs of one row, in stores of 32 bytes (vec 2), 16 (1) or 2.
+__device__ __forceinline__ void put_row32(uint16_t *dst, const float (&v)[32], int left, int vec, int dtype) {
     if (vec && left >= 32) {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4 *>(dst)[i] =
-                make_uint4(pack2(v[8 * i], v[8 * i + 1], dtype), pack2(v[8 * i + 2], v[8 * i + 3], dtype),
-                           pack2(v[8 * i + 4], v[8 * i + 5], dtype), pack2(v[8 * i + 6], v[8 * i + 7], dtype));
+        for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], dtype);
+        if (vec == 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * i), "r"(w[8 * i]),
+                             "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]),
+                             "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(accf + i), 1);
-            mbar_init(smem_u32(acce + i), 8);   // four epilogue warps of each CTA
+            mbar_init(smem_u32(acce + i), 16);   // eight epilogue warps of each CTA
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -206,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
+            const bool mine = elect_one();
             pdl_wait();
             const uint32_t full0 = mapa_shared(smem_u32(full), 0);   // the leader's barriers
             int stage = 0;
@@ -218,8 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
                     const uint32_t st = base + stage * kStage;
                     const uint32_t bar = full0 + 8 * stage;
-                    if (rank == 0) mbar_expect_tx(smem_u32(full + stage), 2 * kStage);
+                    if (rank == 0 && mine) mbar_expect_tx(smem_u32(full + stage), 2 * kStage);
                     if (++stage == kStages) stage = 0, phase ^= 1;
+                    if (!mine) continue;
                     const bool second = kForm == TILE_DX && kb >= p.KB1;
                     const int k = second ? kb - p.KB1 : kb;
                     const CUtensorMap *ma = (kForm == TILE_DX && second) || (kForm == TILE_DW && it.z) ? &tm.a1 : &tm.a0;
@@ -260,111 +272,124 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            // The tensor cores take one MMA at a time and keep next to none
-            // queued, so what this thread does between two stages is time lost:
-            // no divisions here (stage and phase counted on), the descriptors
-            // ready beforehand.
+        if (rank == 0) {
+            const bool mine = elect_one();
+            // The tensor cores keep next to no MMAs queued, so what this thread
+            // does between two stages is time lost. Stage and phase are counted
+            // on, and the next stage is waited for (and its scales are sent to
+            // TMEM) before the last MMA of this one is issued.
             int stage = 0, as = 0;
             uint32_t phase = 0, aphase = 1;
+            auto prepare = [&](int s, uint32_t ph) {
+                mbar_wait_bounded(smem_u32(full + s), ph, abort_flag, p.err, DEV_TIMEOUT_FULL);
+                tc_fence_after();
+                if constexpr (kMx4) {
+                    // columns: A's tiles 0 and 1 of the block, then for each B's two row tiles
+                    const uint32_t sf = tmem + kSfCol + static_cast<uint32_t>(s) * kSfStage;
+                    const uint64_t sc = desc_scales(base + s * kStage + 2 * kHalf);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (!mine) break;
+                        pair_cp_scales(sf + 4 * j, sc + 32 * j);
+                        pair_cp_scales(sf + 8 + 8 * j, sc + 64 + 32 * j);
+                        pair_cp_scales(sf + 12 + 8 * j, sc + 128 + 32 * j);
+                    }
+                }
+            };
+            if (cid < p.items) prepare(0, 0);
             for (int i = cid; i < p.items; i += nclu) {
                 const Item it = item_at(i);
                 mbar_wait_bounded(smem_u32(acce + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
                 tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(as) * 256;
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                    mbar_wait_bounded(smem_u32(full + stage), phase, abort_flag, p.err, DEV_TIMEOUT_FULL);
-                    tc_fence_after();
                     const uint32_t st = base + stage * kStage;
                     const uint64_t ad = kAMn ? desc_mn(st) : desc_kmajor(st);
                     const uint64_t bd = kBMn ? desc_mn(st + kHalf) : desc_kmajor(st + kHalf);
-                    if constexpr (kMx4) {
-                        const uint32_t sf = tmem + kSfCol + static_cast<uint32_t>(stage) * kSfStage;
-                        const uint32_t sc = st + 2 * kHalf;
-                        // columns: A's tiles 0 and 1 of the block, then for each B's two row tiles
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            pair_cp_scales(sf + 4 * j, desc_scales(sc + 512 * j));
-                            pair_cp_scales(sf + 8 + 8 * j, desc_scales(sc + 1024 + 512 * j));
-                            pair_cp_scales(sf + 12 + 8 * j, desc_scales(sc + 2048 + 512 * j));
-                        }
-                        // steps past K are left out: their scales belong to other rows
-                        const int steps = min(4, (p.K - kb * 256 + 63) >> 6);
-                        for (int kk = 0; kk < steps; ++kk)
+                    const uint32_t sf = tmem + kSfCol + static_cast<uint32_t>(stage) * kSfStage;
+                    const uint32_t bar = smem_u32(empty + stage);
+                    // 64 4-bit columns a step, and steps past K are left out (their
+                    // scales belong to other rows); 16 16-bit ones, 32 bytes of a row
+                    // or 16 rows of 128 bytes on
+                    const int steps = kMx4 ? min(4, (p.K - kb * 256 + 63) >> 6) : 4;
+                    auto mma = [&](int kk) {
+                        if (!mine) return;
+                        const uint32_t more = kb > it.kb0 || kk > 0;
+                        if constexpr (kMx4)
                             pair_mma_mxf4(d, ad + 2 * kk, bd + 2 * kk, idesc_sf(p.idesc, (kk & 1) * 2),
-                                          sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (kb > it.kb0 || kk > 0) ? 1u : 0u);
-                    } else {
-                        // 16 K a step: 32 bytes of a row, or 16 rows of 128 bytes
+                                          sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), more);
+                        else
+                            pair_mma_f16(d, ad + kk * (kAMn ? 128 : 2), bd + kk * (kBMn ? 128 : 2), p.idesc, more);
+                    };
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            pair_mma_f16(d, ad + kk * (kAMn ? 128 : 2), bd + kk * (kBMn ? 128 : 2), p.idesc,
-                                         (kb > it.kb0 || kk > 0) ? 1u : 0u);
-                    }
-                    pair_commit(smem_u32(empty + stage));
+                    for (int kk = 0; kk < 3; ++kk)
+                        if (kk < steps - 1) mma(kk);
                     if (++stage == kStages) stage = 0, phase ^= 1;
+                    if (kb + 1 < it.kb1 || i + nclu < p.items) prepare(stage, phase);
+                    mma(steps - 1);
+                    if (mine) pair_commit(bar);
                 }
-                pair_commit(smem_u32(accf + as));
+                if (mine) pair_commit(smem_u32(accf + as));
                 if (++as == kAccs) as = 0, aphase ^= 1;
             }
         }
         __syncwarp();
     } else {
+        // Two warps for each quarter of the accumulator's rows, each with half of
+        // the tile's outputs. A warp reads all of its sums into registers and gives
+        // the accumulator back before it computes or stores anything.
         const int q = warp & 3;
+        const int half = warp >= 6;
+        constexpr int kSpan = kNt / 2;   // outputs of a thread: 128, gated 64 (from 64 + 64 sums)
         int as = 0;
         uint32_t aphase = 0;
         for (int i = cid; i < p.items; i += nclu) {
             const Item it = item_at(i);
             mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
             tc_fence_after();
-            const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16);
-            const int64_t m = it.m0 + rank * 128 + q * 32 + lane;
-            for (int c = 0; c < kNt; c += 32) {
-                uint32_t va[32];
-                tmem_ld32(t + c, va);
-                const int n = it.n0 + c;
-                const int left = p.N - n;
-                if constexpr (kGated) {
-                    uint32_t vb[32];
-                    tmem_ld32(t + 128 + c, vb);
-                    tmem_ld_wait();
-                    if (m < p.M && left > 0) {
-                        float a[32], b[32], h[32];
+            const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * kSpan;
+            uint32_t v[4][32];   // gated: 0 and 1 the gates, 2 and 3 their factors
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            a[j] = __uint_as_float(va[j]);
-                            b[j] = __uint_as_float(vb[j]);
-                            h[j] = ffn_act(a[j], p.act) * b[j];
-                        }
-                        put_row32(p.y0 + m * p.ldy + n, h, left, p.vec != 0, p.dtype);
-                        if (!kMx4 && p.g) {
-                            put_row32(p.g + m * p.N + n, a, left, p.vec != 0, p.dtype);
-                            put_row32(p.u + m * p.N + n, b, left, p.vec != 0, p.dtype);
-                        }
-                    }
-                } else {
-                    tmem_ld_wait();
-                    if (m < p.M && left > 0) {
-                        float a[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(va[j]);
-                        if (kForm == TILE_DX && p.splits > 1) {
-                            float *dst = p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)   // N is a multiple of 8
-                                if (4 * j < left)
-                                    reinterpret_cast<float4 *>(dst)[j] =
-                                        make_float4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
-                        } else {
-                            uint16_t *y = kForm == TILE_DW && it.z ? p.y1 : p.y0;
-                            put_row32(y + m * p.ldy + n, a, left, p.vec != 0, p.dtype);
-                        }
-                    }
-                }
-            }
+            for (int c = 0; c < 4; ++c) tmem_ld32(t + (kGated && c >= 2 ? 64 : 0) + 32 * c, v[c]);
+            tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) remote_arrive(mapa_shared(smem_u32(acce + as), 0));
             if (++as == kAccs) as = 0, aphase ^= 1;
+            const int64_t m = it.m0 + rank * 128 + q * 32 + lane;
+            if (m >= p.M) continue;
+#pragma unroll
+            for (int c = 0; c < kSpan / 32; ++c) {
+                const int n = it.n0 + half * kSpan + 32 * c;
+                const int left = p.N - n;
+                if (left <= 0) break;
+                float a[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(v[c][j]);
+                if constexpr (kGated) {
+                    float b[32], h[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        b[j] = __uint_as_float(v[2 + c][j]);
+                        h[j] = ffn_act(a[j], p.act) * b[j];
+                    }
+                    put_row32(p.y0 + m * p.ldy + n, h, left, p.vec, p.dtype);
+                    if (!kMx4 && p.g) {
+                        put_row32(p.g + m * p.N + n, a, left, p.vec, p.dtype);
+                        put_row32(p.u + m * p.N + n, b, left, p.vec, p.dtype);
+                    }
+                } else if (kForm == TILE_DX && p.splits > 1) {
+                    float *dst = p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)   // N is a multiple of 8
+                        if (4 * j < left)
+                            reinterpret_cast<float4 *>(dst)[j] =
+                                make_float4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+                } else {
+                    uint16_t *y = kForm == TILE_DW && it.z ? p.y1 : p.y0;
+                    put_row32(y + m * p.ldy + n, a, left, p.vec, p.dtype);
+                }
+            }
         }
         __syncwarp();
     }
@@ -457,9 +482,12 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     p.kt_n = static_cast<int>(mx4_ktiles(a.K));
     p.act = a.act;
     p.dtype = a.dtype;
-    // 16-byte stores: y's rows (and g and u's, stride N)
-    p.vec = a.ldy % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1)) & 15) == 0 &&
-            (!a.g || a.N % 8 == 0);
+    // the widest store that every row's 32-column pieces allow: y's rows, and g and
+    // u's (stride N)
+    const uintptr_t starts = reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1) |
+                             reinterpret_cast<uintptr_t>(a.g) | reinterpret_cast<uintptr_t>(a.u) |
+                             static_cast<uintptr_t>(a.ldy * 2) | (a.g ? static_cast<uintptr_t>(a.N) * 2 : 0);
+    p.vec = starts % 32 == 0 ? 2 : starts % 16 == 0 ? 1 : 0;
     p.idesc = mx4 ? idesc_mxf4(256, 256)
                   : idesc_f16(a.dtype, 256, 256, a.form == TILE_DW, a.form == TILE_DW || a.form == TILE_DX);
 
