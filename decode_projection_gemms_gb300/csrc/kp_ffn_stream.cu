@@ -144,41 +144,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
-        if (lane == 0) {
-            pdl_wait();   // x (quantised by the kernel before, when there is one)
+        const bool mine = elect_one();
+        pdl_wait();   // x (quantised by the kernel before, when there is one)
+        if (mine)
             for (int s = 0; s < pre; ++s) issue_x(s, s);
-            for (int s = pre; s < n_st; ++s) {
-                const int stage = s % S;
-                mbar_wait_bounded(smem_u32(empty + stage), static_cast<uint32_t>(((s / S) - 1) & 1), abort_flag,
-                                  p.err, DEV_TIMEOUT_EMPTY);
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int s = pre; s < n_st; ++s) {
+            mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
+            if (mine) {
                 issue_w(s, stage);
                 issue_x(s, stage);
             }
-            if (*abort_flag)
-                for (int s = n_st > S ? n_st - S : 0; s < n_st; ++s)
-                    ffn_drain_wait(smem_u32(full + (s % S)), static_cast<uint32_t>((s / S) & 1));
+            if (++stage == S) stage = 0, phase ^= 1;
         }
+        if (*abort_flag)
+            for (int s = n_st > S ? n_st - S : 0; s < n_st; ++s)
+                ffn_drain_wait(smem_u32(full + (s % S)), static_cast<uint32_t>((s / S) & 1));
+        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            for (int s = 0; s < n_st; ++s) {
-                const int stage = s % S;
-                mbar_wait_bounded(smem_u32(full + stage), static_cast<uint32_t>((s / S) & 1), abort_flag, p.err,
-                                  DEV_TIMEOUT_FULL);
-                tc_fence_after();
+        const bool mine = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int s = 0; s < n_st; ++s) {
+            mbar_wait_bounded(smem_u32(full + stage), phase, abort_flag, p.err, DEV_TIMEOUT_FULL);
+            tc_fence_after();
+            if (mine) {
                 const uint32_t st = base + stage * p.stage_bytes;
                 const uint64_t ad = desc_kmajor(st);
                 const uint64_t bd = desc_kmajor(st + L::w_bytes);
                 if constexpr (kMx4) {
                     const int kb = kb0 + s;
                     const uint32_t sf = tmem + p.sf_col + static_cast<uint32_t>(stage) * L::sf_cols;
-                    const uint32_t sc = st + L::off_sc(p.Mpad);
+                    const uint64_t sc = desc_scales(st + L::off_sc(p.Mpad));
                     for (int j = 0; j < sc_tiles(kb); ++j)
 #pragma unroll
-                        for (int o = 0; o <= kAcc; ++o)   // gate, up, tokens
-                            tmem_cp_scales(sf + 8 * o + 4 * j, desc_scales(sc + 1024 * o + 512 * j));
+                        for (int o = 0; o <= kAcc; ++o)   // weights, tokens
+                            tmem_cp_scales(sf + 8 * o + 4 * j, sc + 64 * o + 32 * j);
                     // 64 columns a step; steps past K are left out (their scales are not loaded)
                     const int steps = min(4, (p.K - kb * 256 + 63) >> 6);
-                    for (int kk = 0; kk < steps; ++kk) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk >= steps) break;
                         const uint32_t id = idesc_sf(p.idesc, (kk & 1) * 2);
                         const uint32_t sfk = sf + 4 * (kk >> 1);
 #pragma unroll
@@ -189,15 +196,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                        for (int a = 0; a < kAcc; ++a)
-                            umma_bf16(tmem + a * p.Mpad, ad + (a * kRows * 128 >> 4) + 2 * kk, bd + 2 * kk, p.idesc,
-                                      (s > 0 || kk > 0) ? 1u : 0u);
+                        umma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, p.idesc, (s > 0 || kk > 0) ? 1u : 0u);
                 }
                 umma_commit(smem_u32(empty + stage));
             }
-            umma_commit(smem_u32(accf));
+            if (++stage == S) stage = 0, phase ^= 1;
         }
+        if (mine) umma_commit(smem_u32(accf));
         __syncwarp();
     } else {
         // accumulators -> this CTA's partial tile [token][kPart], 128 bytes a warp

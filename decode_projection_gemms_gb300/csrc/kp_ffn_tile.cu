@@ -39,7 +39,7 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kTile = 256;                // rows of D per cluster; columns too
 constexpr uint32_t kHalf = 128 * 128;     // bytes of 128 rows of a K block (128 bytes of K)
-constexpr int kBand = 8;                  // row tiles kept together in the tile order
+constexpr int kBand = 16;                 // row tiles kept together in the tile order (8: backward 1.5 % slower)
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kBarBytes = 256;
 
