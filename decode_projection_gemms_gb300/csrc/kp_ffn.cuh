@@ -80,6 +80,7 @@ struct FfnArgs {
 };
 // Few tokens: weight streaming, split-K over a cluster (kp_ffn_stream.cu).
 size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms);   // bytes
+float ffn_stream_us(bool gated, int M, int N, int K, int sms);   // estimate of a 4-bit product's time
 cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s);
 
 // One launch of the tile kernel (kp_ffn_tile.cu), for many tokens and for the
@@ -125,29 +126,43 @@ namespace kp {
 
 // ---- activations ------------------------------------------------------------
 // act(g), in fp32.
-__device__ __forceinline__ float ffn_act(float g, int act) {
-    if (act == KP_ACT_SILU) return __fdividef(g, 1.f + __expf(-g));
-    if (act == KP_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+template <int kAct>
+__device__ __forceinline__ float ffn_act(float g) {
+    if constexpr (kAct == KP_ACT_SILU) return __fdividef(g, 1.f + __expf(-g));
+    if constexpr (kAct == KP_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
     // 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)), z = sqrt(2/pi) (g + 0.044715 g^3)
     const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
     return __fdividef(g, 1.f + __expf(-z2));
 }
+// h = act(a) b. The choice is made once for all N, so only one activation's code
+// runs through the instruction cache.
+template <int N>
+__device__ __forceinline__ void ffn_gate(const float (&a)[N], const float (&b)[N], int act, float (&h)[N]) {
+    if (act == KP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[i] = ffn_act<KP_ACT_SILU>(a[i]) * b[i];
+    } else if (act == KP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[i] = ffn_act<KP_ACT_GELU>(a[i]) * b[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[i] = ffn_act<KP_ACT_GELU_TANH>(a[i]) * b[i];
+    }
+}
 
 // act(g) and act'(g), in fp32.
-__device__ __forceinline__ void ffn_act_grad(float g, int act, float &a, float &da) {
-    if (act == KP_ACT_SILU) {
+template <int kAct>
+__device__ __forceinline__ void ffn_act_grad(float g, float &a, float &da) {
+    a = ffn_act<kAct>(g);
+    if constexpr (kAct == KP_ACT_SILU) {
         const float s = __fdividef(1.f, 1.f + __expf(-g));
-        a = ffn_act(g, act);
         da = s * (1.f + g * (1.f - s));
-    } else if (act == KP_ACT_GELU) {
-        const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
-        a = g * cdf;
-        da = cdf + g * 0.39894228040143268f * __expf(-0.5f * g * g);
+    } else if constexpr (kAct == KP_ACT_GELU) {
+        da = 0.5f * (1.f + erff(g * 0.70710678118654752f)) + g * 0.39894228040143268f * __expf(-0.5f * g * g);
     } else {
         // a = g s(w), s the logistic function, w = 2 sqrt(2/pi) (g + 0.044715 g^3)
         const float w = 1.5957691216057308f * (g + 0.044715f * g * g * g);
         const float s = __fdividef(1.f, 1.f + __expf(-w));
-        a = ffn_act(g, act);
         da = s + g * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * g * g);
     }
 }

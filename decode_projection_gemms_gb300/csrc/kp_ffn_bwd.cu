@@ -9,10 +9,11 @@ namespace kp {
 
 namespace {
 
+template <int kAct>
 __global__ void __launch_bounds__(256)
     gate_grad_kernel(const uint16_t *__restrict__ dh, int64_t lddh, const uint16_t *__restrict__ g,
                      const uint16_t *__restrict__ u, uint16_t *__restrict__ dg, uint16_t *__restrict__ du,
-                     int64_t ld, int T, int F, int act, int dtype, int vec) {
+                     int64_t ld, int T, int F, int dtype, int vec) {
     const int chunks = (F + 7) >> 3;
     const int64_t total = static_cast<int64_t>(T) * chunks;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(256)
         for (int k = 0; k < 8; ++k) {
             const float d = elem_widen(a.h[k], dtype);
             float av, dav;
-            ffn_act_grad(elem_widen(b.h[k], dtype), act, av, dav);
+            ffn_act_grad<kAct>(elem_widen(b.h[k], dtype), av, dav);
             ou.h[k] = elem_round(d * av, dtype);
             og.h[k] = elem_round(d * elem_widen(c.h[k], dtype) * dav, dtype);
         }
@@ -58,9 +59,13 @@ cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const void *g, co
     const int64_t blocks = (total + 255) / 256;
     const int grid = static_cast<int>(blocks < sms * 8LL ? blocks : sms * 8LL);
     const bool vec = F % 8 == 0 && lddh % 8 == 0 && (reinterpret_cast<uintptr_t>(dh) & 15) == 0;
-    gate_grad_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(dh), lddh, static_cast<const uint16_t *>(g),
-                                          static_cast<const uint16_t *>(u), static_cast<uint16_t *>(dg),
-                                          static_cast<uint16_t *>(du), ld, T, F, act, dtype, vec);
+    using Fn = void (*)(const uint16_t *, int64_t, const uint16_t *, const uint16_t *, uint16_t *, uint16_t *, int64_t, int,
+                        int, int, int);
+    static const Fn kernels[] = {gate_grad_kernel<KP_ACT_SILU>, gate_grad_kernel<KP_ACT_GELU>,
+                                 gate_grad_kernel<KP_ACT_GELU_TANH>};
+    kernels[act]<<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(dh), lddh, static_cast<const uint16_t *>(g),
+                                      static_cast<const uint16_t *>(u), static_cast<uint16_t *>(dg),
+                                      static_cast<uint16_t *>(du), ld, T, F, dtype, vec);
     return cudaGetLastError();
 }
 

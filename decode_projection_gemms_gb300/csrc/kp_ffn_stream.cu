@@ -241,48 +241,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t stride = static_cast<size_t>(kPart) * p.Mpad;
         const float *parts = C > 1 ? p.ws + (static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C * stride
                                    : reinterpret_cast<const float *>(gbase);
-        // a lane takes four features of a token; CTA r of the cluster every C-th
-        // group of tokens
+        // A lane takes four features of a token, CTA r of the cluster every C-th
+        // group of tokens, kDeep groups at a time so that their sums are read
+        // together.
         constexpr int kLanes = L::feat / 4;              // lanes per token: 16 or 32
-        constexpr int kTok = kThreads / kLanes;          // tokens at a time
+        constexpr int kTok = kThreads / kLanes;          // tokens of a group
+        constexpr int kDeep = kGated ? 2 : 4;
         const int f = 4 * (threadIdx.x % kLanes);
         const int n = tile * L::feat + f;
-        for (int m = rank * kTok + threadIdx.x / kLanes; m < Mloc; m += kTok * C) {
-            float va[4] = {0.f, 0.f, 0.f, 0.f}, vb[4] = {0.f, 0.f, 0.f, 0.f};
-            const float *src = parts + static_cast<size_t>(m) * kPart + f;
+        for (int mb = rank * kTok + threadIdx.x / kLanes; mb < Mloc; mb += kTok * C * kDeep) {
+            float va[kDeep][4], vb[kDeep][4];
+#pragma unroll
+            for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) va[d][i] = vb[d][i] = 0.f;
             auto add = [&](const float *at, float(&v)[4]) {
                 const float4 a = C > 1 ? __ldcg(reinterpret_cast<const float4 *>(at)) : *reinterpret_cast<const float4 *>(at);
                 v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
             };
 #pragma unroll 4
-            for (int r = 0; r < C; ++r) {   // in rank order
-                add(src + r * stride, va);
-                if constexpr (kGated) add(src + r * stride + L::feat, vb);
-            }
-            const int64_t om = m0 + m;
-            auto put = [&](uint16_t *dst, int64_t ld, const float(&v)[4]) {
-                uint16_t *d = dst + om * ld + n;
-                if (p.vec4 && n + 4 <= p.N) {
+            for (int r = 0; r < C; ++r)   // in rank order
+#pragma unroll
+                for (int d = 0; d < kDeep; ++d) {
+                    // past the end: the last token again, so that no branch parts the loads
+                    const int m = min(mb + d * kTok * C, Mloc - 1);
+                    const float *src = parts + r * stride + static_cast<size_t>(m) * kPart + f;
+                    add(src, va[d]);
+                    if constexpr (kGated) add(src + L::feat, vb[d]);
+                }
+#pragma unroll
+            for (int d = 0; d < kDeep; ++d) {
+                const int64_t om = m0 + mb + d * kTok * C;
+                if (om - m0 >= Mloc) continue;
+                auto put = [&](uint16_t *dst, int64_t ld, const float(&v)[4]) {
+                    uint16_t *o = dst + om * ld + n;
                     const uint32_t lo = elem_round(v[0], p.dtype) | static_cast<uint32_t>(elem_round(v[1], p.dtype)) << 16;
                     const uint32_t hi = elem_round(v[2], p.dtype) | static_cast<uint32_t>(elem_round(v[3], p.dtype)) << 16;
-                    *reinterpret_cast<uint2 *>(d) = make_uint2(lo, hi);
+                    if (p.vec4 && n + 4 <= p.N) {
+                        *reinterpret_cast<uint2 *>(o) = make_uint2(lo, hi);
+                    } else {
+                        if (n < p.N) o[0] = static_cast<uint16_t>(lo);
+                        if (n + 1 < p.N) o[1] = static_cast<uint16_t>(lo >> 16);
+                        if (n + 2 < p.N) o[2] = static_cast<uint16_t>(hi);
+                        if (n + 3 < p.N) o[3] = static_cast<uint16_t>(hi >> 16);
+                    }
+                };
+                if constexpr (kGated) {
+                    float h[4];
+                    ffn_gate(va[d], vb[d], p.act, h);
+                    put(p.y, p.ldy, h);
+                    if (!kMx4 && p.g) {
+                        put(p.g, p.N, va[d]);
+                        put(p.u, p.N, vb[d]);
+                    }
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (n + i < p.N) d[i] = elem_round(v[i], p.dtype);
+                    put(p.y, p.ldy, va[d]);
                 }
-            };
-            if constexpr (kGated) {
-                float h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = ffn_act(va[i], p.act) * vb[i];
-                put(p.y, p.ldy, h);
-                if (!kMx4 && p.g) {
-                    put(p.g, p.N, va);
-                    put(p.u, p.N, vb);
-                }
-            } else {
-                put(p.y, p.ldy, va);
             }
         }
     }
@@ -319,11 +333,16 @@ Plan make_plan(bool mx4, bool gated, int M, int N, int K, int sms) {
     q.mt = (M + q.Mpad - 1) / q.Mpad;
     q.tiles = (N + q.feat - 1) / q.feat;
     q.KB = mx4 ? (K + 255) / 256 : (K + 63) / 64;
-    // Up to two CTAs per SM, while each keeps at least two K blocks. T = 1, F = 2048,
-    // K = 7168, 16-bit gated: C = 8 13.8 us, 4 15.1, 2 24; 77 x 4099 x 2050 in 4 bits
-    // (nine K blocks): C = 8 9.4 us, 4 8.0, 2 11.2.
+    // The cluster grows while each CTA keeps two K blocks and the grid stays below
+    // what was measured to help: 1.7 CTAs per SM in 16 bits (T = 1, K = 7168, gated:
+    // F = 2048 C = 8 10.3 us, 4 10.6; F = 1408 9.1, 10.1; F = 256 7.2, 9.5), one in 4
+    // bits (16 x 4096 x 7168: C = 8 13.1 us, 4 6.6), and for C = 8 in 4 bits the 15
+    // clusters that fit at one CTA per SM (16 x 1408: C = 8 6.0, 4 6.3; 16 x 2048: 9.4,
+    // 6.4). Two blocks: 77 x 4099 x 2050 in 4 bits (nine) C = 8 9.4, 4 8.0, 2 11.2.
+    const int64_t grid = static_cast<int64_t>(q.tiles) * q.mt;
+    const int most = mx4 ? sms : sms * 17 / 10;
     q.C = 1;
-    while (q.C < 8 && static_cast<int64_t>(q.tiles) * q.mt * q.C <= sms && q.C * 4 <= q.KB) q.C *= 2;
+    while (q.C < 8 && q.KB >= 4 * q.C && grid * q.C * 2 <= (mx4 && q.C == 4 ? sms * 4 / 5 : most)) q.C *= 2;
     const uint32_t acc = static_cast<uint32_t>(q.acc) * q.Mpad;
     int st = static_cast<int>((kSmem - 1024 - kBarBytes) / q.stage_bytes);
     st = std::min(st, kMaxStages);
@@ -342,6 +361,19 @@ std::mutex g_mu;
 std::map<int, bool> g_ready;   // devices whose kernels have their shared memory raised
 
 }  // namespace
+
+// Least-squares fit of 480 measured 4-bit products (16 <= M <= 1536, 256 <= N <=
+// 4096, 512 <= K <= 7168), off by 5 to 8 % on average: rounds of CTAs over the SMs,
+// each with its K blocks and its share of the tokens' sums.
+float ffn_stream_us(bool gated, int M, int N, int K, int sms) {
+    const Plan q = make_plan(true, gated, M, N, K, sms);
+    const float tok = static_cast<float>(q.Mpad) / kMaxTok;
+    const int per_sm = gated && q.Mpad > 64 ? 1 : 2;   // TMEM: scales and two accumulators
+    const float r = static_cast<float>((static_cast<int64_t>(q.tiles) * q.mt * q.C + sms * per_sm - 1) / (sms * per_sm));
+    const float kb = static_cast<float>((q.KB + q.C - 1) / q.C);
+    return gated ? 2.3f + r * (1.4f + 0.48f * kb + tok * (5.4f + 1.2f / q.C))
+                 : -5.f + r * (8.7f + 0.38f * kb + tok * (2.6f + 0.8f / q.C));
+}
 
 size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms) {
     const Plan q = make_plan(mx4, gated, M, N, K, sms);

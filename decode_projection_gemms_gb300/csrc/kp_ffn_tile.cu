@@ -115,26 +115,24 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
 
 // 32 consecutive outputs of one row, in stores of 32 bytes (vec 2), 16 (1) or 2.
 __device__ __forceinline__ void put_row32(uint16_t *dst, const float (&v)[32], int left, int vec, int dtype) {
-    if (vec && left >= 32) {
-        uint32_t w[16];
+    uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], dtype);
-        if (vec == 2) {
+    for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], dtype);
+    if (vec == 2 && left >= 32) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * i), "r"(w[8 * i]),
-                             "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]),
-                             "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
-                             : "memory");
-        } else {
+        for (int i = 0; i < 2; ++i)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * i), "r"(w[8 * i]),
+                         "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]),
+                         "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                         : "memory");
+    } else if (vec && left >= 32) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        }
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (i < left) dst[i] = elem_round(v[i], dtype);
+            if (i < left) dst[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
     }
 }
 
@@ -369,15 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if constexpr (kGated) {
                     float b[32], h[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        b[j] = __uint_as_float(v[2 + c][j]);
-                        h[j] = ffn_act(a[j], p.act) * b[j];
-                    }
-                    put_row32(p.y0 + m * p.ldy + n, h, left, p.vec, p.dtype);
+                    for (int j = 0; j < 32; ++j) b[j] = __uint_as_float(v[2 + c][j]);
                     if (!kMx4 && p.g) {
                         put_row32(p.g + m * p.N + n, a, left, p.vec, p.dtype);
                         put_row32(p.u + m * p.N + n, b, left, p.vec, p.dtype);
                     }
+                    ffn_gate(a, b, p.act, h);
+                    put_row32(p.y0 + m * p.ldy + n, h, left, p.vec, p.dtype);
                 } else if (kForm == TILE_DX && p.splits > 1) {
                     float *dst = p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n;
 #pragma unroll
@@ -431,10 +427,17 @@ std::map<int, bool> g_ready;
 
 }  // namespace
 
+// 16 bits: from a quarter of the SM pairs' worth of tiles on (K = 4096, F = 4096: T =
+// 256 25 us either way, T = 384 27 against 31, T = 1024 47 against 64; over 240
+// measured sizes 0.4 % slower than the better of the two each time). 4 bits, where
+// both kernels' fixed costs weigh more: by estimates of both, 1.5 % and 0.5 % (gated)
+// slower than the better one over 240 sizes each.
 bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms) {
-    (void)mx4, (void)K;
-    // enough tiles for half of the SM pairs
-    return 4ll * cdiv(M, kTile) * cdiv(N, gated ? 128 : 256) >= sms;
+    const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, gated ? 128 : 256);
+    if (!mx4) return 4 * tiles >= sms;
+    const float waves = static_cast<float>((tiles + sms / 2 - 1) / (sms / 2));
+    const float us = 5.2f + waves * (2.f + 0.34f * static_cast<float>(cdiv(K, 256)));
+    return us < ffn_stream_us(gated, M, N, K, sms);
 }
 
 size_t ffn_tile_scratch(int form, int M, int N, int K, int sms) {
