@@ -614,7 +614,7 @@ def gated_ffn(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "s
     fp32. ``x`` [T, K], ``Wg`` and ``Wu`` [F, K], all bfloat16 or all float16; rows
     may be strided (strides and K multiples of 8, 16-byte aligned). ``act``:
     "silu", "gelu" (erf) or "gelu_tanh". With ``save`` returns ``(h, g, u)``, the
-    two products rounded to x's type, for ``gated_ffn_backward``."""
+    two products in float32, for ``gated_ffn_backward``."""
     if _elsewhere(x, "x", stream):
         with _on(x.device, stream, x, Wg, Wu, h):
             return gated_ffn(x, Wg, Wu, act, h, save)
@@ -624,7 +624,8 @@ def gated_ffn(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "s
     h, ldh = _out(h, "h", T, F, dt, index)
     g = u = gp = up = None
     if save:
-        g, u = x.new_empty((T, F)), x.new_empty((T, F))
+        g = torch.empty((T, F), dtype=torch.float32, device=_device(index))
+        u = torch.empty((T, F), dtype=torch.float32, device=_device(index))
         gp, up = g.data_ptr(), u.data_ptr()
     work, wp, wn = _work(FFN_GATED, T, F, K, index)
     rc = load().kp_gated_ffn(x.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu, h.data_ptr(), ldh, gp, up,
@@ -650,7 +651,7 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu: 
     lddh = _rows(dh, "dh", dt, index)
     for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
         if t is not dh:
-            _rows(t, name, dt, index)
+            _rows(t, name, torch.float32, index)
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
         if t.shape != (T, F):

@@ -72,7 +72,7 @@ struct FfnArgs {
     Mx4Mat qx, qa, qb;           // microscaled operands
     void *y = nullptr;
     int64_t ldy = 0;
-    void *g = nullptr, *u = nullptr;   // optional, 16-bit gated: both products, rounded, [M, N]
+    float *g = nullptr, *u = nullptr;   // optional, 16-bit gated: both products' sums, [M, N]
     int M = 0, N = 0, K = 0;
     float *ws = nullptr;         // split-K partial tiles
     bool pdl = false;            // launched behind a kernel that writes only qx
@@ -100,7 +100,7 @@ struct FfnTileArgs {
     Mx4Mat qa, qb0, qb1;
     void *y0 = nullptr, *y1 = nullptr;
     int64_t ldy = 0;
-    void *g = nullptr, *u = nullptr;
+    float *g = nullptr, *u = nullptr;
     int M = 0, N = 0, K = 0;     // D is M x N (gated: N = F); K per product
     float *ws = nullptr;         // TILE_DX: split-K partial sums
     bool pdl = false;
@@ -115,7 +115,7 @@ bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms);
 
 // dG = dh u act'(g), dU = dh act(g): the gradients of both products, [T, F]
 // with row stride ld (kp_ffn_bwd.cu).
-cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const void *g, const void *u, void *dg, void *du,
+cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const float *g, const float *u, void *dg, void *du,
                                  int64_t ld, int T, int F, int act, int dtype, int sms, cudaStream_t s);
 
 }  // namespace kp

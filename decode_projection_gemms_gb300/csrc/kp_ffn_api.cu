@@ -346,7 +346,7 @@ int kp_mx4_gated_ffn(const void *x, int64_t ldx, const void *x_codes, const void
 }
 
 int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg, const void *Wu, int64_t ldu, void *h,
-                 int64_t ldh, void *g, void *u, int T, int F, int K, int act, int dtype, void *work,
+                 int64_t ldh, float *g, float *u, int T, int F, int K, int act, int dtype, void *work,
                  size_t work_bytes, kp_stream_t stream) {
     const char *fn = "kp_gated_ffn";
     if (T < 0 || F < 1 || K < 1) return bad_sizes(fn, T, F, K);
@@ -389,7 +389,7 @@ int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg, const 
 }
 
 int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx, const void *Wg, int64_t ldg,
-                          const void *Wu, int64_t ldu, const void *g, const void *u, void *dx, void *dWg, void *dWu,
+                          const void *Wu, int64_t ldu, const float *g, const float *u, void *dx, void *dWg, void *dWu,
                           int T, int F, int K, int act, int dtype, void *work, size_t work_bytes,
                           kp_stream_t stream) {
     const char *fn = "kp_gated_ffn_backward";

@@ -39,7 +39,8 @@ constexpr size_t kSmem = 113 * 1024;
 struct StreamParams {
     const uint8_t *sa, *sb, *sx;   // 4-bit: scale tiles
     int kt_n;                      // 128-column scale tiles per row tile
-    uint16_t *y, *g, *u;
+    uint16_t *y;
+    float *g, *u;   // optional: both products' sums, [M, N]
     int64_t ldy;
     float *ws;
     int *err;
@@ -286,13 +287,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (n + 3 < p.N) o[3] = static_cast<uint16_t>(hi >> 16);
                     }
                 };
+                auto put_sums = [&](float *dst, const float(&v)[4]) {
+                    float *o = dst + om * p.N + n;
+                    if (p.N % 4 == 0 && n + 4 <= p.N) {
+                        *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (n + i < p.N) o[i] = v[i];
+                    }
+                };
                 if constexpr (kGated) {
                     float h[4];
                     ffn_gate(va[d], vb[d], p.act, h);
                     put(p.y, p.ldy, h);
                     if (!kMx4 && p.g) {
-                        put(p.g, p.N, va[d]);
-                        put(p.u, p.N, vb[d]);
+                        put_sums(p.g, va[d]);
+                        put_sums(p.u, vb[d]);
                     }
                 } else {
                     put(p.y, p.ldy, va[d]);
@@ -405,8 +416,8 @@ cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s)
     p.sx = a.qx.scales;
     p.kt_n = static_cast<int>(mx4_ktiles(a.K));
     p.y = static_cast<uint16_t *>(a.y);
-    p.g = static_cast<uint16_t *>(a.g);
-    p.u = static_cast<uint16_t *>(a.u);
+    p.g = a.g;
+    p.u = a.u;
     p.ldy = a.ldy;
     p.ws = a.ws;
     p.err = a.err;
@@ -420,8 +431,7 @@ cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s)
     p.n_tiles = q.tiles;
     p.act = a.act;
     p.dtype = a.dtype;
-    // 8-byte stores: y's rows, and g and u's (stride N, 16-byte aligned bases)
-    p.vec4 = a.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && (!a.g || a.N % 4 == 0);
+    p.vec4 = a.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;   // 8-byte stores of y's rows
     p.idesc = a.mx4 ? idesc_mxf4(kRows, q.Mpad) : idesc_f16(a.dtype, kRows, q.Mpad);
     p.tmem_cols = q.tmem_cols;
     p.stage_bytes = q.stage_bytes;

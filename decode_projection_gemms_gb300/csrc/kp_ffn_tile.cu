@@ -52,7 +52,8 @@ struct TileMaps {
 };
 
 struct TileParams {
-    uint16_t *y0, *y1, *g, *u;
+    uint16_t *y0, *y1;
+    float *g, *u;
     int64_t ldy;
     float *ws;
     int *err;
@@ -60,7 +61,7 @@ struct TileParams {
     int tiles_m, tiles_n, items, splits;
     int KB1, KB;         // K blocks of the first product, of all
     int kt_n;            // 4-bit: scale tiles per row tile
-    int act, dtype, vec;
+    int act, dtype, vec, vec_gu;
     uint32_t idesc;
 };
 
@@ -133,6 +134,19 @@ __device__ __forceinline__ void put_row32(uint16_t *dst, const float (&v)[32], i
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             if (i < left) dst[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// 32 consecutive fp32 sums of one row.
+__device__ __forceinline__ void put_sums32(float *dst, const float (&v)[32], int left, int vec) {
+    if (vec && left >= 32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            reinterpret_cast<float4 *>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) dst[i] = v[i];
     }
 }
 
@@ -369,18 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) b[j] = __uint_as_float(v[2 + c][j]);
                     if (!kMx4 && p.g) {
-                        put_row32(p.g + m * p.N + n, a, left, p.vec, p.dtype);
-                        put_row32(p.u + m * p.N + n, b, left, p.vec, p.dtype);
+                        put_sums32(p.g + m * p.N + n, a, left, p.vec_gu);
+                        put_sums32(p.u + m * p.N + n, b, left, p.vec_gu);
                     }
                     ffn_gate(a, b, p.act, h);
                     put_row32(p.y0 + m * p.ldy + n, h, left, p.vec, p.dtype);
                 } else if (kForm == TILE_DX && p.splits > 1) {
-                    float *dst = p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)   // N is a multiple of 8
-                        if (4 * j < left)
-                            reinterpret_cast<float4 *>(dst)[j] =
-                                make_float4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+                    put_sums32(p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n, a, left, 1);
                 } else {
                     uint16_t *y = kForm == TILE_DW && it.z ? p.y1 : p.y0;
                     put_row32(y + m * p.ldy + n, a, left, p.vec, p.dtype);
@@ -466,8 +475,8 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     TileParams p = {};
     p.y0 = static_cast<uint16_t *>(a.y0);
     p.y1 = static_cast<uint16_t *>(a.y1);
-    p.g = static_cast<uint16_t *>(a.g);
-    p.u = static_cast<uint16_t *>(a.u);
+    p.g = a.g;
+    p.u = a.u;
     p.ldy = a.ldy;
     p.ws = a.ws;
     p.err = a.err;
@@ -485,12 +494,12 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     p.kt_n = static_cast<int>(mx4_ktiles(a.K));
     p.act = a.act;
     p.dtype = a.dtype;
-    // the widest store that every row's 32-column pieces allow: y's rows, and g and
-    // u's (stride N)
+    // the widest store that every row's 32-column pieces allow: of y, and of g and u
+    // (stride N, 16-byte aligned)
     const uintptr_t starts = reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1) |
-                             reinterpret_cast<uintptr_t>(a.g) | reinterpret_cast<uintptr_t>(a.u) |
-                             static_cast<uintptr_t>(a.ldy * 2) | (a.g ? static_cast<uintptr_t>(a.N) * 2 : 0);
+                             static_cast<uintptr_t>(a.ldy * 2);
     p.vec = starts % 32 == 0 ? 2 : starts % 16 == 0 ? 1 : 0;
+    p.vec_gu = a.N % 4 == 0;
     p.idesc = mx4 ? idesc_mxf4(256, 256)
                   : idesc_f16(a.dtype, 256, 256, a.form == TILE_DW, a.form == TILE_DW || a.form == TILE_DX);
 

@@ -389,11 +389,11 @@ KP_API int kp_mx4_gated_ffn(const void *x, int64_t ldx, const void *x_codes, con
 
 /* Gated block h[T, F] = round( act(x Wg^T) * (x Wu^T) ), x [T, K], Wg and Wu
  * [F, K], all of dtype KP_BF16 or KP_FP16; x, Wg and Wu 16-byte aligned with
- * row strides and K multiples of 8. g and u (both or neither; contiguous
- * [T, F], 16-byte aligned) receive the two products for the backward pass,
- * rounded to dtype as the tensor cores that read them there need it. */
+ * row strides and K multiples of 8. g and u (both or neither; contiguous fp32
+ * [T, F], 16-byte aligned) receive the sums of the two products for the backward
+ * pass. */
 KP_API int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg, const void *Wu,
-                        int64_t ldu, void *h, int64_t ldh, void *g, void *u, int T, int F, int K,
+                        int64_t ldu, void *h, int64_t ldh, float *g, float *u, int T, int F, int K,
                         int act, int dtype, void *work, size_t work_bytes, kp_stream_t stream);
 
 /* Its gradients, from dh [T, F], x and the weights (as above, the same values as
@@ -403,7 +403,7 @@ KP_API int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg,
  * dx, dWg and dWu are contiguous, 16-byte aligned and written, not added to; with
  * T = 0 the weights' gradients are set to zero. */
 KP_API int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx, const void *Wg,
-                                 int64_t ldg, const void *Wu, int64_t ldu, const void *g, const void *u,
+                                 int64_t ldg, const void *Wu, int64_t ldu, const float *g, const float *u,
                                  void *dx, void *dWg, void *dWu, int T, int F, int K, int act, int dtype,
                                  void *work, size_t work_bytes, kp_stream_t stream);
 

@@ -86,12 +86,10 @@ def gated(x, Wg, Wu, name):
 
 def gated_grads(dh, x, Wg, Wu, name, unit):
     """{name: (gradient, bound on its error before its own rounding)} of the gated
-    block. g and u reach the backward pass rounded to 16 bits (`unit`), and dG and
-    dU are rounded again as operands; both errors are carried through."""
+    block. g and u reach the backward pass in fp32; dG and dU are rounded to 16 bits
+    (`unit`) as operands, and that error is carried through."""
     g, eg = product_bounds(x, Wg)
     u, eu = product_bounds(x, Wu)
-    eg = eg + unit * (g.abs() + eg)
-    eu = eu + unit * (u.abs() + eu)
     a, da = act(g, name)
     dg, du = dh * u * da, dh * a
     d = dh.abs()

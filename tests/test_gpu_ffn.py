@@ -168,8 +168,8 @@ def test_gated_ffn(T, F, K, dtype):
     h, g, u = kda.gated_ffn(x, Wg, Wu, act=act, save=True)
     rh, eh, rg, eg, ru, eu = gated(x.double(), Wg.double(), Wu.double(), act)
     close(h, rh, eh, "h")
-    close(g, rg, eg, "g")
-    close(u, ru, eu, "u")
+    assert g.dtype is torch.float32 and ((g.double() - rg).abs() <= eg).all()
+    assert u.dtype is torch.float32 and ((u.double() - ru).abs() <= eu).all()
     assert torch.equal(kda.gated_ffn(x, Wg, Wu, act=act), h)
     quiet()
 
