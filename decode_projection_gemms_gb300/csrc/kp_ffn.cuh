@@ -80,7 +80,7 @@ struct FfnArgs {
 };
 // Few tokens: weight streaming, split-K over a cluster (kp_ffn_stream.cu).
 size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms);   // bytes
-float ffn_stream_us(bool gated, int M, int N, int K, int sms);   // estimate of a 4-bit product's time
+float ffn_stream_us(bool mx4, bool gated, int M, int N, int K, int sms);   // estimate of its time
 cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s);
 
 // One launch of the tile kernel (kp_ffn_tile.cu), for many tokens and for the

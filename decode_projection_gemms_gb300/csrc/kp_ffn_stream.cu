@@ -373,15 +373,16 @@ std::map<int, bool> g_ready;   // devices whose kernels have their shared memory
 
 }  // namespace
 
-// Least-squares fit of 480 measured 4-bit products (16 <= M <= 1536, 256 <= N <=
-// 4096, 512 <= K <= 7168), off by 5 to 8 % on average: rounds of CTAs over the SMs,
-// each with its K blocks and its share of the tokens' sums.
-float ffn_stream_us(bool gated, int M, int N, int K, int sms) {
-    const Plan q = make_plan(true, gated, M, N, K, sms);
+// Least-squares fits of 720 measured products (16 <= M <= 1536, 256 <= N <= 4096,
+// 512 <= K <= 7168), off by 5 to 13 % on average: rounds of CTAs over the SMs, each
+// with its K blocks and its share of the tokens' sums.
+float ffn_stream_us(bool mx4, bool gated, int M, int N, int K, int sms) {
+    const Plan q = make_plan(mx4, gated, M, N, K, sms);
     const float tok = static_cast<float>(q.Mpad) / kMaxTok;
-    const int per_sm = gated && q.Mpad > 64 ? 1 : 2;   // TMEM: scales and two accumulators
+    const int per_sm = mx4 && gated && q.Mpad > 64 ? 1 : 2;   // TMEM: scales and two accumulators
     const float r = static_cast<float>((static_cast<int64_t>(q.tiles) * q.mt * q.C + sms * per_sm - 1) / (sms * per_sm));
     const float kb = static_cast<float>((q.KB + q.C - 1) / q.C);
+    if (!mx4) return 4.5f + r * (-0.2f + 0.38f * kb + tok * (2.6f + 2.f / q.C));
     return gated ? 2.3f + r * (1.4f + 0.48f * kb + tok * (5.4f + 1.2f / q.C))
                  : -5.f + r * (8.7f + 0.38f * kb + tok * (2.6f + 0.8f / q.C));
 }

@@ -2,8 +2,8 @@
 // fp32 accumulation, for many tokens (forward) and for the backward pass, where
 // the tensor cores are the bound.
 //
-// Two CTAs of a cluster (an SM pair) compute one 256 x 256 tile with
-// tcgen05.mma.cta_group::2: each holds 128 rows of A, half of B's 256 rows, and
+// Two CTAs of a cluster (an SM pair) compute one 256 x nt tile (nt up to 256) with
+// tcgen05.mma.cta_group::2: each holds 128 rows of A, half of B's nt rows, and
 // the accumulator rows of its own A, so an operand byte in shared memory feeds
 // twice the products that it would in a tile of one CTA. The leader's warp 1
 // issues every MMA; both CTAs' copies complete on the leader's barriers, and
@@ -12,9 +12,9 @@
 // keeps a band of row tiles together so that their operands stay in L2.
 //
 // Forms:
-//   gated    B's halves are 128 rows of Wg (CTA 0) and the same 128 of Wu (CTA
+//   gated    B's halves are nt/2 rows of Wg (CTA 0) and the same ones of Wu (CTA
 //            1): a thread of the epilogue finds the gate in accumulator column c
-//            and its factor in column 128 + c;
+//            and its factor in column nt/2 + c;
 //   dx       two products into one accumulator (dG Wg, then dU Wu), Wg and Wu
 //            read as they lie, N contiguous (the MMA's transposed operand). With
 //            few tokens the contraction is split over clusters, whose fp32
@@ -37,13 +37,14 @@ namespace kp {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kTile = 256;                // rows of D per cluster; columns too
+constexpr int kTile = 256;                // rows of D per cluster; columns at most
 constexpr uint32_t kHalf = 128 * 128;     // bytes of 128 rows of a K block (128 bytes of K)
 constexpr int kBand = 16;                 // row tiles kept together in the tile order (8: backward 1.5 % slower)
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kBarBytes = 256;
 
-// Operand halves and, in 4 bits, three pairs of scale tiles; as many as fit.
+// Operand halves and, in 4 bits, pairs of scale tiles (one of A, up to two of B); as
+// many stages as fit.
 constexpr uint32_t stage_bytes(bool mx4) { return 2 * kHalf + (mx4 ? 3 * 1024 : 0); }
 constexpr int stages(bool mx4) { return static_cast<int>((kMaxSmem - 1024 - kBarBytes) / stage_bytes(mx4)); }
 
@@ -59,6 +60,7 @@ struct TileParams {
     int *err;
     int M, N, K;
     int tiles_m, tiles_n, items, splits;
+    int nt;              // accumulator columns of a tile (gated: of both products)
     int KB1, KB;         // K blocks of the first product, of all
     int kt_n;            // 4-bit: scale tiles per row tile
     int act, dtype, vec, vec_gu;
@@ -114,39 +116,43 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
     return elem_round(a, dtype) | static_cast<uint32_t>(elem_round(b, dtype)) << 16;
 }
 
-// 32 consecutive outputs of one row, in stores of 32 bytes (vec 2), 16 (1) or 2.
+// Up to 32 consecutive outputs of one row, in stores of 32 bytes (vec 2), 16 (1) or
+// 2.
 __device__ __forceinline__ void put_row32(uint16_t *dst, const float (&v)[32], int left, int vec, int dtype) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], dtype);
-    if (vec == 2 && left >= 32) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * i), "r"(w[8 * i]),
-                         "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]),
-                         "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+    for (int i = 0; i < 2; ++i) {
+        const int more = left - 16 * i;
+        const uint32_t *x = w + 8 * i;
+        uint16_t *d = dst + 16 * i;
+        if (vec == 2 && more >= 16) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(x[0]), "r"(x[1]),
+                         "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                          : "memory");
-    } else if (vec && left >= 32) {
+        } else if (vec && more >= 16) {
+            reinterpret_cast<uint4 *>(d)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<uint4 *>(d)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < left) dst[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+            for (int k = 0; k < 16; ++k)
+                if (k < more) d[k] = static_cast<uint16_t>(x[k / 2] >> (16 * (k & 1)));
+        }
     }
 }
 
-// 32 consecutive fp32 sums of one row.
+// Up to 32 consecutive fp32 sums of one row.
 __device__ __forceinline__ void put_sums32(float *dst, const float (&v)[32], int left, int vec) {
-    if (vec && left >= 32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+        if (vec && 4 * i + 4 <= left) {
             reinterpret_cast<float4 *>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
+        } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < left) dst[i] = v[i];
+            for (int k = 0; k < 4; ++k)
+                if (4 * i + k < left) dst[4 * i + k] = v[4 * i + k];
+        }
     }
 }
 
@@ -161,8 +167,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     constexpr int kStages = stages(kMx4);
     constexpr int kAccs = kMx4 ? 1 : 2;
     constexpr int kCols = kMx4 ? 128 : 64;      // map columns per K block, K-major operands
-    constexpr int kNt = kGated ? 128 : 256;     // outputs of a tile along N
     constexpr uint32_t kSfCol = 256, kSfStage = 24;   // 4-bit: scale columns (A 8, B 16 a stage)
+    const int half_n = p.nt / 2;                      // rows of B per CTA
+    const int out_n = kGated ? half_n : p.nt;         // outputs of a tile along N
+    const int sb_tiles = kGated ? 2 : p.nt >> 7;      // 4 bits: row tiles of B's scales
+    const uint32_t tx = 2 * (kHalf + static_cast<uint32_t>(half_n) * 128 + (kMx4 ? 1024u * (1 + sb_tiles) : 0u));
 
     extern __shared__ uint8_t ft_smem_raw[];
     const uint32_t raw = smem_u32(ft_smem_raw);
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int r = i - band * kBand * p.tiles_n;
         const int h = min(kBand, p.tiles_m - band * kBand);
         it.m0 = (band * kBand + r % h) * kTile;
-        it.n0 = r / h * kNt;
+        it.n0 = r / h * out_n;
         it.kb0 = static_cast<int>(static_cast<long long>(p.KB) * it.split / p.splits);
         it.kb1 = static_cast<int>(static_cast<long long>(p.KB) * (it.split + 1) / p.splits);
         return it;
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
                     const uint32_t st = base + stage * kStage;
                     const uint32_t bar = full0 + 8 * stage;
-                    if (rank == 0 && mine) mbar_expect_tx(smem_u32(full + stage), 2 * kStage);
+                    if (rank == 0 && mine) mbar_expect_tx(smem_u32(full + stage), tx);
                     if (++stage == kStages) stage = 0, phase ^= 1;
                     if (!mine) continue;
                     const bool second = kForm == TILE_DX && kb >= p.KB1;
@@ -254,23 +263,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         pair_load(st, ma, bar, k * kCols, m);
                     }
                     const CUtensorMap *mb = (kGated && rank) || second ? &tm.b1 : &tm.b0;
-                    const int n = it.n0 + (kGated ? 0 : rank * 128);
+                    const int n = it.n0 + (kGated ? 0 : rank * half_n);
                     if constexpr (kBMn) {
                         pair_load(st + kHalf, mb, bar, n, k * 64);
-                        pair_load(st + kHalf + 8192, mb, bar, n + 64, k * 64);
+                        if (half_n > 64) pair_load(st + kHalf + 8192, mb, bar, n + 64, k * 64);
                     } else {
                         pair_load(st + kHalf, mb, bar, k * kCols, n);
                     }
                     if constexpr (kMx4) {
-                        // the scales of this CTA's A rows and of all 256 B rows
+                        // the scales of this CTA's A rows and of all of B's rows
                         const uint32_t sc = st + 2 * kHalf;
                         pair_load(sc, &tm.sa, bar, 0, (m >> 7) * p.kt_n + 2 * k);
                         const int nt = it.n0 >> 7;
-                        pair_load(sc + 1024, &tm.sb0, bar, 0, nt * p.kt_n + 2 * k);
-                        if constexpr (kGated)
-                            pair_load(sc + 2048, &tm.sb1, bar, 0, nt * p.kt_n + 2 * k);
-                        else
-                            pair_load(sc + 2048, &tm.sb0, bar, 0, (nt + 1) * p.kt_n + 2 * k);
+                        for (int t = 0; t < sb_tiles; ++t)
+                            pair_load(sc + 1024 * (1 + t), kGated && t ? &tm.sb1 : &tm.sb0, bar, 0,
+                                      (kGated ? nt : nt + t) * p.kt_n + 2 * k);
                     }
                 }
             }
@@ -296,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 mbar_wait_bounded(smem_u32(full + s), ph, abort_flag, p.err, DEV_TIMEOUT_FULL);
                 tc_fence_after();
                 if constexpr (kMx4) {
-                    // columns: A's tiles 0 and 1 of the block, then for each B's two row tiles
+                    // columns of a stage, four a tile: A's tiles 0 and 1 of the block, then
+                    // for either B's row tiles
                     const uint32_t sf = tmem + kSfCol + static_cast<uint32_t>(s) * kSfStage;
                     const uint64_t sc = desc_scales(base + s * kStage + 2 * kHalf);
 #pragma unroll
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         if (!mine) break;
                         pair_cp_scales(sf + 4 * j, sc + 32 * j);
                         pair_cp_scales(sf + 8 + 8 * j, sc + 64 + 32 * j);
-                        pair_cp_scales(sf + 12 + 8 * j, sc + 128 + 32 * j);
+                        if (sb_tiles > 1) pair_cp_scales(sf + 12 + 8 * j, sc + 128 + 32 * j);
                     }
                 }
             };
@@ -352,17 +360,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // the accumulator back before it computes or stores anything.
         const int q = warp & 3;
         const int half = warp >= 6;
-        constexpr int kSpan = kNt / 2;   // outputs of a thread: 128, gated 64 (from 64 + 64 sums)
+        const int span = (out_n / 2 + 31) & ~31;   // outputs of the first half
         int as = 0;
         uint32_t aphase = 0;
         for (int i = cid; i < p.items; i += nclu) {
             const Item it = item_at(i);
             mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
             tc_fence_after();
-            const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * kSpan;
+            const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * span;
             uint32_t v[4][32];   // gated: 0 and 1 the gates, 2 and 3 their factors
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(t + (kGated && c >= 2 ? 64 : 0) + 32 * c, v[c]);
+            for (int c = 0; c < 4; ++c) tmem_ld32(t + (kGated && c >= 2 ? half_n - 64 : 0) + 32 * c, v[c]);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
@@ -371,9 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const int64_t m = it.m0 + rank * 128 + q * 32 + lane;
             if (m >= p.M) continue;
 #pragma unroll
-            for (int c = 0; c < kSpan / 32; ++c) {
-                const int n = it.n0 + half * kSpan + 32 * c;
-                const int left = p.N - n;
+            for (int c = 0; c < (kGated ? 2 : 4); ++c) {
+                const int at = half * span + 32 * c;   // within the tile
+                const int n = it.n0 + at;
+                const int left = min(p.N - n, (half ? out_n : span) - at);
                 if (left <= 0) break;
                 float a[32];
 #pragma unroll
@@ -422,10 +431,29 @@ __global__ void __launch_bounds__(256) join_kernel(const float *ws, int64_t n, i
 
 int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
+// Accumulator columns of a tile: those whose rounds of tiles over the SM pairs cost
+// least, a tile costing its columns' K blocks and about six K blocks of fixed work.
+// 4-bit tiles start at whole scale tiles of 128 rows (a gated one holds one of each
+// weight): the MMA reads B's scales from a multiple of four TMEM columns. B with N
+// contiguous comes in boxes of 64. Gated 4003 x 2048 x 7168 (256 tiles of 256 columns
+// on 76 SM pairs, or 304 of 224): 141 us with 256 columns, 130 with 224.
+int tile_columns(int form, int64_t M, int64_t N, int KB, int sms) {
+    const bool gated = form == TILE_GATED || form == TILE_MX4_GATED;
+    const int step = form == TILE_GATED ? 32 : form == TILE_MX4_GATED ? 256 : 128;
+    int best = 256;
+    int64_t least = -1;
+    for (int nt = 256; nt >= (step > 64 ? step : 64); nt -= step) {
+        const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, gated ? nt / 2 : nt) * (form == TILE_DW ? 2 : 1);
+        const int64_t cost = (tiles + sms / 2 - 1) / (sms / 2) * (static_cast<int64_t>(nt) * KB + 256 * 6);
+        if (least < 0 || cost < least) least = cost, best = nt;
+    }
+    return best;
+}
+
 // K splits of dx: enough that every SM pair has work, each with at least
 // eight K blocks (a partial tile costs about as much as four to write and add).
-int dx_splits(int M, int N, int KB, int sms) {
-    const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, kTile);
+int dx_splits(int M, int N, int nt, int KB, int sms) {
+    const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, nt);
     int s = 1;
     while (tiles * (s + 1) <= sms / 2 && KB / (s + 1) >= 8) ++s;
     return s;
@@ -436,22 +464,25 @@ std::map<int, bool> g_ready;
 
 }  // namespace
 
-// 16 bits: from a quarter of the SM pairs' worth of tiles on (K = 4096, F = 4096: T =
-// 256 25 us either way, T = 384 27 against 31, T = 1024 47 against 64; over 240
-// measured sizes 0.4 % slower than the better of the two each time). 4 bits, where
-// both kernels' fixed costs weigh more: by estimates of both, 1.5 % and 0.5 % (gated)
-// slower than the better one over 240 sizes each.
+// By estimates of both kernels' times, from rounds of 256-column tiles and K blocks
+// for this one. Over the 720 sizes that they were fitted to the choice is 0.8 % (16
+// bits), 0.6 % (4 bits) and 0.5 % (4 bits, gated) slower than the better of the two;
+// each is up to 2.5 times as fast as the other (4 bits, K = 7168: 64 x 256 6.6 us
+// streamed, 16 in tiles; 1024 x 4096 30 against 17).
 bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms) {
     const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, gated ? 128 : 256);
-    if (!mx4) return 4 * tiles >= sms;
     const float waves = static_cast<float>((tiles + sms / 2 - 1) / (sms / 2));
-    const float us = 5.2f + waves * (2.f + 0.34f * static_cast<float>(cdiv(K, 256)));
-    return us < ffn_stream_us(gated, M, N, K, sms);
+    const float kb = static_cast<float>(cdiv(K, mx4 ? 256 : 64));
+    const float us = !mx4    ? 3.7f + waves * (2.7f + 0.21f * kb)
+                     : gated ? 5.3f + waves * (2.1f + 0.34f * kb)
+                             : 2.4f + waves * (3.7f + 0.34f * kb);
+    return us < ffn_stream_us(mx4, gated, M, N, K, sms);
 }
 
 size_t ffn_tile_scratch(int form, int M, int N, int K, int sms) {
     if (form != TILE_DX) return 0;
-    const int s = dx_splits(M, N, 2 * cdiv(K, 64), sms);
+    const int KB = 2 * cdiv(K, 64);
+    const int s = dx_splits(M, N, tile_columns(form, M, N, KB, sms), KB, sms);
     return s > 1 ? static_cast<size_t>(s) * M * N * sizeof(float) : 0;
 }
 
@@ -483,11 +514,12 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     p.M = a.M;
     p.N = a.N;
     p.K = a.K;
-    p.tiles_m = cdiv(a.M, kTile);
-    p.tiles_n = cdiv(a.N, gated ? 128 : 256);
     p.KB1 = mx4 ? cdiv(a.K, 256) : cdiv(a.K, 64);
     p.KB = a.form == TILE_DX ? 2 * p.KB1 : p.KB1;
-    p.splits = a.form == TILE_DX ? dx_splits(a.M, a.N, p.KB, d.sms) : 1;
+    p.nt = tile_columns(a.form, a.M, a.N, p.KB, d.sms);
+    p.tiles_m = cdiv(a.M, kTile);
+    p.tiles_n = cdiv(a.N, gated ? p.nt / 2 : p.nt);
+    p.splits = a.form == TILE_DX ? dx_splits(a.M, a.N, p.nt, p.KB, d.sms) : 1;
     const int64_t items = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits * (a.form == TILE_DW ? 2 : 1);
     if (items > 0x7FFFFFFF || (p.splits > 1 && !a.ws)) return cudaErrorInvalidValue;
     p.items = static_cast<int>(items);
@@ -500,8 +532,8 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
                              static_cast<uintptr_t>(a.ldy * 2);
     p.vec = starts % 32 == 0 ? 2 : starts % 16 == 0 ? 1 : 0;
     p.vec_gu = a.N % 4 == 0;
-    p.idesc = mx4 ? idesc_mxf4(256, 256)
-                  : idesc_f16(a.dtype, 256, 256, a.form == TILE_DW, a.form == TILE_DW || a.form == TILE_DX);
+    p.idesc = mx4 ? idesc_mxf4(256, p.nt)
+                  : idesc_f16(a.dtype, 256, p.nt, a.form == TILE_DW, a.form == TILE_DW || a.form == TILE_DX);
 
     TileMaps tm = {};
     auto map = [&](CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows, int box_cols,
@@ -511,8 +543,8 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     if (mx4) {
         const int64_t pitch = mx4_pitch(a.K);
         map(&tm.a0, a.qa.codes, a.M, pitch, pitch, 128, 128, kMapU8);
-        map(&tm.b0, a.qb0.codes, a.N, pitch, pitch, 128, 128, kMapU8);
-        if (gated) map(&tm.b1, a.qb1.codes, a.N, pitch, pitch, 128, 128, kMapU8);
+        map(&tm.b0, a.qb0.codes, a.N, pitch, pitch, p.nt / 2, 128, kMapU8);
+        if (gated) map(&tm.b1, a.qb1.codes, a.N, pitch, pitch, p.nt / 2, 128, kMapU8);
         auto scales = [&](CUtensorMap *m, const Mx4Mat &q, int rows) {
             if (e == cudaSuccess)
                 e = ffn_scale_map(m, q.scales, static_cast<int64_t>(cdiv(rows, 128)) * p.kt_n);
@@ -522,8 +554,8 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
         if (gated) scales(&tm.sb1, a.qb1, a.N);
     } else if (a.form == TILE_GATED) {
         map(&tm.a0, a.A0, a.M, a.K, a.lda, 128, 64, a.dtype);
-        map(&tm.b0, a.B0, a.N, a.K, a.ldb0, 128, 64, a.dtype);
-        map(&tm.b1, a.B1, a.N, a.K, a.ldb1, 128, 64, a.dtype);
+        map(&tm.b0, a.B0, a.N, a.K, a.ldb0, p.nt / 2, 64, a.dtype);
+        map(&tm.b1, a.B1, a.N, a.K, a.ldb1, p.nt / 2, 64, a.dtype);
     } else if (a.form == TILE_DX) {
         map(&tm.a0, a.A0, a.M, a.K, a.lda, 128, 64, a.dtype);
         map(&tm.a1, a.A1, a.M, a.K, a.lda, 128, 64, a.dtype);
