@@ -39,7 +39,7 @@ SOURCES = [
     "kp_ffn_bwd.cu",
     "kp_ffn_api.cu",
 ]
-HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh", "kp_ffn.cuh"]
+HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh", "kp_ffn.cuh", "kp_mx4.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

@@ -65,7 +65,7 @@ struct FfnArgs {
     bool gated = false;
     int act = 0;                 // enum kp_act
     int dtype = KP_BF16;         // x and W (16-bit), y, g, u
-    const void *x = nullptr;     // 16-bit: [M, ldx]
+    const void *x = nullptr;     // 16 bits: [M, ldx] (microscaled products: then quantised within)
     int64_t ldx = 0;
     const void *Wa = nullptr, *Wb = nullptr;   // 16-bit: [N, lda / ldb]
     int64_t lda = 0, ldb = 0;
@@ -80,6 +80,7 @@ struct FfnArgs {
 };
 // Few tokens: weight streaming, split-K over a cluster (kp_ffn_stream.cu).
 size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms);   // bytes
+bool ffn_stream_quantises(int M);   // whether its 4-bit forms take x in 16 bits
 float ffn_stream_us(bool mx4, bool gated, int M, int N, int K, int sms);   // estimate of its time
 cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s);
 

@@ -165,12 +165,19 @@ static cudaError_t forward_launch(const FfnArgs &a, const FfnDev &d, cudaStream_
     return ffn_tile_launch(t, d, s);
 }
 
-// 4-bit products: x's codes, x's scales, split-K partial tiles.
+// Whether a 4-bit product quantises x within its own launch.
+static bool quantises_within(bool gated, int M, int N, int K, int sms) {
+    return ffn_stream_quantises(M) && !ffn_use_tile(true, gated, M, N, K, sms);
+}
+
+// 4-bit products: x's codes, x's scales, split-K partial tiles; nothing where x is
+// quantised within.
 struct Mx4Work {
     size_t scales, part, bytes;
 };
 static Mx4Work mx4_work(bool gated, int M, int N, int K, int sms) {
-    Mx4Work w;
+    Mx4Work w = {};
+    if (quantises_within(gated, M, N, K, sms)) return w;
     w.scales = up256(mx4_code_bytes(M, K));
     w.part = w.scales + up256(mx4_scale_bytes(M, K));
     w.bytes = w.part + forward_scratch(true, gated, M, N, K, sms);
@@ -223,7 +230,10 @@ static int mx4_product(const char *fn, FfnArgs a, const void *x, int64_t ldx, co
     a.err = d.err;
     a.ws = reinterpret_cast<float *>(base + w.part);
     cudaError_t e;
-    if (x) {
+    if (x && quantises_within(a.gated, a.M, a.N, a.K, d.sms)) {
+        a.x = x;
+        a.ldx = ldx;
+    } else if (x) {
         // quantised on its way in; the product is launched behind it and
         // streams its weights meanwhile
         e = mx4_quantize_launch(x, ldx, a.M, a.K, a.dtype, base, base + w.scales, false, d.sms, s);

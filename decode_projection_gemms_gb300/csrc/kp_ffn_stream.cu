@@ -7,19 +7,24 @@
 // tile, further tiles along the grid's y axis read the weights from L2). The
 // 16-bit gated form has 64 rows of Wg and the same 64 of Wu in one MMA, the 4-bit
 // one 128 of each in two accumulators. A feature tile's K range is split over the
-// C CTAs of a cluster; their fp32 partial tiles go through L2 and the cluster sums
-// them in rank order, so the result does not depend on timing; the sums of a gate
+// C CTAs of a cluster; their fp32 partial tiles go through L2, or up to 8 tokens
+// through distributed shared memory, and the cluster sums them in rank order, so the result does not depend on timing; the sums of a gate
 // and of its factor meet in one thread there. A K block is 128 bytes of a row (64 16-bit or 256
 // 4-bit columns), 8 or 16 KB TMA boxes; a 4-bit stage also brings its
 // scale tiles, which tcgen05.cp lays into the stage's own TMEM columns (their
 // last readers finished before the stage was refilled).
 //
-// Warp 0: copies; warp 1: TMEM and MMA; warps 2 .. 5: epilogue; all six reduce.
+// Up to 8 tokens the 4-bit forms also quantise x themselves: of each stage one warp
+// turns the 256 columns of every token into the operand and scale tile that a copy
+// would have brought (T = 1, N = 4096, K = 7168: ONELAUNCH).
+//
+// Warp 0: copies; warp 1: TMEM and MMA; warps 2 .. 5: x in 4 bits (few tokens),
+// epilogue; all six reduce.
 #include <algorithm>
 #include <map>
 #include <mutex>
 
-#include "kp_ffn.cuh"
+#include "kp_mx4.cuh"
 
 namespace kp {
 
@@ -29,6 +34,7 @@ constexpr int kThreads = 192;
 constexpr int kRows = 128;                 // rows of an MMA
 constexpr int kMaxTok = 128;               // tokens per tile
 constexpr int kMaxStages = 10;
+constexpr int kFewTok = 8;                 // tokens up to which a call needs no workspace
 constexpr size_t kBarBytes = 256;
 constexpr size_t kMaxSmem = 227 * 1024;
 // What a CTA takes for its stages: half an SM, so that clusters of eight fill the
@@ -42,8 +48,12 @@ struct StreamParams {
     uint16_t *y;
     float *g, *u;   // optional: both products' sums, [M, N]
     int64_t ldy;
-    float *ws;
+    float *ws;                     // partial tiles; few tokens: shared memory instead
+    const void *x;                 // 4-bit, few tokens: x in 16 bits, quantised here
+    int64_t ldx;
+    int x_vec;                     // its rows start on 16 bytes
     int *err;
+    int few;                       // partial tiles stay in shared memory
     int M, N, K, Mpad, KB, C, stages, n_tiles, act, dtype, vec4;
     uint32_t idesc, tmem_cols, stage_bytes, sf_col;
 };
@@ -93,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pre = n_st < S ? n_st : S;
     const uint32_t xbytes = static_cast<uint32_t>(p.Mpad) * 128;
     constexpr int kCols = kMx4 ? 128 : 64;   // map columns (bytes or elements) per K block
+    const bool quantises = kMx4 && p.x != nullptr;
 
     // scale tiles that exist of K block kb (two but at the end of K)
     auto sc_tiles = [&](int kb) { return min(2, p.kt_n - 2 * kb); };
@@ -102,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t st = base + stage * p.stage_bytes;
         const uint32_t bar = smem_u32(full + stage);
         const uint32_t scb = kMx4 ? 512u * static_cast<uint32_t>(sc_tiles(kb)) : 0u;
-        mbar_expect_tx(bar, L::w_bytes + xbytes + scb * (kAcc + 1));
+        mbar_expect_tx(bar, L::w_bytes + scb * kAcc + (quantises ? 0u : xbytes + scb));
         tma_load_2d(st, &tma, bar, kb * kCols, tile * L::feat, pol);
         if constexpr (kGated) tma_load_2d(st + L::w_bytes / 2, &tmb, bar, kb * kCols, tile * L::feat, pol);
         if constexpr (kMx4) {
@@ -126,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(full + s), 1);
+            mbar_init(smem_u32(full + s), quantises ? 2 : 1);   // the copies, the quantising warp
             mbar_init(smem_u32(empty + s), 1);
         }
         mbar_init(smem_u32(accf), 1);
@@ -147,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         const bool mine = elect_one();
         pdl_wait();   // x (quantised by the kernel before, when there is one)
-        if (mine)
+        if (mine && !quantises)
             for (int s = 0; s < pre; ++s) issue_x(s, s);
         int stage = 0;
         uint32_t phase = 0;
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
             if (mine) {
                 issue_w(s, stage);
-                issue_x(s, stage);
+                if (!quantises) issue_x(s, stage);
             }
             if (++stage == S) stage = 0, phase ^= 1;
         }
@@ -206,17 +217,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine) umma_commit(smem_u32(accf));
         __syncwarp();
     } else {
+        if constexpr (kMx4) {
+            if (quantises) {
+                auto run = [&](auto zero) {
+                    using T = decltype(zero);
+                    // A buffer belongs to one warp, which sees all of its rounds: it is
+                    // never two phases behind the barrier that it waits on.
+                    for (int s = 0; s < n_st; ++s) {
+                        const int stage = s % S;
+                        if ((stage & 3) != warp - 2) continue;
+                        if (s >= S)
+                            mbar_wait_bounded(smem_u32(empty + stage), static_cast<uint32_t>((s / S - 1) & 1), abort_flag,
+                                              p.err, DEV_TIMEOUT_EMPTY);
+                        const int c = (kb0 + s) * 256 + lane * 8;
+                        Eight<T> e[kFewTok];
+#pragma unroll
+                        for (int r = 0; r < kFewTok; ++r) {
+                            const T *row = static_cast<const T *>(p.x) + (m0 + min(r, Mloc - 1)) * p.ldx;
+                            if (p.x_vec && c + 8 <= p.K)
+                                e[r].load_full(row + c);
+                            else
+                                e[r].load(row, c, p.K);
+                        }
+                        uint8_t *x8 = gbase + static_cast<size_t>(stage) * p.stage_bytes + L::w_bytes;
+                        uint8_t *sc = gbase + static_cast<size_t>(stage) * p.stage_bytes + L::off_sc(p.Mpad) + kAcc * 1024;
+#pragma unroll
+                        for (int r = 0; r < kFewTok; ++r) {
+                            if (r >= Mloc) break;
+                            uint32_t b;
+                            const uint32_t q = quantize8(e[r], b);
+                            // row r of the 128-byte swizzled operand, lane r of the scale tile
+                            *reinterpret_cast<uint32_t *>(x8 + r * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4) = q;
+                            if ((lane & 3) == 0)
+                                sc[(lane >> 4) * 512 + r * 16 + ((lane >> 2) & 3)] = static_cast<uint8_t>(b);
+                        }
+                        // the tensor cores read it through the asynchronous proxy
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(full + stage));
+                    }
+                };
+                if (p.dtype == KP_FP16)
+                    run(__half());
+                else
+                    run(__nv_bfloat16());
+            }
+        }
         // accumulators -> this CTA's partial tile [token][kPart], 128 bytes a warp
-        // and token: in L2, or with one CTA in the stage memory, which is free
-        // once the last MMA has completed
+        // and token: in L2, or for few tokens or one CTA in the stage memory, which
+        // is free once the last MMA has completed
         const int q = warp & 3;
         const int row = q * 32 + lane;
         mbar_wait_bounded(smem_u32(accf), 0, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
         tc_fence_after();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        float *part = C > 1 ? p.ws + ((static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C + rank) *
-                                         static_cast<size_t>(kPart) * p.Mpad
-                            : reinterpret_cast<float *>(gbase);
+        float *part = p.few ? reinterpret_cast<float *>(gbase)
+                            : p.ws + ((static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C + rank) *
+                                         static_cast<size_t>(kPart) * p.Mpad;
         for (int c0 = 0; c0 < Mloc; c0 += 16) {
             uint32_t v[kAcc][16];
 #pragma unroll
@@ -240,8 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
     {
         const size_t stride = static_cast<size_t>(kPart) * p.Mpad;
-        const float *parts = C > 1 ? p.ws + (static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C * stride
-                                   : reinterpret_cast<const float *>(gbase);
+        const float *parts = p.ws + (static_cast<size_t>(blockIdx.y) * p.n_tiles + tile) * C * stride;
         // A lane takes four features of a token, CTA r of the cluster every C-th
         // group of tokens, kDeep groups at a time so that their sums are read
         // together.
@@ -256,19 +312,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int d = 0; d < kDeep; ++d)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) va[d][i] = vb[d][i] = 0.f;
-            auto add = [&](const float *at, float(&v)[4]) {
-                const float4 a = C > 1 ? __ldcg(reinterpret_cast<const float4 *>(at)) : *reinterpret_cast<const float4 *>(at);
-                v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-            };
+            auto add = [](const float4 a, float(&v)[4]) { v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w; };
 #pragma unroll 4
             for (int r = 0; r < C; ++r)   // in rank order
 #pragma unroll
                 for (int d = 0; d < kDeep; ++d) {
                     // past the end: the last token again, so that no branch parts the loads
-                    const int m = min(mb + d * kTok * C, Mloc - 1);
-                    const float *src = parts + r * stride + static_cast<size_t>(m) * kPart + f;
-                    add(src, va[d]);
-                    if constexpr (kGated) add(src + L::feat, vb[d]);
+                    const int at = min(mb + d * kTok * C, Mloc - 1) * kPart + f;
+                    if (p.few) {
+                        const uint32_t src = mapa_shared(base, static_cast<uint32_t>(r)) + 4u * static_cast<uint32_t>(at);
+                        add(ld_dsmem_f4(src), va[d]);
+                        if constexpr (kGated) add(ld_dsmem_f4(src + 4u * L::feat), vb[d]);
+                    } else {
+                        const float4 *src = reinterpret_cast<const float4 *>(parts + r * stride + at);
+                        add(__ldcg(src), va[d]);
+                        if constexpr (kGated) add(__ldcg(src + L::feat / 4), vb[d]);
+                    }
                 }
 #pragma unroll
             for (int d = 0; d < kDeep; ++d) {
@@ -311,6 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    __syncwarp();
+    if (C > 1 && p.few) cluster_sync_all();   // the peers have read this CTA's partial tile
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -322,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct Plan {
     int Mpad, mt, tiles, KB, C, stages;
     int acc, feat;
+    bool few;   // partial tiles in shared memory
     uint32_t stage_bytes, sf_cols, tmem_cols;
 };
 
@@ -359,8 +421,9 @@ Plan make_plan(bool mx4, bool gated, int M, int N, int K, int sms) {
     st = std::min(st, kMaxStages);
     if (mx4) st = std::min(st, static_cast<int>((512 - acc) / q.sf_cols));
     st = std::min(st, (q.KB + q.C - 1) / q.C);
-    // one CTA: its partial tile needs the stage memory
-    if (q.C == 1)
+    // partial tiles in the stage memory
+    q.few = q.C == 1 || M <= kFewTok;
+    if (q.few)
         st = std::max<int>(st, (static_cast<size_t>(q.acc) * kRows * 4 * q.Mpad + q.stage_bytes - 1) / q.stage_bytes);
     q.stages = st;
     q.tmem_cols = 32;
@@ -387,15 +450,19 @@ float ffn_stream_us(bool mx4, bool gated, int M, int N, int K, int sms) {
                  : -5.f + r * (8.7f + 0.38f * kb + tok * (2.6f + 0.8f / q.C));
 }
 
+bool ffn_stream_quantises(int M) { return M <= kFewTok; }
+
 size_t ffn_stream_scratch(bool mx4, bool gated, int M, int N, int K, int sms) {
     const Plan q = make_plan(mx4, gated, M, N, K, sms);
-    if (q.C == 1) return 0;
+    if (q.few) return 0;
     return static_cast<size_t>(q.mt) * q.tiles * q.C * q.acc * kRows * q.Mpad * sizeof(float);
 }
 
 cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s) {
     const Plan q = make_plan(a.mx4, a.gated, a.M, a.N, a.K, d.sms);
-    if (q.C > 1 && !a.ws) return cudaErrorInvalidValue;
+    if (!q.few && !a.ws) return cudaErrorInvalidValue;
+    const bool quantises = a.mx4 && a.x;
+    if (quantises && a.M > kFewTok) return cudaErrorInvalidValue;
     using Fn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, StreamParams);
     static const Fn kernels[] = {ffn_stream_kernel<false, true>, ffn_stream_kernel<true, false>,
                                  ffn_stream_kernel<true, true>};   // 16-bit gated, 4-bit, 4-bit gated
@@ -421,6 +488,12 @@ cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s)
     p.u = a.u;
     p.ldy = a.ldy;
     p.ws = a.ws;
+    p.few = q.few;
+    if (quantises) {
+        p.x = a.x;
+        p.ldx = a.ldx;
+        p.x_vec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ldx % 8 == 0;
+    }
     p.err = a.err;
     p.M = a.M;
     p.N = a.N;
@@ -443,7 +516,10 @@ cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s)
         const int64_t pitch = mx4_pitch(a.K);
         e = ffn_tensor_map(&ma, a.qa.codes, a.N, pitch, pitch, kRows, 128, kMapU8);
         if (e == cudaSuccess && a.gated) e = ffn_tensor_map(&mb, a.qb.codes, a.N, pitch, pitch, kRows, 128, kMapU8);
-        if (e == cudaSuccess) e = ffn_tensor_map(&mx, a.qx.codes, a.M, pitch, pitch, q.Mpad, 128, kMapU8);
+        if (quantises)
+            mx = ma;
+        else if (e == cudaSuccess)
+            e = ffn_tensor_map(&mx, a.qx.codes, a.M, pitch, pitch, q.Mpad, 128, kMapU8);
     } else {
         e = ffn_tensor_map(&ma, a.Wa, a.N, a.K, a.lda, q.feat, 64, a.dtype);
         if (e == cudaSuccess && a.gated) e = ffn_tensor_map(&mb, a.Wb, a.N, a.K, a.ldb, q.feat, 64, a.dtype);
