@@ -315,14 +315,11 @@ def skinny_gemm_noalloc(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor,
 
 _FFN_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
 _FFN_WORK: dict = {}   # workspace bytes by (device, operator, sizes): host arithmetic only
-_current_device = torch.cuda.current_device
-try:
-    _raw_stream = torch._C._cuda_getCurrentRawStream    # the handle alone, without a Stream object
-except AttributeError:   # pragma: no cover
-    def _raw_stream(index):
-        return torch.cuda.current_stream(index).cuda_stream
-
-
+# the current stream's handle without a Stream object, the current device without a
+# check of the CUDA state (the tensors at hand are CUDA tensors)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _DEVICES: dict = {}
 
 
@@ -333,15 +330,16 @@ def _device(index: int):
     return d
 
 
-def _elsewhere(t, name: str, stream) -> bool:
-    """Whether the call has to move to another device or stream first."""
+def _here(t, name: str, stream) -> int:
+    """The index of t's device, or -1 if the call has to move to another device or
+    stream first."""
     try:
-        index = t.device.index
+        index = t.get_device()
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
-    if index is None:
-        raise ValueError(f"{name} must be on a CUDA device, is on {t.device}")
-    return stream is not None or index != _current_device()
+    if index < 0:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return index if stream is None and index == _current_device() else -1
 
 
 @contextlib.contextmanager
@@ -367,12 +365,13 @@ def _rows(t, name: str, dtype, index: int) -> int:
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device.index != index:
+    if t.get_device() != index:
         raise ValueError(f"{name} must be on CUDA device {index}, is on {t.device}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D tensor")
+    try:
+        ld, inner = t.stride()
+    except ValueError:
+        raise ValueError(f"{name} must be a 2-D tensor") from None
     rows, cols = t.shape
-    ld, inner = t.stride()
     if rows <= 1:   # the stride of a single row says nothing
         ld = (cols + 7) // 8 * 8
     if ld < cols or (inner != 1 and cols > 1):
@@ -420,7 +419,7 @@ class Mx4Tensor:
     from stored ``codes`` and ``scales`` (uint8, of the sizes that
     ``Mx4Tensor.sizes`` gives, 16-byte aligned)."""
 
-    __slots__ = ("_buf", "_scales", "_code_bytes", "_scale_bytes", "shape", "device", "code_ptr", "scale_ptr")
+    __slots__ = ("_index", "_buf", "_scales", "_code_bytes", "_scale_bytes", "shape", "device", "code_ptr", "scale_ptr")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
         nc, ns = self.sizes(rows, cols)
@@ -434,7 +433,7 @@ class Mx4Tensor:
 
     def _set(self, buf, scales, nc, ns, rows, cols, code_ptr, scale_ptr):
         self._buf, self._scales, self._code_bytes, self._scale_bytes = buf, scales, nc, ns
-        self.shape, self.device = (rows, cols), buf.device
+        self.shape, self.device, self._index = (rows, cols), buf.device, buf.get_device()
         self.code_ptr, self.scale_ptr = code_ptr, scale_ptr
 
     @classmethod
@@ -456,6 +455,10 @@ class Mx4Tensor:
         a, b = ctypes.c_size_t(), ctypes.c_size_t()
         _check(load().kp_mx4_bytes(rows, cols, ctypes.byref(a), ctypes.byref(b)))
         return int(a.value), int(b.value)
+
+    def get_device(self) -> int:
+        """The CUDA device's index, -1 on the CPU."""
+        return self._index
 
     @property
     def codes(self) -> torch.Tensor:
@@ -482,7 +485,7 @@ class Mx4Tensor:
 def _mx4(q, name: str, index: int) -> Mx4Tensor:
     if not isinstance(q, Mx4Tensor):
         raise TypeError(f"{name} must be an Mx4Tensor (mx4_quantize), got {type(q).__name__}")
-    if q.device.type != "cuda" or q.device.index != index:
+    if q._index != index:
         raise ValueError(f"{name} must be on CUDA device {index}, is on {q.device}")
     return q
 
@@ -492,10 +495,10 @@ def mx4_quantize(x: torch.Tensor, stream=None) -> Mx4Tensor:
     may be strided) to microscaled 4 bits: per 32 columns the scale
     ``2^(floor(log2 max|x|) - 2)``, elements to the nearest of 0, .5, 1, 1.5, 2,
     3, 4, 6 scales, ties to even. A block with a NaN or an infinity becomes NaN."""
-    if _elsewhere(x, "x", stream):
+    index = _here(x, "x", stream)
+    if index < 0:
         with _on(x.device, stream, x):
             return mx4_quantize(x)
-    index = x.device.index
     ld = _rows(x, "x", None, index)
     dt = _FFN_DTYPES.get(x.dtype)
     if dt is None:
@@ -512,10 +515,10 @@ def mx4_dequantize(q: Mx4Tensor, dtype=torch.bfloat16, y: torch.Tensor | None = 
                    stream=None) -> torch.Tensor:
     """The values that ``q`` stands for: exact in bfloat16 and float32 (float16
     rounds, and overflows to infinity)."""
-    if _elsewhere(q, "q", stream):
+    index = _here(q, "q", stream)
+    if index < 0:
         with _on(q.device, stream, q, y):
             return mx4_dequantize(q, dtype, y)
-    index = q.device.index
     _mx4(q, "q", index)
     dt = _FFN_DTYPES.get(dtype)
     if dt is None:
@@ -552,10 +555,10 @@ def mx4_gemm(x, W: Mx4Tensor, y: torch.Tensor | None = None, dtype=None, stream=
     [M, K] is bfloat16 or float16 (quantised within the call; y has its type) or
     an ``Mx4Tensor`` (y has ``dtype``, bfloat16 unless given). ``W`` [N, K]. Any
     sizes; with ``x`` empty nothing runs."""
-    if _elsewhere(x, "x", stream):
+    index = _here(x, "x", stream)
+    if index < 0:
         with _on(x.device, stream, x, W, y):
             return mx4_gemm(x, W, y, dtype)
-    index = x.device.index
     M, K, dt, xargs = _mx4_left(x, dtype, index)
     N, Kw = _mx4(W, "W", index).shape
     if Kw != K:
@@ -574,10 +577,10 @@ def mx4_gated_ffn(x, Wg: Mx4Tensor, Wu: Mx4Tensor, act: str = "silu", h: torch.T
     """``h = round(act(Q(x) @ Q(Wg).T) * (Q(x) @ Q(Wu).T))``: the gated block over
     4-bit weights [F, K] and activations, in one product kernel. ``x`` as for
     ``mx4_gemm``; ``act`` as for ``gated_ffn``."""
-    if _elsewhere(x, "x", stream):
+    index = _here(x, "x", stream)
+    if index < 0:
         with _on(x.device, stream, x, Wg, Wu, h):
             return mx4_gated_ffn(x, Wg, Wu, act, h, dtype)
-    index = x.device.index
     code = _act_code(act)
     T, K, dt, xargs = _mx4_left(x, dtype, index)
     shape = _mx4(Wg, "Wg", index).shape
@@ -615,10 +618,10 @@ def gated_ffn(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "s
     may be strided (strides and K multiples of 8, 16-byte aligned). ``act``:
     "silu", "gelu" (erf) or "gelu_tanh". With ``save`` returns ``(h, g, u)``, the
     two products in float32, for ``gated_ffn_backward``."""
-    if _elsewhere(x, "x", stream):
+    index = _here(x, "x", stream)
+    if index < 0:
         with _on(x.device, stream, x, Wg, Wu, h):
             return gated_ffn(x, Wg, Wu, act, h, save)
-    index = x.device.index
     code = _act_code(act)
     T, F, K, ldx, ldg, ldu, dt = _gated_operands(x, Wg, Wu, index)
     h, ldh = _out(h, "h", T, F, dt, index)
@@ -642,10 +645,10 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu: 
     and ``dU = dh act(g)`` are computed in fp32 and rounded to x's type as the
     tensor cores' operands; the three products are summed in fp32. With no tokens
     the weights' gradients are zero."""
-    if _elsewhere(x, "x", stream):
+    index = _here(x, "x", stream)
+    if index < 0:
         with _on(x.device, stream, dh, x, Wg, Wu, g, u):
             return gated_ffn_backward(dh, x, Wg, Wu, g, u, act)
-    index = x.device.index
     code = _act_code(act)
     T, F, K, ldx, ldg, ldu, dt = _gated_operands(x, Wg, Wu, index)
     lddh = _rows(dh, "dh", dt, index)
