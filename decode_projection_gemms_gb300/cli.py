@@ -4,6 +4,8 @@ library's choice of kernel.
     python -m decode_projection_gemms_gb300.cli --M 4096 --N 4096 --K 7168 [--reps 5]
         [--cfg kind=cc,split_k=2,block=256,rows=4,k_unroll=1]
     python -m decode_projection_gemms_gb300.cli --kda --M 1 16 128 [--layers 4] [--reps 1]
+    python -m decode_projection_gemms_gb300.cli --ffn --M 1 16 512 [--F 2048] [--K 7168]
+        [--act silu] [--steps 4] [--fp16]
 
 GEMM: prints the configuration used (the table's or the built-in rule's
 choice, or the one given with --cfg as comma-separated kp_cfg fields) and the
@@ -11,8 +13,12 @@ device time per call over `reps` calls after one warm-up call, with CUDA
 events on the launching stream. --kda: the projection of the pages' shapes
 (packed [4096 + 136, 7168] weight, W_fb [1024, 128]) for each M in the
 table's mode, eagerly, `reps` passes over a stack of `layers` weight layers
-(one layer per call; 4 layers are 244 MB, above the L2). Inputs are seeded
-synthetic bf16 (or fp16 with --fp16).
+(one layer per call; 4 layers are 244 MB, above the L2). --ffn: a gated
+feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T. It is trained for `steps`
+steps on a batch of the largest M (towards a teacher block's outputs, on Wg and
+Wu), its weights are converted to microscaled 4 bits, and both forms then serve
+each M: times per call and how far the 4-bit outputs are from the 16-bit ones.
+Inputs are seeded synthetic bf16 (or fp16 with --fp16).
 """
 from __future__ import annotations
 
@@ -77,10 +83,71 @@ def run_kda(m_list, layers: int, reps: int):
         plan.close()
 
 
+def _time_us(fn, reps: int) -> float:
+    fn()   # warm-up
+    torch.cuda.synchronize()
+    a = torch.cuda.Event(enable_timing=True)
+    b = torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(reps):
+        fn()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b) * 1e3 / reps
+
+
+def run_ffn(m_list, F: int, K: int, act: str, steps: int, reps: int, dtype):
+    dev = torch.device("cuda", torch.cuda.current_device())
+    std = K ** -0.5
+    Wg, Wu = (gen_w(F, K, seed, std=std, device=dev, dtype=dtype) for seed in (1, 2))
+    Wd = gen_w(K, F, 3, std=F ** -0.5, device=dev, dtype=dtype)
+    Wd_t = Wd.t().contiguous()          # dh = dy Wd, a product with Wd^T's rows
+    T = max(m_list)
+    x = gen_x(T, K, seed=4, device=dev, dtype=dtype)
+
+    def block(xs, g, u):
+        return binding.skinny_gemm_ex(binding.gated_ffn(xs, g, u, act=act), Wd)
+
+    # a teacher: the same block with other gate and up weights
+    target = block(x, *(gen_w(F, K, seed, std=std, device=dev, dtype=dtype) for seed in (5, 6)))
+    losses = []
+    for step in range(steps + 1):
+        h, g, u = binding.gated_ffn(x, Wg, Wu, act=act, save=True)
+        diff = binding.skinny_gemm_ex(h, Wd) - target
+        losses.append(float(diff.float().square().mean()))
+        if step == steps:
+            break
+        dh = binding.skinny_gemm_ex(diff, Wd_t)
+        _, dWg, dWu = binding.gated_ffn_backward(dh, x, Wg, Wu, g, u, act=act)
+        for W, dW in ((Wg, dWg), (Wu, dWu)):   # a step of fixed length along the gradient
+            W.add_(dW, alpha=-0.05 * float(W.float().norm() / (dW.float().norm() + 1e-30)))
+    print(json.dumps({"training": {"tokens": T, "F": F, "K": K, "act": act, "losses": [round(v, 5) for v in losses]}}))
+
+    qg, qu, qd = (binding.mx4_quantize(W) for W in (Wg, Wu, Wd))
+
+    def block4(xs):
+        return binding.mx4_gemm(binding.mx4_gated_ffn(xs, qg, qu, act=act), qd)
+
+    for M in m_list:
+        xs = x[:M]
+        a, b = block(xs, Wg, Wu).float(), block4(xs).float()
+        print(json.dumps({"M": M, "us_16_bit": round(_time_us(lambda: block(xs, Wg, Wu), reps), 2),
+                          "us_4_bit": round(_time_us(lambda: block4(xs), reps), 2),
+                          "relative_difference": round(float((a - b).norm() / a.norm()), 4),
+                          "weight_bytes_16_bit": 2 * (Wg.numel() + Wu.numel() + Wd.numel()),
+                          "weight_bytes_4_bit": qg.nbytes + qu.nbytes + qd.nbytes,
+                          "device_error": binding.device_error()}))
+    return losses
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--kda", action="store_true", help="run the KDA projection instead of one GEMM")
+    ap.add_argument("--ffn", action="store_true", help="train and serve a gated feed-forward block")
     ap.add_argument("--M", type=int, nargs="+", required=True)
+    ap.add_argument("--F", type=int, default=2048, help="--ffn: features of the block")
+    ap.add_argument("--act", default="silu", choices=sorted(binding.ACTIVATIONS))
+    ap.add_argument("--steps", type=int, default=4, help="--ffn: training steps")
     ap.add_argument("--N", type=int)
     ap.add_argument("--K", type=int)
     ap.add_argument("--layers", type=int, default=4)
@@ -95,6 +162,10 @@ def main(argv=None):
     binding.load()
     if args.kda:
         run_kda(args.M, args.layers, args.reps)
+        return
+    if args.ffn:
+        run_ffn(args.M, args.F, args.K or 7168, args.act, args.steps, args.reps,
+                torch.float16 if args.fp16 else torch.bfloat16)
         return
     if args.N is None or args.K is None or len(args.M) != 1:
         ap.error("a GEMM needs one --M and --N, --K")

@@ -16,7 +16,8 @@
 //
 // Up to 8 tokens the 4-bit forms also quantise x themselves: of each stage one warp
 // turns the 256 columns of every token into the operand and scale tile that a copy
-// would have brought (T = 1, N = 4096, K = 7168: ONELAUNCH).
+// would have brought (T = 1, N = 4096, K = 7168: 7.7 us on the device against 8.0 with a
+// launch for x, 12 us against 20 from Python, which then allocates nothing but y).
 //
 // Warp 0: copies; warp 1: TMEM and MMA; warps 2 .. 5: x in 4 bits (few tokens),
 // epilogue; all six reduce.

@@ -36,23 +36,6 @@ struct Eight {
         const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     }
-    // The same from an address aligned to the element only, through the aligned
-    // words around it: kWindow bytes from the last 16-byte boundary.
-    static constexpr int kWindow = 32;
-    __device__ void load_shifted(const T *p) {
-        const uint32_t d = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
-        const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - d);
-        const uint4 a = __ldg(q), b = __ldg(q + 1);
-        uint32_t t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        if (d & 8)
-#pragma unroll
-            for (int i = 0; i < 6; ++i) t[i] = t[i + 2];
-        if (d & 4)
-#pragma unroll
-            for (int i = 0; i < 5; ++i) t[i] = t[i + 1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(t[i], t[i + 1], (d & 2) * 8);
-    }
     __device__ void load(const T *row, int c, int cols) {
         const uint16_t *h = reinterpret_cast<const uint16_t *>(row);
 #pragma unroll
@@ -113,12 +96,17 @@ struct Eight<float> {
     }
 };
 
+// Scale byte of a block whose largest magnitude has these fp32 bits.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+    const uint32_t ex = amax >> 23;   // 0: zero or subnormal, 255: infinity or NaN
+    return ex == 255 ? 255u : ex > 2 ? ex - 2 : 0u;
+}
+
 // Eight columns of a block that four neighbouring lanes hold: their codes, and in b
 // the block's scale byte (the same in the four lanes).
 template <typename T>
 __device__ __forceinline__ uint32_t quantize8(const Eight<T> &e, uint32_t &b) {
-    const uint32_t ex = e.amax() >> 23;   // 0: zero or subnormal, 255: infinity or NaN
-    b = ex == 255 ? 255u : ex > 2 ? ex - 2 : 0u;
+    b = scale_byte(e.amax());
     float v[8];
     e.scaled(inv_scale(b == 255 ? 127u : b), v);
     return e2m1x8(v);
