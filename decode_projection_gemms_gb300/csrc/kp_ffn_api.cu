@@ -34,7 +34,7 @@ static cudaError_t encoder(EncodeFn *out) {
 }
 
 cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld,
-                           int box_rows, int box_cols, int dtype) {
+                           int box_rows, int box_cols, int dtype, bool swizzle) {
     EncodeFn enc;
     cudaError_t e = encoder(&enc);
     if (e != cudaSuccess) return e;
@@ -47,7 +47,8 @@ cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int6
                                   : dtype == KP_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUresult r = enc(map, t, 2, const_cast<void *>(ptr), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

@@ -43,13 +43,25 @@ constexpr int kBand = 16;                 // row tiles kept together in the tile
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kBarBytes = 256;
 
+// 16-bit forms' outputs leave through shared memory, 32 rows of 64 columns a warp at
+// a time, in copies of whole lines (gated 4003 x 2048 x 7168: 127 us, with stores of
+// 32 bytes from each lane to a row of its own 130). In 4 bits the stage that this
+// memory costs is worth more (4096 x 4096 x 7168: 51.6 us, with stores 50.1).
+// Outputs whose rows do not start on 16 bytes pass through it in both cases, 16
+// columns at a time in rows of kOutPitch bytes.
+constexpr uint32_t kOutPitch = 48;
+constexpr uint32_t out_box(bool mx4) { return mx4 ? 32 * kOutPitch : 32 * 128; }
+constexpr uint32_t out_bytes(bool mx4) { return 8 * out_box(mx4); }
 // Operand halves and, in 4 bits, pairs of scale tiles (one of A, up to two of B); as
 // many stages as fit.
 constexpr uint32_t stage_bytes(bool mx4) { return 2 * kHalf + (mx4 ? 3 * 1024 : 0); }
-constexpr int stages(bool mx4) { return static_cast<int>((kMaxSmem - 1024 - kBarBytes) / stage_bytes(mx4)); }
+constexpr int stages(bool mx4) {
+    return static_cast<int>((kMaxSmem - 1024 - kBarBytes - out_bytes(mx4)) / stage_bytes(mx4));
+}
 
 struct TileMaps {
     CUtensorMap a0, a1, b0, b1, sa, sb0, sb1;
+    CUtensorMap y[2];   // outputs: gated, of the tile's two halves; dW, of both products
 };
 
 struct TileParams {
@@ -64,6 +76,8 @@ struct TileParams {
     int KB1, KB;         // K blocks of the first product, of all
     int kt_n;            // 4-bit: scale tiles per row tile
     int act, dtype, vec, vec_gu;
+    int pairs;           // y's rows start on 4 bytes
+    int copy_out;        // y's rows allow copies from shared memory (16-byte rows)
     uint32_t idesc;
 };
 
@@ -116,12 +130,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
     return elem_round(a, dtype) | static_cast<uint32_t>(elem_round(b, dtype)) << 16;
 }
 
-// Up to 32 consecutive outputs of one row, in stores of 32 bytes (vec 2), 16 (1) or
-// 2.
-__device__ __forceinline__ void put_row32(uint16_t *dst, const float (&v)[32], int left, int vec, int dtype) {
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], dtype);
+// Up to 32 consecutive outputs of one row (pairs), in stores of 32 bytes (vec 2) or
+// 16 (1); 8 columns at a time at the row's end.
+__device__ __forceinline__ void put_row32(uint16_t *dst, const uint32_t (&w)[16], int left, int vec) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int more = left - 16 * i;
@@ -131,16 +142,81 @@ __device__ __forceinline__ void put_row32(uint16_t *dst, const float (&v)[32], i
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(x[0]), "r"(x[1]),
                          "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                          : "memory");
-        } else if (vec && more >= 16) {
-            reinterpret_cast<uint4 *>(d)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-            reinterpret_cast<uint4 *>(d)[1] = make_uint4(x[4], x[5], x[6], x[7]);
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (k < more) d[k] = static_cast<uint16_t>(x[k / 2] >> (16 * (k & 1)));
+            for (int k = 0; k < 2; ++k) {
+                if (more >= 8 * k + 8) {
+                    reinterpret_cast<uint4 *>(d)[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (8 * k + j < more) d[8 * k + j] = static_cast<uint16_t>(x[4 * k + j / 2] >> (16 * (j & 1)));
+                }
+            }
         }
     }
 }
+
+// The same for rows that do not start on 16 bytes, by a whole warp (a lane a row):
+// through shared memory, so that a store covers 4 rows of 32 bytes (two columns a
+// lane, where rows start on 4 bytes) or 2 instead of 2 bytes in each of 32 rows
+// (16-bit gated 1536 x 700 x 1024: 11.1 us against 19.0).
+__device__ __forceinline__ void put_odd_rows32(uint16_t *dst, int64_t ld, const uint32_t (&w)[16], int left, int rows,
+                                               uint32_t box, int lane, bool pairs) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int cols = left - 16 * h;
+        if (cols <= 0) break;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t *x = w + 8 * h + 4 * i;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * kOutPitch + 16 * i), "r"(x[0]),
+                         "r"(x[1]), "r"(x[2]), "r"(x[3])
+                         : "memory");
+        }
+        __syncwarp();
+        uint16_t *d = dst + 16 * h;
+        if (pairs) {
+            const int c = 2 * (lane & 7);
+#pragma unroll 2
+            for (int r = lane >> 3; r < 32; r += 4) {
+                uint32_t two;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(two) : "r"(box + r * kOutPitch + 2 * c) : "memory");
+                if (r >= rows || c >= cols) continue;
+                if (c + 1 < cols)
+                    *reinterpret_cast<uint32_t *>(d + r * ld + c) = two;
+                else
+                    d[r * ld + c] = static_cast<uint16_t>(two);
+            }
+        } else {
+            const int c = lane & 15;
+#pragma unroll 2
+            for (int r = lane >> 4; r < 32; r += 2) {
+                uint16_t one;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(one) : "r"(box + r * kOutPitch + 2 * c) : "memory");
+                if (r < rows && c < cols) d[r * ld + c] = one;
+            }
+        }
+    }
+}
+
+// The same into a row of a warp's box in shared memory: 16-byte pieces 4 k .. 4 k + 3,
+// as far as the row goes; rows of 128 bytes are swizzled.
+__device__ __forceinline__ void put_box32(uint32_t row, const uint32_t (&w)[16], int k, int lane, uint32_t pitch) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t piece = static_cast<uint32_t>(4 * k + i);
+        if (piece * 16 >= pitch) break;
+        const uint32_t at = row + (pitch == 128 ? (piece ^ (static_cast<uint32_t>(lane) & 7u)) : piece) * 16;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[4 * i]), "r"(w[4 * i + 1]),
+                     "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                     : "memory");
+    }
+}
+
+// Outputs of a tile's columns that the first four epilogue warps take.
+__host__ __device__ constexpr int first_half(int out_n) { return (out_n / 2 + 31) & ~31; }
 
 // Up to 32 consecutive fp32 sums of one row.
 __device__ __forceinline__ void put_sums32(float *dst, const float (&v)[32], int left, int vec) {
@@ -177,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t raw = smem_u32(ft_smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = ft_smem_raw + (base - raw);
-    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + kStages * kStage);
+    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + kStages * kStage + out_bytes(kMx4));
     uint64_t *empty = full + kStages;
     uint64_t *accf = empty + kStages;
     uint64_t *acce = accf + 2;
@@ -360,7 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // the accumulator back before it computes or stores anything.
         const int q = warp & 3;
         const int half = warp >= 6;
-        const int span = (out_n / 2 + 31) & ~31;   // outputs of the first half
+        const int span = first_half(out_n);
+        const uint32_t box = base + kStages * kStage + static_cast<uint32_t>(warp - 2) * out_box(kMx4);
+        const uint32_t pitch = kGated ? 2u * static_cast<uint32_t>(half ? out_n - span : span) : 128u;   // bytes of its rows
         int as = 0;
         uint32_t aphase = 0;
         for (int i = cid; i < p.items; i += nclu) {
@@ -376,35 +454,73 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (lane == 0) remote_arrive(mapa_shared(smem_u32(acce + as), 0));
             if (++as == kAccs) as = 0, aphase ^= 1;
-            const int64_t m = it.m0 + rank * 128 + q * 32 + lane;
-            if (m >= p.M) continue;
+            const int m_first = it.m0 + rank * 128 + q * 32;
+            if (m_first >= p.M) continue;
+            const int64_t m = m_first + lane;
 #pragma unroll
-            for (int c = 0; c < (kGated ? 2 : 4); ++c) {
-                const int at = half * span + 32 * c;   // within the tile
+            for (int pair = 0; pair < (kGated ? 1 : 2); ++pair) {   // 64 columns at a time
+                const int at = half * span + 64 * pair;              // within the tile
                 const int n = it.n0 + at;
                 const int left = min(p.N - n, (half ? out_n : span) - at);
                 if (left <= 0) break;
-                float a[32];
+                const bool copy_out = !kMx4 && p.copy_out;
+                if (copy_out) {   // the last copy has read the buffer
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+                }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(v[c][j]);
-                if constexpr (kGated) {
-                    float b[32], h[32];
+                for (int k = 0; k < 2; ++k) {
+                    if (32 * k >= left) break;
+                    const int c = 2 * pair + k;
+                    float a[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) b[j] = __uint_as_float(v[2 + c][j]);
-                    if (!kMx4 && p.g) {
-                        put_sums32(p.g + m * p.N + n, a, left, p.vec_gu);
-                        put_sums32(p.u + m * p.N + n, b, left, p.vec_gu);
+                    for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(v[c][j]);
+                    if constexpr (kGated) {
+                        float b[32], h[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) b[j] = __uint_as_float(v[2 + k][j]);
+                        if (!kMx4 && p.g && m < p.M) {
+                            put_sums32(p.g + m * p.N + n + 32 * k, a, left - 32 * k, p.vec_gu);
+                            put_sums32(p.u + m * p.N + n + 32 * k, b, left - 32 * k, p.vec_gu);
+                        }
+                        ffn_gate(a, b, p.act, h);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) a[j] = h[j];
                     }
-                    ffn_gate(a, b, p.act, h);
-                    put_row32(p.y0 + m * p.ldy + n, h, left, p.vec, p.dtype);
-                } else if (kForm == TILE_DX && p.splits > 1) {
-                    put_sums32(p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n, a, left, 1);
-                } else {
-                    uint16_t *y = kForm == TILE_DW && it.z ? p.y1 : p.y0;
-                    put_row32(y + m * p.ldy + n, a, left, p.vec, p.dtype);
+                    if (kForm == TILE_DX && p.splits > 1) {
+                        if (m < p.M)
+                            put_sums32(p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n + 32 * k, a,
+                                       left - 32 * k, 1);
+                    } else {
+                        // the gradients' rows, multiples of 8 columns, always start on 16 bytes
+                        constexpr bool kAligned = kForm == TILE_DX || kForm == TILE_DW;
+                        uint16_t *y = (kForm == TILE_DW && it.z ? p.y1 : p.y0) + n + 32 * k;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = pack2(a[2 * j], a[2 * j + 1], p.dtype);
+                        if (copy_out) {
+                            put_box32(box + lane * pitch, w, k, lane, pitch);
+                        } else if (kAligned || p.vec) {
+                            if (m < p.M) put_row32(y + m * p.ldy, w, left - 32 * k, p.vec);
+                        } else {
+                            put_odd_rows32(y + m_first * p.ldy, p.ldy, w, left - 32 * k, p.M - m_first, box, lane, p.pairs);
+                        }
+                    }
+                }
+                if (copy_out) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)   // rows and columns past the output's are left out
+                        asm volatile(
+                            "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                            "cp.async.bulk.commit_group;" ::"l"(
+                                reinterpret_cast<uint64_t>(&tm.y[kGated ? half : kForm == TILE_DW ? it.z : 0])),
+                            "r"(n), "r"(m_first), "r"(box)
+                            : "memory");
                 }
             }
         }
+        if (!kMx4 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
     }
     tc_fence_before();
@@ -465,15 +581,16 @@ std::map<int, bool> g_ready;
 }  // namespace
 
 // By estimates of both kernels' times, from rounds of 256-column tiles and K blocks
-// for this one. Over the 720 sizes that they were fitted to the choice is 0.8 % (16
-// bits), 0.6 % (4 bits) and 0.5 % (4 bits, gated) slower than the better of the two;
-// each is up to 2.5 times as fast as the other (4 bits, K = 7168: 64 x 256 6.6 us
-// streamed, 16 in tiles; 1024 x 4096 30 against 17).
+// for this one (in 16 bits a tenth more, which the choice was best with). Over 300
+// sizes in 16 bits and 240 in 4, plain and gated, the choice is 0.9, 0.6 and 0.5 %
+// slower than the better of the two on average; each is up to 2.5 times as fast as
+// the other (4 bits, K = 7168: 64 x 256 6.6 us streamed, 16 in tiles; 1024 x 4096 30
+// against 17).
 bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms) {
     const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, gated ? 128 : 256);
     const float waves = static_cast<float>((tiles + sms / 2 - 1) / (sms / 2));
     const float kb = static_cast<float>(cdiv(K, mx4 ? 256 : 64));
-    const float us = !mx4    ? 3.7f + waves * (2.7f + 0.21f * kb)
+    const float us = !mx4    ? 1.1f * (3.7f + waves * (2.7f + 0.21f * kb))
                      : gated ? 5.3f + waves * (2.1f + 0.34f * kb)
                              : 2.4f + waves * (3.7f + 0.34f * kb);
     return us < ffn_stream_us(mx4, gated, M, N, K, sms);
@@ -531,14 +648,15 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     const uintptr_t starts = reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1) |
                              static_cast<uintptr_t>(a.ldy * 2);
     p.vec = starts % 32 == 0 ? 2 : starts % 16 == 0 ? 1 : 0;
+    p.pairs = starts % 4 == 0;
     p.vec_gu = a.N % 4 == 0;
     p.idesc = mx4 ? idesc_mxf4(256, p.nt)
                   : idesc_f16(a.dtype, 256, p.nt, a.form == TILE_DW, a.form == TILE_DW || a.form == TILE_DX);
 
     TileMaps tm = {};
     auto map = [&](CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows, int box_cols,
-                   int type) {
-        if (e == cudaSuccess) e = ffn_tensor_map(m, ptr, rows, cols, ld, box_rows, box_cols, type);
+                   int type, bool swizzle = true) {
+        if (e == cudaSuccess) e = ffn_tensor_map(m, ptr, rows, cols, ld, box_rows, box_cols, type, swizzle);
     };
     if (mx4) {
         const int64_t pitch = mx4_pitch(a.K);
@@ -566,10 +684,20 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
         map(&tm.a1, a.A1, a.K, a.M, a.lda, 64, 64, a.dtype);
         map(&tm.b0, a.B0, a.K, a.N, a.ldb0, 64, 64, a.dtype);
     }
+    p.copy_out = !mx4 && p.vec != 0 && p.splits == 1;
+    if (p.copy_out) {
+        const int out_n = gated ? p.nt / 2 : p.nt;
+        const int first = first_half(out_n);
+        for (int i = 0; i < 2; ++i) {
+            const int cols = !gated ? 64 : i ? out_n - first : first;
+            const void *y = a.form == TILE_DW && i ? a.y1 : a.y0;
+            if (cols && (i == 0 || gated || a.form == TILE_DW)) map(&tm.y[i], y, a.M, a.N, a.ldy, 32, cols, a.dtype, cols == 64);
+        }
+    }
     if (e != cudaSuccess) return e;
 
     size_t smem = 0;
-    if ((e = ffn_smem_for_tmem(d.dev, 512, stages(mx4) * stage_bytes(mx4) + 1024 + kBarBytes, &smem)) != cudaSuccess) return e;
+    if ((e = ffn_smem_for_tmem(d.dev, 512, stages(mx4) * stage_bytes(mx4) + out_bytes(mx4) + 1024 + kBarBytes, &smem)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2u * static_cast<unsigned>(std::min(p.items, d.sms / 2)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
