@@ -22,7 +22,6 @@
 // Warp 0: copies; warp 1: TMEM and MMA; warps 2 .. 5: x in 4 bits (few tokens),
 // epilogue; all six reduce.
 #include <algorithm>
-#include <map>
 #include <mutex>
 
 #include "kp_mx4.cuh"
@@ -433,7 +432,7 @@ Plan make_plan(bool mx4, bool gated, int M, int N, int K, int sms) {
 }
 
 std::mutex g_mu;
-std::map<int, bool> g_ready;   // devices whose kernels have their shared memory raised
+bool g_ready[64];   // devices whose kernels have their shared memory raised
 
 }  // namespace
 
@@ -471,12 +470,12 @@ cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s)
     cudaError_t e = cudaSuccess;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        if (!g_ready[d.dev]) {
+        if (d.dev >= 64 || !g_ready[d.dev]) {
             for (Fn f : kernels)
                 if (e == cudaSuccess)
                     e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
             if (e != cudaSuccess) return e;
-            g_ready[d.dev] = true;
+            if (d.dev < 64) g_ready[d.dev] = true;
         }
     }
     StreamParams p = {};

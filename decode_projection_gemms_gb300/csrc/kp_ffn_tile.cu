@@ -27,7 +27,6 @@
 //
 // Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 9: epilogue.
 #include <algorithm>
-#include <map>
 #include <mutex>
 
 #include "kp_ffn.cuh"
@@ -576,7 +575,7 @@ int dx_splits(int M, int N, int nt, int KB, int sms) {
 }
 
 std::mutex g_mu;
-std::map<int, bool> g_ready;
+bool g_ready[64];   // devices whose kernels have their shared memory raised
 
 }  // namespace
 
@@ -593,7 +592,8 @@ bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms) {
     const float us = !mx4    ? 1.1f * (3.7f + waves * (2.7f + 0.21f * kb))
                      : gated ? 5.3f + waves * (2.1f + 0.34f * kb)
                              : 2.4f + waves * (3.7f + 0.34f * kb);
-    return us < ffn_stream_us(mx4, gated, M, N, K, sms);
+    // (the other kernel has its token tiles of 128 on the grid's y axis)
+    return M > 65535 * 128 || us < ffn_stream_us(mx4, gated, M, N, K, sms);
 }
 
 size_t ffn_tile_scratch(int form, int M, int N, int K, int sms) {
@@ -612,12 +612,12 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     cudaError_t e = cudaSuccess;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        if (!g_ready[d.dev]) {
+        if (d.dev >= 64 || !g_ready[d.dev]) {
             for (Fn f : kernels)
                 if (e == cudaSuccess)
                     e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
             if (e != cudaSuccess) return e;
-            g_ready[d.dev] = true;
+            if (d.dev < 64) g_ready[d.dev] = true;
         }
     }
     TileParams p = {};
