@@ -85,30 +85,30 @@ float ffn_stream_us(bool mx4, bool gated, int M, int N, int K, int sms);   // es
 cudaError_t ffn_stream_launch(const FfnArgs &a, const FfnDev &d, cudaStream_t s);
 
 // One launch of the tile kernel (kp_ffn_tile.cu), for many tokens and for the
-// backward pass. D[m, n] = sum_k A[m, k] B[n, k], D row-major.
+// backward pass.
 enum FfnTileForm {
     TILE_GATED,       // A = x, B = Wg and Wu side by side: h (and g, u)
     TILE_MX4_GATED,   // the same over microscaled operands
     TILE_MX4,         // A = x, B = W, microscaled: y
-    TILE_DX,          // D = A0 B0 + A1 B1, A = dG, dU [m, k], B = Wg, Wu stored [k, n]
-    TILE_DW           // D0 = A0 B0, D1 = A1 B0, A = dG, dU stored [k, m], B = x stored [k, n]
+    TILE_BACKWARD     // dx = dG Wg + dU Wu, dWg = dG^T x and dWu = dU^T x
 };
 struct FfnTileArgs {
     int form = TILE_GATED;
     int act = 0, dtype = KP_BF16;
-    const void *A0 = nullptr, *A1 = nullptr, *B0 = nullptr, *B1 = nullptr;
-    int64_t lda = 0, ldb0 = 0, ldb1 = 0;
+    const void *A0 = nullptr, *A1 = nullptr;     // x; backward: dG, dU [M, N]
+    const void *B0 = nullptr, *B1 = nullptr;     // Wg, Wu
+    const void *X = nullptr;                     // backward: x
+    int64_t lda = 0, ldb0 = 0, ldb1 = 0, ldx = 0;
     Mx4Mat qa, qb0, qb1;
-    void *y0 = nullptr, *y1 = nullptr;
+    void *y0 = nullptr, *y1 = nullptr, *y2 = nullptr;   // h or y; backward: dx, dWg, dWu (row stride K)
     int64_t ldy = 0;
     float *g = nullptr, *u = nullptr;
-    int M = 0, N = 0, K = 0;     // D is M x N (gated: N = F); K per product
-    float *ws = nullptr;         // TILE_DX: split-K partial sums
+    int M = 0, N = 0, K = 0;     // tokens, features, columns of x
+    float *ws = nullptr;         // backward: partial sums of dx
     bool pdl = false;
     int *err = nullptr;
 };
-// Split-K partial sums of TILE_DX, bytes (0: it does not split).
-size_t ffn_tile_scratch(int form, int M, int N, int K, int sms);
+size_t ffn_backward_scratch(int T, int F, int K, int sms);   // bytes of ws (0: dx is not split)
 cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t s);
 
 // Whether a forward product takes the tile kernel or the weight-streaming one.

@@ -195,7 +195,7 @@ static BwdWork bwd_work(int T, int F, int K, int sms) {
     w.ld = (static_cast<int64_t>(F) + 7) / 8 * 8;
     w.du = up256(static_cast<size_t>(T) * w.ld * 2);
     w.part = 2 * w.du;
-    w.bytes = w.part + ffn_tile_scratch(TILE_DX, T, K, F, sms);
+    w.bytes = w.part + ffn_backward_scratch(T, F, K, sms);
     return w;
 }
 
@@ -432,7 +432,7 @@ int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t l
     cudaError_t e = ffn_gate_grad_launch(dh, lddh, g, u, base, base + w.du, w.ld, T, F, act, dtype, d.sms, stream);
     if (e != cudaSuccess) return cuda_failed(e, fn);
     FfnTileArgs t;
-    t.form = TILE_DX;
+    t.form = TILE_BACKWARD;
     t.dtype = dtype;
     t.A0 = base;
     t.A1 = base + w.du;
@@ -441,22 +441,17 @@ int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t l
     t.B1 = Wu;
     t.ldb0 = ldg;
     t.ldb1 = ldu;
+    t.X = x;
+    t.ldx = ldx;
     t.y0 = dx;
+    t.y1 = dWg;
+    t.y2 = dWu;
     t.ldy = K;
     t.M = T;
-    t.N = K;
-    t.K = F;
+    t.N = F;
+    t.K = K;
     t.ws = reinterpret_cast<float *>(base + w.part);
     t.err = d.err;
-    if ((e = ffn_tile_launch(t, d, stream)) != cudaSuccess) return cuda_failed(e, fn);
-    t.form = TILE_DW;
-    t.B0 = x;
-    t.ldb0 = ldx;
-    t.y0 = dWg;
-    t.y1 = dWu;
-    t.M = F;
-    t.N = K;
-    t.K = T;
     if ((e = ffn_tile_launch(t, d, stream)) != cudaSuccess) return cuda_failed(e, fn);
     return KP_OK;
 }

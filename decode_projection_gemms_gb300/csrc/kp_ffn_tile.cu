@@ -10,17 +10,20 @@
 // tcgen05.commit returns stages and accumulators to both. Clusters are
 // persistent: a cluster takes items c, c + n, ... of the tile list, whose order
 // keeps a band of row tiles together so that their operands stay in L2.
+// D[m, n] = sum_k A[m, k] B[n, k], D row-major.
 //
 // Forms:
 //   gated    B's halves are nt/2 rows of Wg (CTA 0) and the same ones of Wu (CTA
 //            1): a thread of the epilogue finds the gate in accumulator column c
 //            and its factor in column nt/2 + c;
-//   dx       two products into one accumulator (dG Wg, then dU Wu), Wg and Wu
-//            read as they lie, N contiguous (the MMA's transposed operand). With
-//            few tokens the contraction is split over clusters, whose fp32
+//   backward one list of the tiles of dx and of both weights' gradients (T = 333, F =
+//            1416, K = 2048: 20 us, as two launches 30). dx is two products into one accumulator (dG
+//            Wg, then dU Wu), Wg and Wu read as they lie, N contiguous (the MMA's
+//            transposed operand); the weights' gradients are dG^T x and dU^T x, both
+//            operands with K (the tokens) strided. dx's items, the longest, come
+//            first; clusters without one take weight tiles for as long. Where even so
+//            dx would end last, its contraction is split over clusters, whose fp32
 //            partial sums a second kernel adds in order;
-//   dW       two outputs in one tile list (dG^T x and dU^T x), both operands
-//            with K (the tokens) strided;
 //   4-bit    kind::mxf4; scale tiles go to TMEM columns of their stage. The
 //            accumulator and the scales fill the tensor memory, so these have
 //            one accumulator, the 16-bit forms two.
@@ -60,24 +63,35 @@ constexpr int stages(bool mx4) {
 
 struct TileMaps {
     CUtensorMap a0, a1, b0, b1, sa, sb0, sb1;
-    CUtensorMap y[2];   // outputs: gated, of the tile's two halves; dW, of both products
+    CUtensorMap aw0, aw1, bw;   // backward: operands of the weights' gradients
+    CUtensorMap y[3];           // outputs: gated, of the tile's two halves; backward, dx, dWg, dWu
+};
+
+// The tiles of one output shape.
+struct TileSet {
+    int M, N;             // of the output
+    int tiles_m, tiles_n;
+    int nt;               // accumulator columns of a tile (gated: of both products)
+    int KB;               // K blocks
+    uint32_t idesc;
 };
 
 struct TileParams {
-    uint16_t *y0, *y1;
+    TileSet set[2];       // 0: the forward output or dx; 1: the weights' gradients, twice
+    uint16_t *y[3];
     float *g, *u;
     int64_t ldy;
     float *ws;
     int *err;
-    int M, N, K;
-    int tiles_m, tiles_n, items, splits;
-    int nt;              // accumulator columns of a tile (gated: of both products)
-    int KB1, KB;         // K blocks of the first product, of all
-    int kt_n;            // 4-bit: scale tiles per row tile
+    int K;
+    int items;            // of set 0: tiles, times the parts of a split contraction
+    int splits;
+    int w_items, w_first; // of set 1; those a cluster without an own last item of set 0 takes meanwhile
+    int KB1;              // K blocks of dx's first product
+    int kt_n;             // 4-bit: scale tiles per row tile
     int act, dtype, vec, vec_gu;
-    int pairs;           // y's rows start on 4 bytes
-    int copy_out;        // y's rows allow copies from shared memory (16-byte rows)
-    uint32_t idesc;
+    int pairs;            // y's rows start on 4 bytes
+    int copy_out;         // y's rows allow copies from shared memory (16-byte rows)
 };
 
 // ---- cta_group::2 forms ----------------------------------------------------------
@@ -236,17 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     ffn_tile_kernel(const __grid_constant__ TileMaps tm, const TileParams p) {
     constexpr bool kMx4 = kForm == TILE_MX4 || kForm == TILE_MX4_GATED;
     constexpr bool kGated = kForm == TILE_GATED || kForm == TILE_MX4_GATED;
-    constexpr bool kAMn = kForm == TILE_DW;
-    constexpr bool kBMn = kForm == TILE_DW || kForm == TILE_DX;
+    constexpr bool kBwd = kForm == TILE_BACKWARD;
     constexpr uint32_t kStage = stage_bytes(kMx4);
     constexpr int kStages = stages(kMx4);
     constexpr int kAccs = kMx4 ? 1 : 2;
     constexpr int kCols = kMx4 ? 128 : 64;      // map columns per K block, K-major operands
     constexpr uint32_t kSfCol = 256, kSfStage = 24;   // 4-bit: scale columns (A 8, B 16 a stage)
-    const int half_n = p.nt / 2;                      // rows of B per CTA
-    const int out_n = kGated ? half_n : p.nt;         // outputs of a tile along N
-    const int sb_tiles = kGated ? 2 : p.nt >> 7;      // 4 bits: row tiles of B's scales
-    const uint32_t tx = 2 * (kHalf + static_cast<uint32_t>(half_n) * 128 + (kMx4 ? 1024u * (1 + sb_tiles) : 0u));
+    const int sb_tiles = kGated ? 2 : p.set[0].nt >> 7;   // 4 bits: row tiles of B's scales
 
     extern __shared__ uint8_t ft_smem_raw[];
     const uint32_t raw = smem_u32(ft_smem_raw);
@@ -290,25 +300,49 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = *tmem_slot;
 
     struct Item {
+        int set;              // 1: a tile of a weight's gradient, z which
         int z, split, m0, n0, kb0, kb1;
+        int half_n, out_n;    // rows of B per CTA, outputs along N
     };
-    const int tiles = p.tiles_m * p.tiles_n;
-    auto item_at = [&](int i) {
-        Item it;
-        const int per = tiles * p.splits;
-        it.z = i / per;
-        i -= it.z * per;
-        it.split = i / tiles;
-        i -= it.split * tiles;
+    // The i-th item of this cluster; false when there is none.
+    auto get = [&](int i, Item &it) {
+        int j = cid + i * nclu;
+        it.set = 0;
+        if constexpr (kBwd) {
+            // items of set 0 in rounds; `last` clusters have one more than the others,
+            // which take up to w_first weight tiles each before the common rounds
+            const int last = p.items % nclu;
+            const int mine0 = p.items / nclu + (cid < last);
+            if (i >= mine0) {
+                i -= mine0;
+                const int idle = nclu - last;
+                const int early = last ? min(p.w_first * idle, p.w_items) : 0;
+                const int own = cid >= last && early > cid - last ? (early - (cid - last) + idle - 1) / idle : 0;
+                j = i < own ? cid - last + i * idle : early + cid + (i - own) * nclu;
+                if (j >= p.w_items) return false;
+                it.set = 1;
+            }
+        } else if (j >= p.items) {
+            return false;
+        }
+        const TileSet &t = p.set[kBwd ? it.set : 0];
+        const int tiles = t.tiles_m * t.tiles_n;
+        const int part = j / tiles;      // set 0: of the contraction; set 1: which weight
+        j -= part * tiles;
+        it.z = it.set ? part : 0;
+        it.split = it.set ? 0 : part;
+        const int splits = it.set ? 1 : p.splits;
         // bands of kBand row tiles, column tiles within a band, rows innermost
-        const int band = i / (kBand * p.tiles_n);
-        const int r = i - band * kBand * p.tiles_n;
-        const int h = min(kBand, p.tiles_m - band * kBand);
+        const int band = j / (kBand * t.tiles_n);
+        const int r = j - band * kBand * t.tiles_n;
+        const int h = min(kBand, t.tiles_m - band * kBand);
+        it.half_n = t.nt / 2;
+        it.out_n = kGated ? it.half_n : t.nt;
         it.m0 = (band * kBand + r % h) * kTile;
-        it.n0 = r / h * out_n;
-        it.kb0 = static_cast<int>(static_cast<long long>(p.KB) * it.split / p.splits);
-        it.kb1 = static_cast<int>(static_cast<long long>(p.KB) * (it.split + 1) / p.splits);
-        return it;
+        it.n0 = r / h * it.out_n;
+        it.kb0 = static_cast<int>(static_cast<long long>(t.KB) * it.split / splits);
+        it.kb1 = static_cast<int>(static_cast<long long>(t.KB) * (it.split + 1) / splits);
+        return true;
     };
 
     if (warp == 0) {
@@ -318,9 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t full0 = mapa_shared(smem_u32(full), 0);   // the leader's barriers
             int stage = 0;
             uint32_t phase = 1;   // a fresh barrier passes a wait for the phase before its first
-            for (int i = cid; i < p.items; i += nclu) {
-                const Item it = item_at(i);
+            Item it;
+            for (int i = 0; get(i, it); ++i) {
                 const int m = it.m0 + rank * 128;
+                const uint32_t tx =
+                    2 * (kHalf + static_cast<uint32_t>(it.half_n) * 128 + (kMx4 ? 1024u * (1 + sb_tiles) : 0u));
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
                     mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
                     const uint32_t st = base + stage * kStage;
@@ -328,31 +364,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     if (rank == 0 && mine) mbar_expect_tx(smem_u32(full + stage), tx);
                     if (++stage == kStages) stage = 0, phase ^= 1;
                     if (!mine) continue;
-                    const bool second = kForm == TILE_DX && kb >= p.KB1;
-                    const int k = second ? kb - p.KB1 : kb;
-                    const CUtensorMap *ma = (kForm == TILE_DX && second) || (kForm == TILE_DW && it.z) ? &tm.a1 : &tm.a0;
-                    if constexpr (kAMn) {
-                        pair_load(st, ma, bar, m, k * 64);
-                        pair_load(st + 8192, ma, bar, m + 64, k * 64);
-                    } else {
-                        pair_load(st, ma, bar, k * kCols, m);
-                    }
-                    const CUtensorMap *mb = (kGated && rank) || second ? &tm.b1 : &tm.b0;
-                    const int n = it.n0 + (kGated ? 0 : rank * half_n);
-                    if constexpr (kBMn) {
+                    const int n = it.n0 + (kGated ? 0 : rank * it.half_n);
+                    if constexpr (kBwd) {
+                        const bool second = !it.set && kb >= p.KB1;
+                        const int k = second ? kb - p.KB1 : kb;
+                        if (it.set) {
+                            const CUtensorMap *ma = it.z ? &tm.aw1 : &tm.aw0;
+                            pair_load(st, ma, bar, m, k * 64);
+                            pair_load(st + 8192, ma, bar, m + 64, k * 64);
+                        } else {
+                            pair_load(st, second ? &tm.a1 : &tm.a0, bar, k * 64, m);
+                        }
+                        const CUtensorMap *mb = it.set ? &tm.bw : second ? &tm.b1 : &tm.b0;
                         pair_load(st + kHalf, mb, bar, n, k * 64);
-                        if (half_n > 64) pair_load(st + kHalf + 8192, mb, bar, n + 64, k * 64);
+                        if (it.half_n > 64) pair_load(st + kHalf + 8192, mb, bar, n + 64, k * 64);
                     } else {
-                        pair_load(st + kHalf, mb, bar, k * kCols, n);
+                        pair_load(st, &tm.a0, bar, kb * kCols, m);
+                        pair_load(st + kHalf, kGated && rank ? &tm.b1 : &tm.b0, bar, kb * kCols, n);
                     }
                     if constexpr (kMx4) {
                         // the scales of this CTA's A rows and of all of B's rows
                         const uint32_t sc = st + 2 * kHalf;
-                        pair_load(sc, &tm.sa, bar, 0, (m >> 7) * p.kt_n + 2 * k);
+                        pair_load(sc, &tm.sa, bar, 0, (m >> 7) * p.kt_n + 2 * kb);
                         const int nt = it.n0 >> 7;
                         for (int t = 0; t < sb_tiles; ++t)
                             pair_load(sc + 1024 * (1 + t), kGated && t ? &tm.sb1 : &tm.sb0, bar, 0,
-                                      (kGated ? nt : nt + t) * p.kt_n + 2 * k);
+                                      (kGated ? nt : nt + t) * p.kt_n + 2 * kb);
                     }
                 }
             }
@@ -391,16 +428,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
             };
-            if (cid < p.items) prepare(0, 0);
-            for (int i = cid; i < p.items; i += nclu) {
-                const Item it = item_at(i);
+            Item it, next;
+            bool more_items = get(0, it);
+            if (more_items) prepare(0, 0);
+            for (int i = 0; more_items; ++i, it = next) {
+                more_items = get(i + 1, next);
+                const bool a_mn = kBwd && it.set;
+                const uint32_t idesc = p.set[kBwd ? it.set : 0].idesc;
                 mbar_wait_bounded(smem_u32(acce + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
                 tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(as) * 256;
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
                     const uint32_t st = base + stage * kStage;
-                    const uint64_t ad = kAMn ? desc_mn(st) : desc_kmajor(st);
-                    const uint64_t bd = kBMn ? desc_mn(st + kHalf) : desc_kmajor(st + kHalf);
+                    const uint64_t ad = a_mn ? desc_mn(st) : desc_kmajor(st);
+                    const uint64_t bd = kBwd ? desc_mn(st + kHalf) : desc_kmajor(st + kHalf);
                     const uint32_t sf = tmem + kSfCol + static_cast<uint32_t>(stage) * kSfStage;
                     const uint32_t bar = smem_u32(empty + stage);
                     // 64 4-bit columns a step, and steps past K are left out (their
@@ -411,16 +452,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         if (!mine) return;
                         const uint32_t more = kb > it.kb0 || kk > 0;
                         if constexpr (kMx4)
-                            pair_mma_mxf4(d, ad + 2 * kk, bd + 2 * kk, idesc_sf(p.idesc, (kk & 1) * 2),
+                            pair_mma_mxf4(d, ad + 2 * kk, bd + 2 * kk, idesc_sf(idesc, (kk & 1) * 2),
                                           sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), more);
                         else
-                            pair_mma_f16(d, ad + kk * (kAMn ? 128 : 2), bd + kk * (kBMn ? 128 : 2), p.idesc, more);
+                            pair_mma_f16(d, ad + kk * (a_mn ? 128 : 2), bd + kk * (kBwd ? 128 : 2), idesc, more);
                     };
 #pragma unroll
                     for (int kk = 0; kk < 3; ++kk)
                         if (kk < steps - 1) mma(kk);
                     if (++stage == kStages) stage = 0, phase ^= 1;
-                    if (kb + 1 < it.kb1 || i + nclu < p.items) prepare(stage, phase);
+                    if (kb + 1 < it.kb1 || more_items) prepare(stage, phase);
                     mma(steps - 1);
                     if (mine) pair_commit(bar);
                 }
@@ -435,34 +476,35 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // the accumulator back before it computes or stores anything.
         const int q = warp & 3;
         const int half = warp >= 6;
-        const int span = first_half(out_n);
         const uint32_t box = base + kStages * kStage + static_cast<uint32_t>(warp - 2) * out_box(kMx4);
-        const uint32_t pitch = kGated ? 2u * static_cast<uint32_t>(half ? out_n - span : span) : 128u;   // bytes of its rows
         int as = 0;
         uint32_t aphase = 0;
-        for (int i = cid; i < p.items; i += nclu) {
-            const Item it = item_at(i);
+        Item it;
+        for (int i = 0; get(i, it); ++i) {
+            const int span = first_half(it.out_n);
+            const uint32_t pitch = kGated ? 2u * static_cast<uint32_t>(half ? it.out_n - span : span) : 128u;   // of the box's rows
+            const int M = p.set[kBwd ? it.set : 0].M, N = p.set[kBwd ? it.set : 0].N;
             mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
             tc_fence_after();
             const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * span;
             uint32_t v[4][32];   // gated: 0 and 1 the gates, 2 and 3 their factors
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(t + (kGated && c >= 2 ? half_n - 64 : 0) + 32 * c, v[c]);
+            for (int c = 0; c < 4; ++c) tmem_ld32(t + (kGated && c >= 2 ? it.half_n - 64 : 0) + 32 * c, v[c]);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) remote_arrive(mapa_shared(smem_u32(acce + as), 0));
             if (++as == kAccs) as = 0, aphase ^= 1;
             const int m_first = it.m0 + rank * 128 + q * 32;
-            if (m_first >= p.M) continue;
+            if (m_first >= M) continue;
             const int64_t m = m_first + lane;
 #pragma unroll
             for (int pair = 0; pair < (kGated ? 1 : 2); ++pair) {   // 64 columns at a time
                 const int at = half * span + 64 * pair;              // within the tile
                 const int n = it.n0 + at;
-                const int left = min(p.N - n, (half ? out_n : span) - at);
+                const int left = min(N - n, (half ? it.out_n : span) - at);
                 if (left <= 0) break;
-                const bool copy_out = !kMx4 && p.copy_out;
+                const bool copy_out = kBwd ? it.set || p.splits == 1 : !kMx4 && p.copy_out;
                 if (copy_out) {   // the last copy has read the buffer
                     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     __syncwarp();
@@ -478,31 +520,29 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         float b[32], h[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) b[j] = __uint_as_float(v[2 + k][j]);
-                        if (!kMx4 && p.g && m < p.M) {
-                            put_sums32(p.g + m * p.N + n + 32 * k, a, left - 32 * k, p.vec_gu);
-                            put_sums32(p.u + m * p.N + n + 32 * k, b, left - 32 * k, p.vec_gu);
+                        if (!kMx4 && p.g && m < M) {
+                            put_sums32(p.g + m * N + n + 32 * k, a, left - 32 * k, p.vec_gu);
+                            put_sums32(p.u + m * N + n + 32 * k, b, left - 32 * k, p.vec_gu);
                         }
                         ffn_gate(a, b, p.act, h);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) a[j] = h[j];
                     }
-                    if (kForm == TILE_DX && p.splits > 1) {
-                        if (m < p.M)
-                            put_sums32(p.ws + (static_cast<int64_t>(it.split) * p.M + m) * p.N + n + 32 * k, a,
+                    if (kBwd && !copy_out) {
+                        if (m < M)
+                            put_sums32(p.ws + (static_cast<int64_t>(it.split) * M + m) * N + n + 32 * k, a,
                                        left - 32 * k, 1);
                     } else {
-                        // the gradients' rows, multiples of 8 columns, always start on 16 bytes
-                        constexpr bool kAligned = kForm == TILE_DX || kForm == TILE_DW;
-                        uint16_t *y = (kForm == TILE_DW && it.z ? p.y1 : p.y0) + n + 32 * k;
                         uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[j] = pack2(a[2 * j], a[2 * j + 1], p.dtype);
-                        if (copy_out) {
+                        uint16_t *y = p.y[0] + n + 32 * k;
+                        if (kBwd || copy_out) {
                             put_box32(box + lane * pitch, w, k, lane, pitch);
-                        } else if (kAligned || p.vec) {
-                            if (m < p.M) put_row32(y + m * p.ldy, w, left - 32 * k, p.vec);
+                        } else if (p.vec) {
+                            if (m < M) put_row32(y + m * p.ldy, w, left - 32 * k, p.vec);
                         } else {
-                            put_odd_rows32(y + m_first * p.ldy, p.ldy, w, left - 32 * k, p.M - m_first, box, lane, p.pairs);
+                            put_odd_rows32(y + m_first * p.ldy, p.ldy, w, left - 32 * k, M - m_first, box, lane, p.pairs);
                         }
                     }
                 }
@@ -513,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         asm volatile(
                             "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
                             "cp.async.bulk.commit_group;" ::"l"(
-                                reinterpret_cast<uint64_t>(&tm.y[kGated ? half : kForm == TILE_DW ? it.z : 0])),
+                                reinterpret_cast<uint64_t>(&tm.y[kGated ? half : it.set ? 1 + it.z : 0])),
                             "r"(n), "r"(m_first), "r"(box)
                             : "memory");
                 }
@@ -546,32 +586,67 @@ __global__ void __launch_bounds__(256) join_kernel(const float *ws, int64_t n, i
 
 int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// Accumulator columns of a tile: those whose rounds of tiles over the SM pairs cost
-// least, a tile costing its columns' K blocks and about six K blocks of fixed work.
-// 4-bit tiles start at whole scale tiles of 128 rows (a gated one holds one of each
-// weight): the MMA reads B's scales from a multiple of four TMEM columns. B with N
-// contiguous comes in boxes of 64. Gated 4003 x 2048 x 7168 (256 tiles of 256 columns
-// on 76 SM pairs, or 304 of 224): 141 us with 256 columns, 130 with 224.
+// Accumulator columns of a forward tile: those whose rounds of tiles over the SM
+// pairs cost least, a tile costing its columns' K blocks and about six K blocks of
+// fixed work. 4-bit tiles start at whole scale tiles of 128 rows (a gated one holds
+// one of each weight): the MMA reads B's scales from a multiple of four TMEM columns.
+// Gated 4003 x 2048 x 7168 (256 tiles of 256 columns on 76 SM pairs, or 304 of 224):
+// 141 us with 256 columns, 130 with 224.
 int tile_columns(int form, int64_t M, int64_t N, int KB, int sms) {
     const bool gated = form == TILE_GATED || form == TILE_MX4_GATED;
     const int step = form == TILE_GATED ? 32 : form == TILE_MX4_GATED ? 256 : 128;
     int best = 256;
     int64_t least = -1;
     for (int nt = 256; nt >= (step > 64 ? step : 64); nt -= step) {
-        const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, gated ? nt / 2 : nt) * (form == TILE_DW ? 2 : 1);
+        const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, gated ? nt / 2 : nt);
         const int64_t cost = (tiles + sms / 2 - 1) / (sms / 2) * (static_cast<int64_t>(nt) * KB + 256 * 6);
         if (least < 0 || cost < least) least = cost, best = nt;
     }
     return best;
 }
 
-// K splits of dx: enough that every SM pair has work, each with at least
-// eight K blocks (a partial tile costs about as much as four to write and add).
-int dx_splits(int M, int N, int nt, int KB, int sms) {
-    const int64_t tiles = static_cast<int64_t>(cdiv(M, kTile)) * cdiv(N, nt);
-    int s = 1;
-    while (tiles * (s + 1) <= sms / 2 && KB / (s + 1) >= 8) ++s;
-    return s;
+// The backward list: columns of dx's and of the weight gradients' tiles (256, or 128
+// for more and shorter items; B with N contiguous comes in boxes of 64), parts that
+// dx's contraction is split into, and the weight tiles that take as long as the last
+// item of dx. Chosen by the longest cluster's work, in K blocks of a 256-column tile:
+// a 128-column one takes 0.65 (its loads bind), an item's start and end four, the
+// kernel that joins a split dx twelve.
+struct BackwardPlan {
+    int nt[2], tiles_m[2], tiles_n[2], KB[2];
+    int splits, w_first;
+    int64_t items, w_items;
+};
+
+BackwardPlan backward_plan(int T, int F, int K, int sms) {
+    const int P = sms / 2;
+    BackwardPlan best = {};
+    float least = -1.f;
+    for (int pick = 0; pick < 4; ++pick) {
+        BackwardPlan q = {};
+        q.nt[0] = pick & 1 ? 128 : 256;
+        q.nt[1] = pick & 2 ? 128 : 256;
+        q.KB[0] = 2 * cdiv(F, 64);
+        q.KB[1] = cdiv(T, 64);
+        q.tiles_m[0] = cdiv(T, kTile);
+        q.tiles_m[1] = cdiv(F, kTile);
+        for (int i = 0; i < 2; ++i) q.tiles_n[i] = cdiv(K, q.nt[i]);
+        const int64_t tiles = static_cast<int64_t>(q.tiles_m[0]) * q.tiles_n[0];
+        q.w_items = 2ll * q.tiles_m[1] * q.tiles_n[1];
+        const float w = q.KB[1] * (q.nt[1] == 128 ? 0.65f : 1.f) + 4.f;
+        for (q.splits = 1; q.splits <= 8; ++q.splits) {
+            if (q.splits > 1 && (q.KB[0] / q.splits < 8 || tiles * q.splits > P)) break;
+            q.items = tiles * q.splits;
+            const float x = (q.KB[0] + q.splits - 1) / q.splits * (q.nt[0] == 128 ? 0.65f : 1.f) + 4.f;
+            const int64_t rounds = q.items / P, last = q.items % P;
+            q.w_first = last ? static_cast<int>(x / w + 0.5f) : 0;
+            const int64_t early = last ? std::min<int64_t>(q.w_first * (P - last), q.w_items) : 0;
+            const int64_t early_rounds = early ? (early + P - last - 1) / (P - last) : 0;
+            const float cost = rounds * x + std::max(last ? x : 0.f, early_rounds * w) +
+                               static_cast<float>((q.w_items - early + P - 1) / P) * w + (q.splits > 1 ? 12.f : 0.f);
+            if (least < 0 || cost < least) least = cost, best = q;
+        }
+    }
+    return best;
 }
 
 std::mutex g_mu;
@@ -596,19 +671,18 @@ bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms) {
     return M > 65535 * 128 || us < ffn_stream_us(mx4, gated, M, N, K, sms);
 }
 
-size_t ffn_tile_scratch(int form, int M, int N, int K, int sms) {
-    if (form != TILE_DX) return 0;
-    const int KB = 2 * cdiv(K, 64);
-    const int s = dx_splits(M, N, tile_columns(form, M, N, KB, sms), KB, sms);
-    return s > 1 ? static_cast<size_t>(s) * M * N * sizeof(float) : 0;
+size_t ffn_backward_scratch(int T, int F, int K, int sms) {
+    const int s = backward_plan(T, F, K, sms).splits;
+    return s > 1 ? static_cast<size_t>(s) * T * K * sizeof(float) : 0;
 }
 
 cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t s) {
     const bool mx4 = a.form == TILE_MX4 || a.form == TILE_MX4_GATED;
     const bool gated = a.form == TILE_GATED || a.form == TILE_MX4_GATED;
+    const bool backward = a.form == TILE_BACKWARD;
     using Fn = void (*)(TileMaps, TileParams);
     static const Fn kernels[] = {ffn_tile_kernel<TILE_GATED>, ffn_tile_kernel<TILE_MX4_GATED>,
-                                 ffn_tile_kernel<TILE_MX4>, ffn_tile_kernel<TILE_DX>, ffn_tile_kernel<TILE_DW>};
+                                 ffn_tile_kernel<TILE_MX4>, ffn_tile_kernel<TILE_BACKWARD>};
     cudaError_t e = cudaSuccess;
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -621,37 +695,50 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
         }
     }
     TileParams p = {};
-    p.y0 = static_cast<uint16_t *>(a.y0);
-    p.y1 = static_cast<uint16_t *>(a.y1);
+    p.y[0] = static_cast<uint16_t *>(a.y0);
+    p.y[1] = static_cast<uint16_t *>(a.y1);
+    p.y[2] = static_cast<uint16_t *>(a.y2);
     p.g = a.g;
     p.u = a.u;
     p.ldy = a.ldy;
     p.ws = a.ws;
     p.err = a.err;
-    p.M = a.M;
-    p.N = a.N;
     p.K = a.K;
-    p.KB1 = mx4 ? cdiv(a.K, 256) : cdiv(a.K, 64);
-    p.KB = a.form == TILE_DX ? 2 * p.KB1 : p.KB1;
-    p.nt = tile_columns(a.form, a.M, a.N, p.KB, d.sms);
-    p.tiles_m = cdiv(a.M, kTile);
-    p.tiles_n = cdiv(a.N, gated ? p.nt / 2 : p.nt);
-    p.splits = a.form == TILE_DX ? dx_splits(a.M, a.N, p.nt, p.KB, d.sms) : 1;
-    const int64_t items = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits * (a.form == TILE_DW ? 2 : 1);
-    if (items > 0x7FFFFFFF || (p.splits > 1 && !a.ws)) return cudaErrorInvalidValue;
+    p.splits = 1;
+    int64_t items = 0, w_items = 0;
+    if (backward) {
+        const BackwardPlan q = backward_plan(a.M, a.N, a.K, d.sms);
+        for (int i = 0; i < 2; ++i)
+            p.set[i] = {i ? a.N : a.M, a.K, q.tiles_m[i], q.tiles_n[i], q.nt[i], q.KB[i],
+                        idesc_f16(a.dtype, 256, q.nt[i], i == 1, true)};
+        items = q.items;
+        w_items = q.w_items;
+        p.splits = q.splits;
+        p.w_first = q.w_first;
+        p.KB1 = q.KB[0] / 2;
+    } else {
+        TileSet &t = p.set[0];
+        t.M = a.M;
+        t.N = a.N;
+        t.KB = mx4 ? cdiv(a.K, 256) : cdiv(a.K, 64);
+        t.nt = tile_columns(a.form, a.M, a.N, t.KB, d.sms);
+        t.tiles_m = cdiv(a.M, kTile);
+        t.tiles_n = cdiv(a.N, gated ? t.nt / 2 : t.nt);
+        t.idesc = mx4 ? idesc_mxf4(256, t.nt) : idesc_f16(a.dtype, 256, t.nt);
+        items = static_cast<int64_t>(t.tiles_m) * t.tiles_n;
+    }
+    if (items + w_items > (1 << 30) || (p.splits > 1 && !a.ws)) return cudaErrorInvalidValue;
     p.items = static_cast<int>(items);
+    p.w_items = static_cast<int>(w_items);
     p.kt_n = static_cast<int>(mx4_ktiles(a.K));
     p.act = a.act;
     p.dtype = a.dtype;
     // the widest store that every row's 32-column pieces allow: of y, and of g and u
     // (stride N, 16-byte aligned)
-    const uintptr_t starts = reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1) |
-                             static_cast<uintptr_t>(a.ldy * 2);
+    const uintptr_t starts = reinterpret_cast<uintptr_t>(a.y0) | static_cast<uintptr_t>(a.ldy * 2);
     p.vec = starts % 32 == 0 ? 2 : starts % 16 == 0 ? 1 : 0;
     p.pairs = starts % 4 == 0;
     p.vec_gu = a.N % 4 == 0;
-    p.idesc = mx4 ? idesc_mxf4(256, p.nt)
-                  : idesc_f16(a.dtype, 256, p.nt, a.form == TILE_DW, a.form == TILE_DW || a.form == TILE_DX);
 
     TileMaps tm = {};
     auto map = [&](CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows, int box_cols,
@@ -661,8 +748,8 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     if (mx4) {
         const int64_t pitch = mx4_pitch(a.K);
         map(&tm.a0, a.qa.codes, a.M, pitch, pitch, 128, 128, kMapU8);
-        map(&tm.b0, a.qb0.codes, a.N, pitch, pitch, p.nt / 2, 128, kMapU8);
-        if (gated) map(&tm.b1, a.qb1.codes, a.N, pitch, pitch, p.nt / 2, 128, kMapU8);
+        map(&tm.b0, a.qb0.codes, a.N, pitch, pitch, p.set[0].nt / 2, 128, kMapU8);
+        if (gated) map(&tm.b1, a.qb1.codes, a.N, pitch, pitch, p.set[0].nt / 2, 128, kMapU8);
         auto scales = [&](CUtensorMap *m, const Mx4Mat &q, int rows) {
             if (e == cudaSuccess)
                 e = ffn_scale_map(m, q.scales, static_cast<int64_t>(cdiv(rows, 128)) * p.kt_n);
@@ -672,34 +759,33 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
         if (gated) scales(&tm.sb1, a.qb1, a.N);
     } else if (a.form == TILE_GATED) {
         map(&tm.a0, a.A0, a.M, a.K, a.lda, 128, 64, a.dtype);
-        map(&tm.b0, a.B0, a.N, a.K, a.ldb0, p.nt / 2, 64, a.dtype);
-        map(&tm.b1, a.B1, a.N, a.K, a.ldb1, p.nt / 2, 64, a.dtype);
-    } else if (a.form == TILE_DX) {
-        map(&tm.a0, a.A0, a.M, a.K, a.lda, 128, 64, a.dtype);
-        map(&tm.a1, a.A1, a.M, a.K, a.lda, 128, 64, a.dtype);
-        map(&tm.b0, a.B0, a.K, a.N, a.ldb0, 64, 64, a.dtype);
-        map(&tm.b1, a.B1, a.K, a.N, a.ldb1, 64, 64, a.dtype);
+        map(&tm.b0, a.B0, a.N, a.K, a.ldb0, p.set[0].nt / 2, 64, a.dtype);
+        map(&tm.b1, a.B1, a.N, a.K, a.ldb1, p.set[0].nt / 2, 64, a.dtype);
     } else {
-        map(&tm.a0, a.A0, a.K, a.M, a.lda, 64, 64, a.dtype);
-        map(&tm.a1, a.A1, a.K, a.M, a.lda, 64, 64, a.dtype);
-        map(&tm.b0, a.B0, a.K, a.N, a.ldb0, 64, 64, a.dtype);
+        map(&tm.a0, a.A0, a.M, a.N, a.lda, 128, 64, a.dtype);
+        map(&tm.a1, a.A1, a.M, a.N, a.lda, 128, 64, a.dtype);
+        map(&tm.b0, a.B0, a.N, a.K, a.ldb0, 64, 64, a.dtype);
+        map(&tm.b1, a.B1, a.N, a.K, a.ldb1, 64, 64, a.dtype);
+        map(&tm.aw0, a.A0, a.M, a.N, a.lda, 64, 64, a.dtype);
+        map(&tm.aw1, a.A1, a.M, a.N, a.lda, 64, 64, a.dtype);
+        map(&tm.bw, a.X, a.M, a.K, a.ldx, 64, 64, a.dtype);
+        if (p.splits == 1) map(&tm.y[0], a.y0, a.M, a.K, a.ldy, 32, 64, a.dtype);
+        map(&tm.y[1], a.y1, a.N, a.K, a.ldy, 32, 64, a.dtype);
+        map(&tm.y[2], a.y2, a.N, a.K, a.ldy, 32, 64, a.dtype);
     }
-    p.copy_out = !mx4 && p.vec != 0 && p.splits == 1;
+    p.copy_out = a.form == TILE_GATED && p.vec != 0;
     if (p.copy_out) {
-        const int out_n = gated ? p.nt / 2 : p.nt;
+        const int out_n = p.set[0].nt / 2;
         const int first = first_half(out_n);
-        for (int i = 0; i < 2; ++i) {
-            const int cols = !gated ? 64 : i ? out_n - first : first;
-            const void *y = a.form == TILE_DW && i ? a.y1 : a.y0;
-            if (cols && (i == 0 || gated || a.form == TILE_DW)) map(&tm.y[i], y, a.M, a.N, a.ldy, 32, cols, a.dtype, cols == 64);
-        }
+        map(&tm.y[0], a.y0, a.M, a.N, a.ldy, 32, first, a.dtype, first == 64);
+        if (out_n > first) map(&tm.y[1], a.y0, a.M, a.N, a.ldy, 32, out_n - first, a.dtype, out_n - first == 64);
     }
     if (e != cudaSuccess) return e;
 
     size_t smem = 0;
     if ((e = ffn_smem_for_tmem(d.dev, 512, stages(mx4) * stage_bytes(mx4) + out_bytes(mx4) + 1024 + kBarBytes, &smem)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2u * static_cast<unsigned>(std::min(p.items, d.sms / 2)), 1, 1);
+    cfg.gridDim = dim3(2u * static_cast<unsigned>(std::min(p.items + p.w_items, d.sms / 2)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -710,9 +796,9 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     cfg.numAttrs = a.pdl ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, kernels[a.form], tm, p)) != cudaSuccess) return e;
     if (p.splits > 1) {
-        const int64_t n = static_cast<int64_t>(a.M) * a.N;
+        const int64_t n = static_cast<int64_t>(a.M) * a.K;
         const int blocks = static_cast<int>(std::min<int64_t>((n / 4 + 255) / 256, static_cast<int64_t>(d.sms) * 8));
-        join_kernel<<<blocks, 256, 0, s>>>(a.ws, n, p.splits, p.y0, a.dtype);
+        join_kernel<<<blocks, 256, 0, s>>>(a.ws, n, p.splits, p.y[0], a.dtype);
         e = cudaGetLastError();
     }
     return e;
