@@ -413,8 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const bool mine = elect_one();
             // The tensor cores keep next to no MMAs queued, so what this thread
             // does between two stages is time lost. Stage and phase are counted
-            // on, and the next stage is waited for (and its scales are sent to
-            // TMEM) before the last MMA of this one is issued.
+            // on, and the next stage is waited for before the last MMA of this one
+            // is issued; in 4 bits before the first, since its scales' way to TMEM
+            // then passes under all four (4096 x 4096 x 7168: after 3, 2, 1 and 0 MMAs
+            // 51.0, 48.1, 45.9 and 44.8 us; 16-bit gated 126.6, 126.5, 126.4, 127.8).
+            // Two stages ahead cost more than it gave.
+            constexpr int kBefore = kMx4 ? 0 : 3;
             int stage = 0, as = 0;
             uint32_t phase = 0, aphase = 1;
             auto prepare = [&](int s, uint32_t ph) {
@@ -464,11 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                             pair_mma_f16(d, ad + kk * (a_mn ? 128 : 2), bd + kk * (kBwd ? 128 : 2), idesc, more);
                     };
 #pragma unroll
-                    for (int kk = 0; kk < 3; ++kk)
-                        if (kk < steps - 1) mma(kk);
+                    for (int kk = 0; kk < kBefore; ++kk) mma(kk);
                     if (++stage == kStages) stage = 0, phase ^= 1;
                     if (kb + 1 < it.kb1 || more_items) prepare(stage, phase);
-                    mma(steps - 1);
+#pragma unroll
+                    for (int kk = kBefore; kk < 4; ++kk)
+                        if (kk < steps) mma(kk);
                     if (mine) pair_commit(bar);
                 }
                 if (mine) pair_commit(smem_u32(accf + as));
