@@ -18,11 +18,11 @@
 // Bound: HBM, and at a single token the fixed 4 to 5 us of a launch with clusters
 // and a two-step sum: T = 1, F = 2048, K = 7168 reads 58.7 MB in 13.3 us (4.4 TB/s,
 // of 6.8 measured), F = 4096 117 MB in 21.4 (5.5 TB/s), in 4 bits N = 4096 15.7 MB in
-// 7.7.
+// 7.5.
 //
-// Up to 8 tokens the 4-bit forms also quantise x themselves: of each stage one warp
-// turns the 256 columns of every token into the operand and scale tile that a copy
-// would have brought (T = 1, N = 4096, K = 7168: 7.7 us on the device against 8.0 with a
+// Up to 8 tokens the 4-bit forms also quantise x themselves: warps 2 .. 5 turn a
+// stage's 256 columns of two tokens each into the operand and scale tile that a copy
+// would have brought (T = 1, N = 4096, K = 7168: 7.5 us on the device against 8.0 with a
 // launch for x, 12 us against 20 from Python, which then allocates nothing but y).
 //
 // Warp 0: copies; warp 1: TMEM and MMA; warps 2 .. 5: x in 4 bits (few tokens),
@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(full + s), quantises ? 2 : 1);   // the copies, the quantising warp
+            // the copies, and the warps that quantise a token
+            mbar_init(smem_u32(full + s), quantises ? 1 + static_cast<uint32_t>(min(Mloc, 4)) : 1u);
             mbar_init(smem_u32(empty + s), 1);
         }
         mbar_init(smem_u32(accf), 1);
@@ -225,42 +226,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         if constexpr (kMx4) {
             if (quantises) {
+                // Warp 2 + w has tokens w and w + 4 of every stage, eight rows of 256
+                // columns loaded at a time. It sees every round of every buffer, so it
+                // is never two phases behind the barrier that it waits on.
                 auto run = [&](auto zero) {
                     using T = decltype(zero);
-                    // A buffer belongs to one warp, which sees all of its rounds: it is
-                    // never two phases behind the barrier that it waits on.
-                    for (int s = 0; s < n_st; ++s) {
-                        const int stage = s % S;
-                        if ((stage & 3) != warp - 2) continue;
-                        if (s >= S)
-                            mbar_wait_bounded(smem_u32(empty + stage), static_cast<uint32_t>((s / S - 1) & 1), abort_flag,
-                                              p.err, DEV_TIMEOUT_EMPTY);
-                        const int c = (kb0 + s) * 256 + lane * 8;
-                        Eight<T> e[kFewTok];
+                    const int w = warp - 2;
+                    const int lg = w + 4 < Mloc ? 1 : 0;     // log2 of its tokens
+                    const int units = w < Mloc ? n_st << lg : 0;
+                    int stage = 0;
+                    uint32_t phase = 1;   // of a buffer's round before: passes at once in the first
+                    for (int u0 = 0; u0 < units; u0 += 8) {
+                        Eight<T> e[8];
 #pragma unroll
-                        for (int r = 0; r < kFewTok; ++r) {
-                            const T *row = static_cast<const T *>(p.x) + (m0 + min(r, Mloc - 1)) * p.ldx;
+                        for (int i = 0; i < 8; ++i) {
+                            const int u = min(u0 + i, units - 1);
+                            const T *row = static_cast<const T *>(p.x) + (m0 + w + 4 * (u & lg)) * p.ldx;
+                            const int c = (kb0 + (u >> lg)) * 256 + lane * 8;
                             if (p.x_vec && c + 8 <= p.K)
-                                e[r].load_full(row + c);
+                                e[i].load_full(row + c);
                             else
-                                e[r].load(row, c, p.K);
+                                e[i].load(row, c, p.K);
                         }
-                        uint8_t *x8 = gbase + static_cast<size_t>(stage) * p.stage_bytes + L::w_bytes;
-                        uint8_t *sc = gbase + static_cast<size_t>(stage) * p.stage_bytes + L::off_sc(p.Mpad) + kAcc * 1024;
 #pragma unroll
-                        for (int r = 0; r < kFewTok; ++r) {
-                            if (r >= Mloc) break;
+                        for (int i = 0; i < 8; ++i) {
+                            if (u0 + i >= units) break;
+                            const int r = w + 4 * ((u0 + i) & lg);
+                            mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
+                            uint8_t *x8 = gbase + static_cast<size_t>(stage) * p.stage_bytes + L::w_bytes;
+                            uint8_t *sc = gbase + static_cast<size_t>(stage) * p.stage_bytes + L::off_sc(p.Mpad) + kAcc * 1024;
                             uint32_t b;
-                            const uint32_t q = quantize8(e[r], b);
+                            const uint32_t q = quantize8(e[i], b);
                             // row r of the 128-byte swizzled operand, lane r of the scale tile
                             *reinterpret_cast<uint32_t *>(x8 + r * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4) = q;
                             if ((lane & 3) == 0)
                                 sc[(lane >> 4) * 512 + r * 16 + ((lane >> 2) & 3)] = static_cast<uint8_t>(b);
+                            if (((u0 + i) & lg) == lg) {   // the warp's last token of the stage
+                                // the tensor cores read it through the asynchronous proxy
+                                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(smem_u32(full + stage));
+                                if (++stage == S) stage = 0, phase ^= 1;
+                            }
                         }
-                        // the tensor cores read it through the asynchronous proxy
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(full + stage));
                     }
                 };
                 if (p.dtype == KP_FP16)
