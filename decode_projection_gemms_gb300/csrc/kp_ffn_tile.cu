@@ -30,9 +30,9 @@
 //
 // Bound: the tensor cores, which are busy 87 % of the time in the gated form (4003 x
 // 2048 x 7168, 127 us, 1.85 PFLOP/s: the measured library rate is 1.88), 90 % in the
-// backward pass and 47 % in 4 bits (4096 x 4096 x 7168, 50 us, 4.8 PFLOP/s; there four
-// rounds of tiles hold 3.4 rounds of work, the scale copies take 12 %, the
-// accumulator's way out 8 %).
+// backward pass and about 53 % in 4 bits (4096 x 4096 x 7168, 45 us, 5.3 PFLOP/s;
+// there four rounds of tiles hold 3.4 rounds of work, and the accumulator's way out
+// takes 9 %).
 //
 // Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 9: epilogue.
 #include <algorithm>
@@ -198,7 +198,7 @@ __device__ __forceinline__ void put_odd_rows32(uint16_t *dst, int64_t ld, const 
         uint16_t *d = dst + 16 * h;
         if (pairs) {
             const int c = 2 * (lane & 7);
-#pragma unroll 2
+#pragma unroll
             for (int r = lane >> 3; r < 32; r += 4) {
                 uint32_t two;
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(two) : "r"(box + r * kOutPitch + 2 * c) : "memory");
@@ -210,7 +210,7 @@ __device__ __forceinline__ void put_odd_rows32(uint16_t *dst, int64_t ld, const 
             }
         } else {
             const int c = lane & 15;
-#pragma unroll 2
+#pragma unroll 4
             for (int r = lane >> 4; r < 32; r += 2) {
                 uint16_t one;
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(one) : "r"(box + r * kOutPitch + 2 * c) : "memory");
