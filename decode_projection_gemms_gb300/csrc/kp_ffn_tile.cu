@@ -97,7 +97,7 @@ struct TileParams {
     int kt_n;             // 4-bit: scale tiles per row tile
     int act, dtype, vec, vec_gu;
     int pairs;            // y's rows start on 4 bytes
-    int copy_out;         // y's rows allow copies from shared memory (16-byte rows)
+    int copy_out;         // y's rows allow copies from shared memory (16-byte starts and lengths)
 };
 
 // ---- cta_group::2 forms ----------------------------------------------------------
@@ -784,7 +784,8 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
         map(&tm.y[1], a.y1, a.N, a.K, a.ldy, 32, 64, a.dtype);
         map(&tm.y[2], a.y2, a.N, a.K, a.ldy, 32, 64, a.dtype);
     }
-    p.copy_out = a.form == TILE_GATED && p.vec != 0;
+    // whole 16-byte pieces only: a copy's last piece reaches past a row end within one
+    p.copy_out = a.form == TILE_GATED && p.vec != 0 && a.N % 8 == 0;
     if (p.copy_out) {
         const int out_n = p.set[0].nt / 2;
         const int first = first_half(out_n);

@@ -385,20 +385,24 @@ def test_operators_share_the_gpu_across_streams():
     quiet()
 
 
-@pytest.mark.parametrize("T", [5, 70, 300])
-def test_nothing_is_written_outside_the_outputs(T):
-    F, K = 203, 264
+@pytest.mark.parametrize("T", [5, 70, 300, 1100])
+@pytest.mark.parametrize("F,first,width", [(203, 30, 264), (203, 32, 264), (512, 32, 576), (720, 16, 752), (1000, 8, 1021)])
+def test_nothing_is_written_outside_the_outputs(T, F, first, width):
+    """Outputs as views into wider matrices, whose rows start on 32, 16, 4 or 2
+    bytes: both kernels, tiles that end inside and outside the columns."""
+    K = 264
     x, Wg, Wu = normal(T, K, 1, torch.bfloat16), normal(F, K, 2, torch.bfloat16), normal(F, K, 3, torch.bfloat16)
     q = kda.mx4_quantize(Wg)
     for run in (lambda y: kda.gated_ffn(x, Wg, Wu, h=y), lambda y: kda.mx4_gated_ffn(x, q, q, h=y),
                 lambda y: kda.mx4_gemm(x, q, y=y)):
-        guard = torch.full((T + 40, F + 61), 9.0, dtype=torch.bfloat16, device="cuda")
-        y = guard[20:20 + T, 30:30 + F]
+        want = run(None)
+        guard = torch.full((T + 40, width), 9.0, dtype=torch.bfloat16, device="cuda")
+        y = guard[20:20 + T, first:first + F]
         y.fill_(math.nan)
         run(y)
-        assert torch.isfinite(y).all()
+        assert torch.equal(y, want)
         keep = torch.ones_like(guard, dtype=torch.bool)
-        keep[20:20 + T, 30:30 + F] = False
+        keep[20:20 + T, first:first + F] = False
         assert (guard[keep] == 9.0).all()
     quiet()
 
