@@ -210,7 +210,7 @@ __device__ __forceinline__ uint32_t mul2(uint32_t v, uint32_t s) {
     return a.u;
 }
 
-// bf16 values to the output type: one, or V of them in one store of 16 or 8 bytes.
+// bf16 values to the output type: one, or 16 bytes of them in stores of kPiece bytes.
 template <typename T>
 __device__ __forceinline__ void store_one(T *dst, uint32_t bf16) {
     if constexpr (sizeof(T) == 4)
@@ -219,38 +219,42 @@ __device__ __forceinline__ void store_one(T *dst, uint32_t bf16) {
         *reinterpret_cast<uint16_t *>(dst) =
             __is_same(T, __half) ? elem_round<KP_FP16>(bf16lo(bf16)) : static_cast<uint16_t>(bf16);
 }
-template <typename T, int V>
+template <typename T, int kPiece>
 __device__ __forceinline__ void store_word(T *dst, const uint32_t (&h)[4]) {
+    uint32_t o[4];
     if constexpr (sizeof(T) == 4) {
-        if constexpr (V == 4)
-            *reinterpret_cast<float4 *>(dst) = make_float4(bf16lo(h[0]), bf16hi(h[0]), bf16lo(h[1]), bf16hi(h[1]));
-        else
-            *reinterpret_cast<float2 *>(dst) = make_float2(bf16lo(h[0]), bf16hi(h[0]));
+        o[0] = h[0] << 16, o[1] = h[0] & 0xFFFF0000u, o[2] = h[1] << 16, o[3] = h[1] & 0xFFFF0000u;
     } else {
-        uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k)
+        for (int k = 0; k < 4; ++k)
             o[k] = __is_same(T, __half) ? elem_round<KP_FP16>(bf16lo(h[k])) |
                                               static_cast<uint32_t>(elem_round<KP_FP16>(bf16hi(h[k]))) << 16
                                         : h[k];
-        if constexpr (V == 8)
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-        else
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(o[0], o[1]);
+    }
+    if constexpr (kPiece == 16) {
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else if constexpr (kPiece == 8) {
+        reinterpret_cast<uint2 *>(dst)[0] = make_uint2(o[0], o[1]);
+        reinterpret_cast<uint2 *>(dst)[1] = make_uint2(o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) reinterpret_cast<uint32_t *>(dst)[k] = o[k];
     }
 }
 
-// A warp takes 1024 columns of a row, a lane the V columns of one store of every
-// 32 V: 16 bytes, or 8 where rows are only 8-byte aligned (8191 x 7156 in bf16: 33
-// us against 42 with the shifts below). kShift: rows may start anywhere; the
-// columns before a row's first 16-byte boundary (h of them) are stored one by one,
-// and the V columns of a store start inside a code word and may straddle two
-// blocks (4096 x 7167 in bf16: 19 us against 48 with 2-byte stores).
+// A warp takes 1024 columns of a row, a lane the V columns of 16 bytes of every 32 V,
+// in stores of kPiece bytes: as wide as the rows' starts allow (8191 x 7156 in bf16,
+// rows of 14312 bytes: 28 us in two stores a lane, 32 with 8 bytes a lane, 42 with the
+// shifts below; 4096 x 7166 in four stores 16 us, with shifts 19). kShift, for 16-bit
+// rows that start on 2 bytes: the columns before a row's first 16-byte boundary (h of
+// them) are stored one by one, and the V columns of a store start inside a code word and
+// may straddle two blocks (4096 x 7167: 19 us, with eight 2-byte stores a lane 87).
 constexpr int kDqSpan = 1024;
-template <typename T, int V, bool kShift>
+template <typename T, int kPiece, bool kShift>
 __global__ void __launch_bounds__(kQThreads)
     mx4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int rows,
                           int cols, T *__restrict__ y, int64_t ldy) {
+    constexpr int V = 16 / sizeof(T);
     constexpr int kSteps = kDqSpan / (32 * V);
     const int lane = threadIdx.x & 31;
     const int nb = (cols + 31) >> 5;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kQThreads)
                 for (int k = 0; k < V / 2; ++k) v[k] = mul2(v[k], a | a << 16);
             }
             if (c + V <= cols) {
-                store_word<T, V>(row + c, v);
+                store_word<T, kPiece>(row + c, v);
             } else {
 #pragma unroll
                 for (int k = 0; k < V; ++k)
@@ -356,14 +360,15 @@ void dequantize_go(const uint8_t *codes, const uint8_t *scales, int rows, int co
                    cudaStream_t s) {
     T *p = static_cast<T *>(y);
     const int grid = grid_for(static_cast<int64_t>(rows) * ((cols + kDqSpan - 1) / kDqSpan), sms, 8);
-    constexpr int kMost = 16 / sizeof(T);
     const uintptr_t starts = reinterpret_cast<uintptr_t>(y) | static_cast<uintptr_t>(ldy * sizeof(T));
     if (starts % 16 == 0)
-        mx4_dequantize_kernel<T, kMost, false><<<grid, kQThreads, 0, s>>>(codes, scales, rows, cols, p, ldy);
+        mx4_dequantize_kernel<T, 16, false><<<grid, kQThreads, 0, s>>>(codes, scales, rows, cols, p, ldy);
     else if (starts % 8 == 0)
-        mx4_dequantize_kernel<T, kMost / 2, false><<<grid, kQThreads, 0, s>>>(codes, scales, rows, cols, p, ldy);
-    else
-        mx4_dequantize_kernel<T, kMost, true><<<grid, kQThreads, 0, s>>>(codes, scales, rows, cols, p, ldy);
+        mx4_dequantize_kernel<T, 8, false><<<grid, kQThreads, 0, s>>>(codes, scales, rows, cols, p, ldy);
+    else if (sizeof(T) == 4 || starts % 4 == 0)
+        mx4_dequantize_kernel<T, 4, false><<<grid, kQThreads, 0, s>>>(codes, scales, rows, cols, p, ldy);
+    else if constexpr (sizeof(T) == 2)
+        mx4_dequantize_kernel<T, 16, true><<<grid, kQThreads, 0, s>>>(codes, scales, rows, cols, p, ldy);
 }
 
 }  // namespace
