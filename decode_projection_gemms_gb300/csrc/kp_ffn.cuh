@@ -26,9 +26,10 @@ struct FfnDev {
 };
 int ffn_device(FfnDev *out);   // KP_OK, or a status with the message set (KP_EDEVICE included)
 
-// Tensor map of a row-major matrix of 16-bit elements (KP_BF16, KP_FP16) or of
-// bytes (kMapU8), box_cols x box_rows, 128-byte swizzle or none, zero fill outside.
-constexpr int kMapU8 = 16;
+// Tensor map of a row-major matrix of 16-bit elements (KP_BF16, KP_FP16), of
+// fp32 (kMapF32) or bytes (kMapU8), box_cols x box_rows, 128-byte swizzle or none, zero
+// fill outside.
+constexpr int kMapU8 = 16, kMapF32 = 17;
 cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld,
                            int box_rows, int box_cols, int dtype, bool swizzle = true);
 // The scale tiles of a microscaled matrix, 512 bytes each, boxes of two.

@@ -38,12 +38,13 @@ cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int6
     EncodeFn enc;
     cudaError_t e = encoder(&enc);
     if (e != cudaSuccess) return e;
-    const cuuint64_t es = dtype == kMapU8 ? 1 : 2;
+    const cuuint64_t es = dtype == kMapU8 ? 1 : dtype == kMapF32 ? 4 : 2;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType t = dtype == kMapU8    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                  : dtype == kMapF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                   : dtype == KP_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUresult r = enc(map, t, 2, const_cast<void *>(ptr), dims, strides, box, estr,

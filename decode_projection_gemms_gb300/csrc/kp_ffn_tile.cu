@@ -71,6 +71,7 @@ struct TileMaps {
     CUtensorMap a0, a1, b0, b1, sa, sb0, sb1;
     CUtensorMap aw0, aw1, bw;   // backward: operands of the weights' gradients
     CUtensorMap y[3];           // outputs: gated, of the tile's two halves; backward, dx, dWg, dWu
+    CUtensorMap g, u;           // gated: the two products in fp32
 };
 
 // The tiles of one output shape.
@@ -232,6 +233,15 @@ __device__ __forceinline__ void put_box32(uint32_t row, const uint32_t (&w)[16],
                      "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
                      : "memory");
     }
+}
+
+// 32 fp32 sums into a swizzled row of a warp's box.
+__device__ __forceinline__ void put_box_sums32(uint32_t row, const float (&v)[32], int lane) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((i ^ (lane & 7)) << 4)), "f"(v[4 * i]),
+                     "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
+                     : "memory");
 }
 
 // Outputs of a tile's columns that the first four epilogue warps take.
@@ -488,6 +498,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int q = warp & 3;
         const int half = warp >= 6;
         const uint32_t box = base + kStages * kStage + static_cast<uint32_t>(warp - 2) * out_box(kMx4);
+        auto take_box = [&]() {   // the last copy has read it
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+        };
+        auto send_box = [&](const CUtensorMap *map, int n, int m) {   // rows and columns past the output's are left out
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                    "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                    "r"(n), "r"(m), "r"(box)
+                    : "memory");
+        };
         int as = 0;
         uint32_t aphase = 0;
         Item it;
@@ -516,10 +540,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int left = min(N - n, (half ? it.out_n : span) - at);
                 if (left <= 0) break;
                 const bool copy_out = kBwd ? it.set || p.splits == 1 : !kMx4 && p.copy_out;
-                if (copy_out) {   // the last copy has read the buffer
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    __syncwarp();
+                if (kForm == TILE_GATED && p.g) {
+                    // g and u through the box as well, 32 columns at a time (2046 x 3216 x 328:
+                    // 25.7 us, with stores of 16 bytes from each lane 32.8; three boxes a
+                    // warp for two stages less 23.5, but 4096 x 2048 x 7168 131.7 -> 158)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {   // two pieces of g, two of u
+                        const int c = 32 * (k & 1);
+                        if (c >= left) continue;
+                        float a[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(v[k][j]);
+                        if (copy_out && (half ? it.out_n : span) - at >= c + 32) {
+                            take_box();
+                            put_box_sums32(box + lane * 128, a, lane);
+                            send_box(k < 2 ? &tm.g : &tm.u, n + c, m_first);
+                        } else if (m < M) {
+                            put_sums32((k < 2 ? p.g : p.u) + m * N + n + c, a, left - c, p.vec_gu);
+                        }
+                    }
                 }
+                if (copy_out) take_box();
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (32 * k >= left) break;
@@ -531,10 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         float b[32], h[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) b[j] = __uint_as_float(v[2 + k][j]);
-                        if (!kMx4 && p.g && m < M) {
-                            put_sums32(p.g + m * N + n + 32 * k, a, left - 32 * k, p.vec_gu);
-                            put_sums32(p.u + m * N + n + 32 * k, b, left - 32 * k, p.vec_gu);
-                        }
                         ffn_gate(a, b, p.act, h);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) a[j] = h[j];
@@ -557,17 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         }
                     }
                 }
-                if (copy_out) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0)   // rows and columns past the output's are left out
-                        asm volatile(
-                            "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
-                            "cp.async.bulk.commit_group;" ::"l"(
-                                reinterpret_cast<uint64_t>(&tm.y[kGated ? half : it.set ? 1 + it.z : 0])),
-                            "r"(n), "r"(m_first), "r"(box)
-                            : "memory");
-                }
+                if (copy_out) send_box(&tm.y[kGated ? half : it.set ? 1 + it.z : 0], n, m_first);
             }
         }
         if (!kMx4 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -791,6 +818,10 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
         const int first = first_half(out_n);
         map(&tm.y[0], a.y0, a.M, a.N, a.ldy, 32, first, a.dtype, first == 64);
         if (out_n > first) map(&tm.y[1], a.y0, a.M, a.N, a.ldy, 32, out_n - first, a.dtype, out_n - first == 64);
+        if (a.g) {
+            map(&tm.g, a.g, a.M, a.N, a.N, 32, 32, kMapF32);
+            map(&tm.u, a.u, a.M, a.N, a.N, 32, 32, kMapF32);
+        }
     }
     if (e != cudaSuccess) return e;
 
