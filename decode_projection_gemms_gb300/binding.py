@@ -652,11 +652,11 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu: 
     code = _act_code(act)
     T, F, K, ldx, ldg, ldu, dt = _gated_operands(x, Wg, Wu, index)
     lddh = _rows(dh, "dh", dt, index)
+    for t, name in ((g, "g"), (u, "u")):
+        _rows(t, name, torch.float32 if T else None, index)   # with no tokens nothing is read
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
     for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
-        if t is not dh:
-            _rows(t, name, torch.float32, index)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
         if t.shape != (T, F):
             raise ValueError(f"{name} must be {(T, F)}, got {tuple(t.shape)}")
     dx, dWg, dWu = x.new_empty((T, K)), x.new_empty((F, K)), x.new_empty((F, K))
