@@ -643,8 +643,9 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu: 
     """Gradients ``(dx, dWg, dWu)`` of ``gated_ffn`` for the gradient ``dh`` of its
     output, from its operands and the ``g`` and ``u`` it saved. ``dG = dh u act'(g)``
     and ``dU = dh act(g)`` are computed in fp32 and rounded to x's type as the
-    tensor cores' operands; the three products are summed in fp32. With no tokens
-    the weights' gradients are zero."""
+    tensor cores' operands (in float16 scaled by a power of two, so that neither
+    overflows); the three products are summed in fp32. With no tokens the weights'
+    gradients are zero."""
     index = _here(x, "x", stream)
     if index < 0:
         with _on(x.device, stream, dh, x, Wg, Wu, g, u):

@@ -106,6 +106,7 @@ struct FfnTileArgs {
     float *g = nullptr, *u = nullptr;
     int M = 0, N = 0, K = 0;     // tokens, features, columns of x
     float *ws = nullptr;         // backward: partial sums of dx
+    const float *scale = nullptr;   // backward: device factor of every sum (none: 1)
     bool pdl = false;
     int *err = nullptr;
 };
@@ -116,9 +117,13 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
 bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms);
 
 // dG = dh u act'(g), dU = dh act(g): the gradients of both products, [T, F]
-// with row stride ld (kp_ffn_bwd.cu).
+// with row stride ld (kp_ffn_bwd.cu). scaling (fp16; NULL: none): both come out as
+// multiples of a power of two, whose reciprocal goes to scaling[0]; the rest of its
+// ffn_gate_grad_scratch bytes is the kernels' own.
+size_t ffn_gate_grad_scratch(int sms);
 cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const float *g, const float *u, void *dg, void *du,
-                                 int64_t ld, int T, int F, int act, int dtype, int sms, cudaStream_t s);
+                                 int64_t ld, float *scaling, int T, int F, int act, int dtype, int sms,
+                                 cudaStream_t s);
 
 }  // namespace kp
 

@@ -186,16 +186,18 @@ static Mx4Work mx4_work(bool gated, int M, int N, int K, int sms) {
     return w;
 }
 
-// Backward: dG and dU [T][F rounded up to 8] in 16 bits, then dx's partial sums.
+// Backward: dG and dU [T][F rounded up to 8] in 16 bits, their scaling (fp16), then
+// dx's partial sums.
 struct BwdWork {
-    size_t du, part, bytes;
+    size_t du, scaling, part, bytes;
     int64_t ld;
 };
 static BwdWork bwd_work(int T, int F, int K, int sms) {
     BwdWork w;
     w.ld = (static_cast<int64_t>(F) + 7) / 8 * 8;
     w.du = up256(static_cast<size_t>(T) * w.ld * 2);
-    w.part = 2 * w.du;
+    w.scaling = 2 * w.du;
+    w.part = w.scaling + up256(ffn_gate_grad_scratch(sms));
     w.bytes = w.part + ffn_backward_scratch(T, F, K, sms);
     return w;
 }
@@ -430,7 +432,9 @@ int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t l
     const BwdWork w = bwd_work(T, F, K, d.sms);
     if ((rc = check_workspace(fn, work, work_bytes, w.bytes))) return rc;
     uint8_t *base = static_cast<uint8_t *>(work);
-    cudaError_t e = ffn_gate_grad_launch(dh, lddh, g, u, base, base + w.du, w.ld, T, F, act, dtype, d.sms, stream);
+    float *scaling = dtype == KP_FP16 ? reinterpret_cast<float *>(base + w.scaling) : nullptr;
+    cudaError_t e = ffn_gate_grad_launch(dh, lddh, g, u, base, base + w.du, w.ld, scaling, T, F, act, dtype, d.sms,
+                                         stream);
     if (e != cudaSuccess) return cuda_failed(e, fn);
     FfnTileArgs t;
     t.form = TILE_BACKWARD;
@@ -452,6 +456,7 @@ int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t l
     t.N = F;
     t.K = K;
     t.ws = reinterpret_cast<float *>(base + w.part);
+    t.scale = scaling;
     t.err = d.err;
     if ((e = ffn_tile_launch(t, d, stream)) != cudaSuccess) return cuda_failed(e, fn);
     return KP_OK;

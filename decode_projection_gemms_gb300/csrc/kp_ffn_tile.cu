@@ -89,6 +89,7 @@ struct TileParams {
     float *g, *u;
     int64_t ldy;
     float *ws;
+    const float *scale;   // backward: factor of every sum (none: 1)
     int *err;
     int K;
     int items;            // of set 0: tiles, times the parts of a split contraction
@@ -512,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     "r"(n), "r"(m), "r"(box)
                     : "memory");
         };
+        const float scale = kBwd && p.scale ? __ldg(p.scale) : 1.f;   // a power of two
         int as = 0;
         uint32_t aphase = 0;
         Item it;
@@ -568,6 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     float a[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(v[c][j]);
+                    if constexpr (kBwd)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) a[j] *= scale;
                     if constexpr (kGated) {
                         float b[32], h[32];
 #pragma unroll
@@ -740,6 +745,7 @@ cudaError_t ffn_tile_launch(const FfnTileArgs &a, const FfnDev &d, cudaStream_t 
     p.u = a.u;
     p.ldy = a.ldy;
     p.ws = a.ws;
+    p.scale = a.scale;
     p.err = a.err;
     p.K = a.K;
     p.splits = 1;

@@ -400,6 +400,9 @@ KP_API int kp_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg,
  * in the forward call) and its g and u:
  *   dU = dh act(g), dG = dh u act'(g)   rounded to dtype, as the operands of
  *   dx [T, K] = dG Wg + dU Wu, dWg [F, K] = dG^T x, dWu [F, K] = dU^T x.
+ * In fp16 both are rounded as multiples of one power of two, taken from their largest
+ * finite magnitude m: they do not overflow, and an element is off by 2^-11 of itself or
+ * 2^-39 m, whichever is more.
  * dx, dWg and dWu are contiguous, 16-byte aligned and written, not added to; with
  * T = 0 the weights' gradients are set to zero. */
 KP_API int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx, const void *Wg,
