@@ -132,11 +132,35 @@ cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const float *g, c
 namespace kp {
 
 // ---- activations ------------------------------------------------------------
+// The normal distribution's integral up to g, and e = exp(-g^2 / 2). 1 + erf(g / sqrt 2)
+// cancels for negative g (4 % off at -5, zero from -5.5 on); here the integral from |g|
+// on is e times a polynomial in 1 / (1 + 0.3 |g|), which Mills' ratio is close to: a
+// fit of least relative error over |g| <= 14, 2^-24 off and 2^-21 with fp32's roundings.
+// erfcf gives the same values, but the epilogue of tiles with few K blocks waits for it
+// (2000 x 4096 x 512: 27.8 us with erff, 40.3 with erfcf, 30.2 with this).
+__device__ __forceinline__ float ffn_normal_cdf(float g, float &e) {
+    const float t = __fdividef(1.f, fmaf(0.3f, fabsf(g), 1.f));
+    float p = 0.0383782685f;
+    p = fmaf(p, t, -0.169166028f);
+    p = fmaf(p, t, 0.228659928f);
+    p = fmaf(p, t, -0.0765063167f);
+    p = fmaf(p, t, 0.142535433f);
+    p = fmaf(p, t, 0.0946835577f);
+    p = fmaf(p, t, 0.121920332f);
+    p = fmaf(p, t, 0.119487688f);
+    p = fmaf(p, t, 7.16883596e-06f);
+    e = __expf(-0.5f * g * g);
+    p *= e;
+    return g < 0.f ? p : 1.f - p;
+}
 // act(g), in fp32.
 template <int kAct>
 __device__ __forceinline__ float ffn_act(float g) {
     if constexpr (kAct == KP_ACT_SILU) return __fdividef(g, 1.f + __expf(-g));
-    if constexpr (kAct == KP_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+    if constexpr (kAct == KP_ACT_GELU) {
+        float e;
+        return g * ffn_normal_cdf(g, e);
+    }
     // 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)), z = sqrt(2/pi) (g + 0.044715 g^3)
     const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
     return __fdividef(g, 1.f + __expf(-z2));
@@ -165,7 +189,10 @@ __device__ __forceinline__ void ffn_act_grad(float g, float &a, float &da) {
         const float s = __fdividef(1.f, 1.f + __expf(-g));
         da = s * (1.f + g * (1.f - s));
     } else if constexpr (kAct == KP_ACT_GELU) {
-        da = 0.5f * (1.f + erff(g * 0.70710678118654752f)) + g * 0.39894228040143268f * __expf(-0.5f * g * g);
+        float e;
+        const float cdf = ffn_normal_cdf(g, e);
+        a = g * cdf;
+        da = cdf + g * 0.39894228040143268f * e;
     } else {
         // a = g s(w), s the logistic function, w = 2 sqrt(2/pi) (g + 0.044715 g^3)
         const float w = 1.5957691216057308f * (g + 0.044715f * g * g * g);
