@@ -197,7 +197,9 @@ __device__ __forceinline__ void ffn_act_grad(float g, float &a, float &da) {
         // a = g s(w), s the logistic function, w = 2 sqrt(2/pi) (g + 0.044715 g^3)
         const float w = 1.5957691216057308f * (g + 0.044715f * g * g * g);
         const float s = __fdividef(1.f, 1.f + __expf(-w));
-        da = s + g * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * g * g);
+        // from 20 on s (1 - s) is 0, and g^2 need not be finite
+        const float c = fminf(fmaxf(g, -20.f), 20.f);
+        da = s + c * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * c * c);
     }
 }
 

@@ -92,3 +92,20 @@ def test_left_tail_over_4_bits(act, tokens):
     assert torch.equal(mx4_values(x), x.double())
     h = kda.mx4_gated_ffn(x, kda.mx4_quantize(Wg), kda.mx4_quantize(Wu), act=act)
     near(h, act64(g, act)[0][:, None].expand(-1, 130), torch.bfloat16, act)
+
+
+@pytest.mark.parametrize("act", [a for a, _ in LEFT])
+def test_gradients_of_huge_gates(act):
+    """bf16 reaches 3e38, and g^2 and g^3 pass fp32 long before: the activation is then
+    g or 0, its derivative 1 or 0."""
+    g = torch.tensor([s * m for m in (30.0, 1e4, 1e12, 1e15, 1.8e19, 3e19, 1e30, 2e38) for s in (1, -1)],
+                     dtype=torch.float64).to(torch.bfloat16).cuda()
+    x, Wg, Wu = operands(g, 1, 64, torch.bfloat16)
+    dh = torch.ones((g.numel(), 1), dtype=torch.bfloat16, device="cuda")
+    h, gs, us = kda.gated_ffn(x, Wg, Wu, act=act, save=True)
+    dx, _, _ = kda.gated_ffn_backward(dh, x, Wg, Wu, gs, us, act=act)
+    right = g > 0
+    # below 1e-12 on the left: silu's exp(-30) 30 is the largest value there
+    for got, want in ((h[:, 0], g), (dx[:, 32], g), (dx[:, 0], torch.ones_like(g))):
+        assert torch.equal(got[right], want[right])
+        assert (got[~right].abs() < 1e-11).all()
