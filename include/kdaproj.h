@@ -335,7 +335,9 @@ KP_API int kda_proj_destroy(kda_plan *plan);
  * KP_ENODEV, KP_ECUDA, KP_EDEVICE. */
 
 /* Gate activations: g / (1 + e^-g); g (1 + erf(g / sqrt 2)) / 2; and the tanh
- * form of the latter, g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. */
+ * form of the latter, g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. Computed in
+ * fp32 to 2^-13 of their value or better, also where it is small; a factor of g below
+ * 2^-126 counts as zero (silu from g = -87 down). */
 enum kp_act {
     KP_ACT_SILU = 0,
     KP_ACT_GELU = 1,
