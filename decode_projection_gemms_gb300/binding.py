@@ -346,6 +346,8 @@ def _here(t, name: str, stream) -> int:
 def _on(device, stream, *inputs):
     """Make device and stream current. The inputs are marked as used on the
     stream, so memory that is freed meanwhile is not handed out under it."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the operands are on {device}")
     with torch.cuda.device(device):
         if stream is None:
             yield

@@ -86,3 +86,27 @@ def test_backward_without_tokens_reads_no_sums(library):
     p["g"] = p["u"] = p["dh"]
     binding.gated_ffn_backward(**p)
     assert library.calls == ["kp_gated_ffn_backward"]
+
+
+class StreamOf:
+    cuda_stream = 7
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+@pytest.mark.parametrize("op", ["mx4_quantize", "mx4_dequantize", "mx4_gemm", "mx4_gated_ffn", "gated_ffn",
+                                "gated_ffn_backward"])
+def test_refuses_a_stream_of_another_device(library, op):
+    """The work would otherwise run on the operands' device, on a stream that nobody
+    named."""
+    p = backward_operands()
+    q = binding.Mx4Tensor.__new__(binding.Mx4Tensor)
+    q._buf, q._scales, q._index, q.shape, q.device = p["x"], None, 0, (16, 24), torch.device("cuda", 0)
+    q.code_ptr = q.scale_ptr = 256
+    args = {"mx4_quantize": (p["x"],), "mx4_dequantize": (q,), "mx4_gemm": (p["x"], q),
+            "mx4_gated_ffn": (p["x"], q, q), "gated_ffn": (p["x"], p["Wg"], p["Wu"]),
+            "gated_ffn_backward": tuple(p[k] for k in ("dh", "x", "Wg", "Wu", "g", "u"))}[op]
+    with pytest.raises(ValueError, match="stream"):
+        getattr(binding, op)(*args, stream=StreamOf(1))
+    assert library.calls == []
