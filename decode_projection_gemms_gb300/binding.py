@@ -419,7 +419,9 @@ class Mx4Tensor:
     codes and one power-of-two scale per 32 columns (4.25 bits an element), in
     the layout that ``include/kdaproj.h`` describes. Made by ``mx4_quantize``, or
     from stored ``codes`` and ``scales`` (uint8, of the sizes that
-    ``Mx4Tensor.sizes`` gives, 16-byte aligned)."""
+    ``Mx4Tensor.sizes`` gives, 16-byte aligned; codes past the columns and scales of
+    blocks past them must be 0, as ``mx4_quantize`` leaves them, since the products
+    read them)."""
 
     __slots__ = ("_index", "_buf", "_scales", "_code_bytes", "_scale_bytes", "shape", "device", "code_ptr", "scale_ptr")
 

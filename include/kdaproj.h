@@ -365,7 +365,12 @@ KP_API int kp_ffn_workspace(int op, int M, int N, int K, size_t *bytes);
  *   codes   [rows][ceil(cols / 32) * 16] bytes, the lower column in the low
  *           half of a byte; columns past the end are 0
  *   scales  tiles of 128 rows x 4 blocks, 512 bytes each, row tiles outermost;
- *           row r, block b of a tile at byte (r % 32) * 16 + (r / 32) * 4 + b
+ *           row r, block b of a tile at byte (r % 32) * 16 + (r / 32) * 4 + b;
+ *           bytes of blocks past the columns are 0 (the products read them: a NaN
+ *           there, 255, makes whole outputs NaN), those of rows past the end are
+ *           not used
+ * kp_mx4_quantize writes all of both; a matrix that comes from elsewhere has to hold
+ * the same zeros.
  * kp_mx4_bytes gives both sizes (host only). Both pointers are 16-byte aligned. */
 KP_API int kp_mx4_bytes(int rows, int cols, size_t *code_bytes, size_t *scale_bytes);
 /* x [rows, cols] of dtype KP_BF16, KP_FP16 or KP_FP32, aligned to its elements. */
