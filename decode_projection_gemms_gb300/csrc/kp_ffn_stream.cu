@@ -177,9 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (++stage == S) stage = 0, phase ^= 1;
         }
-        if (*abort_flag)
-            for (int s = n_st > S ? n_st - S : 0; s < n_st; ++s)
-                ffn_drain_wait(smem_u32(full + (s % S)), static_cast<uint32_t>((s / S) & 1));
+        // every copy has landed before this CTA leaves, also where another warp's wait
+        // runs out after this one's last copy is issued
+        for (int s = n_st > S ? n_st - S : 0; s < n_st; ++s)
+            ffn_drain_wait(smem_u32(full + (s % S)), static_cast<uint32_t>((s / S) & 1));
         __syncwarp();
     } else if (warp == 1) {
         const bool mine = elect_one();
