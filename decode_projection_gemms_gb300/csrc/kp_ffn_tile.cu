@@ -412,9 +412,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             // Every copy of this CTA has landed, and every MMA that reads its
             // shared memory has completed, before it leaves: each stage's last
-            // round was returned (a stage without a round passes at once).
+            // round was returned (a stage without a round passes at once). After a
+            // wait that ran out MMAs are issued, and their stages returned, without
+            // their copies: the leader, which the other CTA does not leave before,
+            // waits for those of both as well (the same parity: that of the last round).
             for (int t = 0; t < kStages; ++t) {
                 ffn_drain_wait(smem_u32(empty + stage), phase);
+                if (rank == 0) ffn_drain_wait(smem_u32(full + stage), phase);
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
         }
