@@ -5,7 +5,8 @@
 // rounded to 16 bits because the tensor cores of the three products behind them
 // read 16-bit operands; everything before that rounding is fp32, g and u included:
 // with those saved in bf16 the gradients were 1.8 times as far from the formula as
-// the rounding of a gradient alone, so 1.4 times.
+// the rounding of a gradient alone, so 1.4 times. That rounding is the price of one
+// product per gradient: with the operands in two 16-bit parts each there would be two.
 //
 // fp16 operands: dh u act'(g) passes 65504, or falls to subnormals, where the
 // products behind it do not. A first pass finds the largest finite magnitude of both
@@ -14,7 +15,8 @@
 // are multiplied back. One factor for both, because dx adds the two products, and for
 // all rows and columns, because the products run along either. Scaling is exact, and
 // elements down to 2^-28 of the largest keep fp16's relative precision. The pass adds
-// 4 us to a training step of T = 333, F = 1416, K = 2048 (34.3 -> 38.1).
+// 4 us to a training step of T = 333, F = 1416, K = 2048 (34.3 -> 38.1), 19 us at T =
+// 4003, F = 2048 (cold).
 #include "kp_ffn.cuh"
 
 namespace kp {

@@ -15,14 +15,16 @@
 // which tcgen05.cp lays into the stage's own TMEM columns (their last readers
 // finished before the stage was refilled).
 //
-// Bound: HBM, and at a single token the fixed 4 to 5 us of a launch with clusters
-// and a two-step sum: T = 1, F = 2048, K = 7168 reads 58.7 MB in 13.3 us (4.4 TB/s,
-// of 6.8 measured), F = 4096 117 MB in 21.4 (5.5 TB/s), in 4 bits N = 4096 15.7 MB in
-// 7.5.
+// Bound: HBM plus about 5 us that do not grow with the weights (launch, tensor memory,
+// the first copies' latency, the two-step sum): with cold weights in a graph, T = 1, K =
+// 7168 reads F = 256 (7.3 MB) in 7.2 us, F = 1408 (40 MB) in 10.9, F = 2048 (58.7 MB) in
+// 13.1 (4.5 TB/s, of 6.8 measured), F = 4096 (117 MB) in 21.2 (5.5 TB/s); in 4 bits N =
+// 4096 (15.7 MB) in 7.4. That part is not a floor: the projection's kernels read the
+// same 58.7 MB in 10.7 us (CUDA cores, one token) and 11.4 (tcgen05, two tokens).
 //
 // Up to 8 tokens the 4-bit forms also quantise x themselves: warps 2 .. 5 turn a
 // stage's 256 columns of two tokens each into the operand and scale tile that a copy
-// would have brought (T = 1, N = 4096, K = 7168: 7.5 us on the device against 8.0 with a
+// would have brought (T = 1, N = 4096, K = 7168: 7.4 us on the device against 8.0 with a
 // launch for x, 12 us against 20 from Python, which then allocates nothing but y).
 //
 // Warp 0: copies; warp 1: TMEM and MMA; warps 2 .. 5: x in 4 bits (few tokens),
@@ -45,7 +47,7 @@ constexpr size_t kBarBytes = 256;
 constexpr size_t kMaxSmem = 227 * 1024;
 // What a CTA takes for its stages: half an SM, so that clusters of eight fill the
 // GPU. With all of an SM's shared memory each, 15 such clusters fit where two to
-// an SM makes 36 (T = 1, F = 2048, K = 7168: 16.1 us against 13.8).
+// an SM makes 36 (T = 1, F = 2048, K = 7168, cold weights: 24.6 us against 13.1).
 constexpr size_t kSmem = 113 * 1024;
 
 struct StreamParams {
@@ -422,11 +424,12 @@ Plan make_plan(bool mx4, bool gated, int M, int N, int K, int sms) {
     q.tiles = (N + q.feat - 1) / q.feat;
     q.KB = mx4 ? (K + 255) / 256 : (K + 63) / 64;
     // The cluster grows while each CTA keeps two K blocks and the grid stays below
-    // what was measured to help: 1.7 CTAs per SM in 16 bits (T = 1, K = 7168, gated:
-    // F = 2048 C = 8 10.3 us, 4 10.6; F = 1408 9.1, 10.1; F = 256 7.2, 9.5), one in 4
-    // bits (16 x 4096 x 7168: C = 8 13.1 us, 4 6.6), and for C = 8 in 4 bits the 15
-    // clusters that fit at one CTA per SM (16 x 1408: C = 8 6.0, 4 6.3; 16 x 2048: 9.4,
-    // 6.4). Two blocks: 77 x 4099 x 2050 in 4 bits (nine) C = 8 9.4, 4 8.0, 2 11.2.
+    // what was measured to help, with weights that the L2 does not hold: 1.7 CTAs per SM
+    // in 16 bits (T = 1, K = 7168, gated: F = 2048 C = 8 13.1 us, 4 13.4, 2 16.0; F = 1408
+    // 10.9, 11.4, 15.3; F = 256 7.2, 9.4, 14.4), one in 4 bits (x quantised before, 16 x
+    // 4096 x 7168: C = 8 8.5 us, 4 7.7, 2 8.8), and for C = 8 in 4 bits the 15 clusters
+    // that fit at one CTA per SM (16 x 1408: C = 8 6.7, 4 6.8; 16 x 2048: 7.3, 7.0). Two
+    // blocks: 77 x 4099 x 2050 in 4 bits (nine) C = 8 8.9, 4 6.7, 2 8.1.
     const int64_t grid = static_cast<int64_t>(q.tiles) * q.mt;
     const int most = mx4 ? sms : sms * 17 / 10;
     q.C = 1;

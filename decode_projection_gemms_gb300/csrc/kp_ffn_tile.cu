@@ -29,10 +29,10 @@
 //            one accumulator, the 16-bit forms two.
 //
 // Bound: the tensor cores, which are busy 87 % of the time in the gated form (4003 x
-// 2048 x 7168, 127 us, 1.85 PFLOP/s: the measured library rate is 1.88), 90 % in the
-// backward pass and about 53 % in 4 bits (4096 x 4096 x 7168, 45 us, 5.3 PFLOP/s;
-// there four rounds of tiles hold 3.4 rounds of work, and the accumulator's way out
-// takes 9 %).
+// 2048 x 7168, 128 to 130 us, 1.81 to 1.84 PFLOP/s: the measured library rate is 1.88),
+// 90 % in the backward pass and 52 % in 4 bits (4096 x 4096 x 7168, the product alone,
+// 47 us, 5.1 PFLOP/s; there four rounds of tiles hold 3.4 rounds of work, and the
+// accumulator's way out takes 9 %).
 //
 // Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 9: epilogue.
 #include <algorithm>
