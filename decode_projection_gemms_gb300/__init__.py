@@ -9,7 +9,10 @@ from __future__ import annotations
 __all__ = ["KdaPlan", "KpCfg", "KdaProjError", "skinny_gemm", "select_config", "make_events",
            "table_load", "table_clear", "device_error", "check_device",
            "Mx4Tensor", "mx4_quantize", "mx4_dequantize", "mx4_gemm", "mx4_gated_ffn", "gated_ffn",
-           "gated_ffn_backward"]
+           "gated_ffn_backward",
+           "MoeRoute", "moe_route", "moe_route_backward", "moe_dispatch", "moe_dispatch_backward", "moe_combine",
+           "moe_combine_backward", "grouped_gemm", "grouped_gemm_backward", "grouped_gated_ffn",
+           "grouped_gated_ffn_backward"]
 
 
 def __getattr__(name):

@@ -35,6 +35,9 @@ DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 FFN_MX4_GEMM, FFN_MX4_GATED, FFN_GATED, FFN_GATED_BACKWARD = 0, 1, 2, 3
 BRANCH_QKVG, BRANCH_FAB, BRANCH_FB = 0, 1, 2
+# enum kp_moe_op, enum kp_moe_score
+MOE_ROUTE, MOE_GATED_BACKWARD = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 # exported symbols (must match include/kdaproj.h)
 EXPORTS = (
@@ -45,6 +48,9 @@ EXPORTS = (
     "kp_selftest_timeout", "kp_pdl_consumer_checksum",
     "kp_ffn_workspace", "kp_mx4_bytes", "kp_mx4_quantize", "kp_mx4_dequantize", "kp_mx4_gemm",
     "kp_mx4_gated_ffn", "kp_gated_ffn", "kp_gated_ffn_backward",
+    "kp_moe_workspace", "kp_moe_route", "kp_moe_route_backward", "kp_moe_dispatch", "kp_moe_combine",
+    "kp_moe_combine_backward", "kp_grouped_gemm", "kp_grouped_gemm_backward", "kp_grouped_gated_ffn",
+    "kp_grouped_gated_ffn_backward",
 )
 DEV_SELFTEST = 5   # device error code of kp_selftest_timeout
 
@@ -122,6 +128,18 @@ def load(path: str | None = None):
             "kp_gated_ffn": [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp, sz, vp],
             "kp_gated_ffn_backward": [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci,
                                       vp, sz, vp],
+            "kp_moe_workspace": [ci, ci, ci, ci, ctypes.POINTER(ctypes.c_size_t)],
+            "kp_moe_route": [vp, i64, vp, ci, ci, ci, ci, ci, vp, vp, vp, vp, vp, vp, sz, vp],
+            "kp_moe_route_backward": [vp, vp, i64, vp, vp, vp, i64, ci, ci, ci, ci, ci, vp],
+            "kp_moe_dispatch": [vp, i64, vp, vp, i64, ci, ci, ci, ci, vp],
+            "kp_moe_combine": [vp, i64, vp, vp, vp, i64, ci, ci, ci, ci, vp],
+            "kp_moe_combine_backward": [vp, i64, vp, i64, vp, vp, vp, i64, vp, ci, ci, ci, ci, vp],
+            "kp_grouped_gemm": [vp, i64, vp, i64, i64, vp, i64, vp, ci, ci, ci, ci, ci, vp],
+            "kp_grouped_gemm_backward": [vp, i64, vp, i64, vp, i64, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp],
+            "kp_grouped_gated_ffn": [vp, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp, ci, ci, ci, ci, ci, ci,
+                                     vp],
+            "kp_grouped_gated_ffn_backward": [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, i64, vp, vp, vp,
+                                              ci, ci, ci, ci, ci, ci, vp, sz, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -353,7 +371,8 @@ def _on(device, stream, *inputs):
             yield
             return
         for t in inputs:
-            for part in ((t._buf, t._scales) if isinstance(t, Mx4Tensor) else (t,)):
+            for part in ((t._buf, t._scales) if isinstance(t, Mx4Tensor) else
+                         (t._buf,) if isinstance(t, MoeRoute) else (t,)):
                 if isinstance(part, torch.Tensor) and part.is_cuda:
                     part.record_stream(stream)
         with torch.cuda.stream(stream):
@@ -669,6 +688,408 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu: 
     rc = load().kp_gated_ffn_backward(dh.data_ptr(), lddh, x.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(),
                                       ldu, g.data_ptr(), u.data_ptr(), dx.data_ptr(), dWg.data_ptr(),
                                       dWu.data_ptr(), T, F, K, code, _DTYPES[dt], wp, wn, _raw_stream(index))
+    if rc:
+        _check(rc)
+    return dx, dWg, dWu
+
+
+# ---- mixture-of-experts operators ----------------------------------------------
+#
+# As the feed-forward operators: every function runs on the current device and stream,
+# or makes those of its operands and of `stream` current first.
+
+class MoeRoute:
+    """Which experts each token goes to, made by ``moe_route`` for ``tokens`` tokens, the
+    best ``top_k`` of ``experts`` each. On the device, int32 unless said otherwise:
+
+    * ``ids`` [tokens, top_k]: the experts, best first; -1 where there is none;
+    * ``weights`` [tokens, top_k] float32: of their outputs, adding up to 1;
+    * ``offsets`` [experts + 1]: expert e has rows ``offsets[e]`` to ``offsets[e + 1] - 1``;
+    * ``order`` [tokens * top_k]: the pair ``token * top_k + slot`` of every row, -1 behind
+      the last;
+    * ``position`` [tokens, top_k]: the row of every pair, -1 where there is none."""
+
+    __slots__ = ("_buf", "_index", "_ptr", "tokens", "top_k", "experts", "score", "device")
+
+    def __init__(self, tokens: int, top_k: int, experts: int, score: str, index: int):
+        self.tokens, self.top_k, self.experts, self.score, self._index = tokens, top_k, experts, score, index
+        self.device = _device(index)
+        # all parts in one allocation: ids, position, order, weights, offsets
+        self._buf = torch.empty(4 * tokens * top_k + experts + 1, dtype=torch.int32, device=self.device)
+        self._ptr = self._buf.data_ptr()
+
+    def get_device(self) -> int:
+        """The CUDA device's index."""
+        return self._index
+
+    def _at(self, part: int) -> int:
+        """Address of a part."""
+        return self._ptr + 4 * part * self.tokens * self.top_k
+
+    def _pairs(self, part: int) -> torch.Tensor:
+        n = self.tokens * self.top_k
+        return self._buf.as_strided((self.tokens, self.top_k), (self.top_k, 1), part * n)
+
+    @property
+    def ids(self) -> torch.Tensor:
+        return self._pairs(0)
+
+    @property
+    def position(self) -> torch.Tensor:
+        return self._pairs(1)
+
+    @property
+    def order(self) -> torch.Tensor:
+        n = self.tokens * self.top_k
+        return self._buf.as_strided((n,), (1,), 2 * n)
+
+    @property
+    def weights(self) -> torch.Tensor:
+        return self._pairs(3).view(torch.float32)
+
+    @property
+    def offsets(self) -> torch.Tensor:
+        return self._buf.as_strided((self.experts + 1,), (1,), 4 * self.tokens * self.top_k)
+
+    def __repr__(self):
+        return f"MoeRoute({self.tokens} tokens, top {self.top_k} of {self.experts}, {self.score}, {self.device})"
+
+
+def _moe_work(op: int, M: int, N: int, K: int, index: int):
+    """(tensor or None, pointer, bytes) of this call's workspace."""
+    key = (index, "moe", op, M, N, K)
+    n = _FFN_WORK.get(key)
+    if n is None:
+        b = ctypes.c_size_t()
+        _check(load().kp_moe_workspace(op, M, N, K, ctypes.byref(b)))
+        if len(_FFN_WORK) > 4096:
+            _FFN_WORK.clear()
+        n = _FFN_WORK[key] = int(b.value)
+    if not n:
+        return None, None, 0
+    t = torch.empty(n, dtype=torch.uint8, device=_device(index))
+    return t, t.data_ptr(), n
+
+
+def _route(r, name: str, index: int) -> MoeRoute:
+    if not isinstance(r, MoeRoute):
+        raise TypeError(f"{name} must be a MoeRoute (moe_route), got {type(r).__name__}")
+    if r._index != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, is on {r.device}")
+    return r
+
+
+def _experts(W, name: str, dtype, index: int):
+    """Check all experts' matrices [E, rows, cols]; returns their row and expert strides."""
+    if not isinstance(W, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(W).__name__}")
+    if W.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {W.dtype}")
+    if W.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, is on {W.device}")
+    if W.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D tensor [experts, features, columns]")
+    se, ld, inner = W.stride()
+    E, rows, cols = W.shape
+    if rows <= 1:   # the stride of a single row, and of a single expert, says nothing
+        ld = (cols + 7) // 8 * 8
+    if E <= 1:
+        se = ld * rows
+    if ld < cols or (inner != 1 and cols > 1):
+        raise ValueError(f"{name} must have contiguous rows (strides {tuple(W.stride())})")
+    return ld, se
+
+
+def _offsets(t, E: int, index: int) -> int:
+    """Address of the experts' offsets, checked."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"offsets must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype is not torch.int32:
+        raise TypeError(f"offsets must be int32, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"offsets must be on CUDA device {index}, is on {t.device}")
+    if t.dim() != 1 or t.shape[0] != E + 1 or not t.is_contiguous():
+        raise ValueError(f"offsets must be contiguous with {E + 1} numbers, got shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _pair_floats(t, name: str, r: MoeRoute) -> int:
+    """Address of float32 numbers [tokens, top_k], checked."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if t.get_device() != r._index:
+        raise ValueError(f"{name} must be on CUDA device {r._index}, is on {t.device}")
+    if t.shape != (r.tokens, r.top_k) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {(r.tokens, r.top_k)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+              stream=None) -> MoeRoute:
+    """Send every token (a row of ``logits`` [T, E]; bfloat16, float16 or float32, rows may
+    be strided) to the ``top_k`` experts with the largest logits, ties to the lowest
+    expert. Their weights are the chosen scores over the scores' sum, ``score`` being
+    "softmax" or "sigmoid". With ``bias`` (float32 [E], sigmoid only) the choice is by
+    score plus bias; the weights do not see it. Experts at minus infinity (or NaN) are not
+    chosen, so a padded token, all of whose logits are minus infinity, goes nowhere. At
+    most 1024 experts and 32 of them a token."""
+    index = _here(logits, "logits", stream)
+    if index < 0:
+        with _on(logits.device, stream, logits, bias):
+            return moe_route(logits, top_k, score, bias)
+    code = SCORES.get(score)
+    if code is None:
+        raise ValueError(f"unknown score {score!r}: one of {', '.join(SCORES)}")
+    ld = _rows(logits, "logits", None, index)
+    dt = _FFN_DTYPES.get(logits.dtype)
+    if dt is None:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+    T, E = logits.shape
+    bp = None
+    if bias is not None:
+        if not isinstance(bias, torch.Tensor) or bias.dtype is not torch.float32:
+            raise TypeError("bias must be a float32 tensor")
+        if bias.get_device() != index or bias.shape != (E,) or not bias.is_contiguous():
+            raise ValueError(f"bias must be contiguous, [{E}] and on CUDA device {index}")
+        bp = bias.data_ptr()
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k must be within 1 .. {E}, got {top_k}")
+    work, wp, wn = _moe_work(MOE_ROUTE, T, E, top_k, index)
+    r = MoeRoute(T, top_k, E, score, index)
+    rc = load().kp_moe_route(logits.data_ptr(), ld, bp, T, E, top_k, code, dt, r._at(0), r._at(3), r._at(4), r._at(2),
+                             r._at(1), wp, wn, _raw_stream(index))
+    if rc:
+        _check(rc)
+    return r
+
+
+def moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, route: MoeRoute, stream=None) -> torch.Tensor:
+    """The gradient of ``moe_route``'s logits (of their type) for the gradient
+    ``dweights`` [T, top_k] float32 of its weights: zero but for the chosen experts. A bias
+    has none."""
+    index = _here(logits, "logits", stream)
+    if index < 0:
+        with _on(logits.device, stream, dweights, logits, route):
+            return moe_route_backward(dweights, logits, route)
+    _route(route, "route", index)
+    ld = _rows(logits, "logits", None, index)
+    dt = _FFN_DTYPES.get(logits.dtype)
+    if dt is None:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+    T, E, k = route.tokens, route.experts, route.top_k
+    if logits.shape != (T, E):
+        raise ValueError(f"logits must be {(T, E)}, got {tuple(logits.shape)}")
+    dp = _pair_floats(dweights, "dweights", route)
+    out = torch.empty((T, E), dtype=logits.dtype, device=_device(index))
+    rc = load().kp_moe_route_backward(dp, logits.data_ptr(), ld, route._at(0), route._at(3), out.data_ptr(), E, T, E, k,
+                                      SCORES[route.score], dt, _raw_stream(index))
+    if rc:
+        _check(rc)
+    return out
+
+
+def _half_rows(t, name: str, rows: int, index: int, dtype=None) -> int:
+    """Check a 16-bit matrix with that many rows; returns its row stride."""
+    ld = _rows(t, name, dtype, index)
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    if t.shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {t.shape[0]}")
+    return ld
+
+
+def moe_dispatch(x: torch.Tensor, route: MoeRoute, rows: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The tokens' rows ``x`` [T, K] (bfloat16 or float16, rows may be strided) in expert
+    order: ``rows`` [T * top_k, K], one for each pair of a token and an expert of its.
+    Rows from ``route.offsets[-1]`` on are not written."""
+    index = _here(x, "x", stream)
+    if index < 0:
+        with _on(x.device, stream, x, route, rows):
+            return moe_dispatch(x, route, rows)
+    _route(route, "route", index)
+    T, k = route.tokens, route.top_k
+    ldx = _half_rows(x, "x", T, index)
+    K = x.shape[1]
+    rows, ldr = _out(rows, "rows", T * k, K, x.dtype, index)
+    rc = load().kp_moe_dispatch(x.data_ptr(), ldx, route._at(1), rows.data_ptr(), ldr, T, k, K, _DTYPES[x.dtype],
+                                _raw_stream(index))
+    if rc:
+        _check(rc)
+    return rows
+
+
+def _combine(rows, route, weighted: bool, y, stream):
+    index = _here(rows, "rows", stream)
+    if index < 0:
+        with _on(rows.device, stream, rows, route, y):
+            return _combine(rows, route, weighted, y, None)
+    _route(route, "route", index)
+    T, k = route.tokens, route.top_k
+    ldr = _half_rows(rows, "rows", T * k, index)
+    K = rows.shape[1]
+    y, ldy = _out(y, "y", T, K, rows.dtype, index)
+    rc = load().kp_moe_combine(rows.data_ptr(), ldr, route._at(3) if weighted else None, route._at(1), y.data_ptr(), ldy,
+                               T, k, K, _DTYPES[rows.dtype], _raw_stream(index))
+    if rc:
+        _check(rc)
+    return y
+
+
+def moe_dispatch_backward(drows: torch.Tensor, route: MoeRoute, dx: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """The gradient [T, K] of ``moe_dispatch``'s tokens: the sum of their rows'."""
+    return _combine(drows, route, False, dx, stream)
+
+
+def moe_combine(rows: torch.Tensor, route: MoeRoute, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``y[t] = round(sum_s route.weights[t, s] * rows[route.position[t, s]])``, summed in
+    fp32: the experts' outputs ``rows`` [T * top_k, K] back with their tokens. A token
+    without experts gets zeros."""
+    return _combine(rows, route, True, y, stream)
+
+
+def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, route: MoeRoute, drows: torch.Tensor | None = None,
+                         stream=None):
+    """Gradients ``(drows, dweights)`` of ``moe_combine`` for the gradient ``dy`` [T, K] of
+    its output: the rows' in their type (rows from ``route.offsets[-1]`` on are not
+    written), the weights' [T, top_k] in float32."""
+    index = _here(dy, "dy", stream)
+    if index < 0:
+        with _on(dy.device, stream, dy, rows, route, drows):
+            return moe_combine_backward(dy, rows, route, drows)
+    _route(route, "route", index)
+    T, k = route.tokens, route.top_k
+    lddy = _half_rows(dy, "dy", T, index)
+    ldr = _half_rows(rows, "rows", T * k, index, dy.dtype)
+    K = dy.shape[1]
+    if rows.shape[1] != K:
+        raise ValueError(f"rows must have {K} columns, got {rows.shape[1]}")
+    drows, lddr = _out(drows, "drows", T * k, K, dy.dtype, index)
+    dw = torch.empty((T, k), dtype=torch.float32, device=_device(index))
+    rc = load().kp_moe_combine_backward(dy.data_ptr(), lddy, rows.data_ptr(), ldr, route._at(3), route._at(1),
+                                        drows.data_ptr(), lddr, dw.data_ptr(), T, k, K, _DTYPES[dy.dtype],
+                                        _raw_stream(index))
+    if rc:
+        _check(rc)
+    return drows, dw
+
+
+def _grouped_operands(x, W, name: str, offsets, index: int):
+    """(R, E, N, K, x's row stride, W's row and expert strides, type, offsets' address)."""
+    dt = x.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"x must be bfloat16 or float16, got {dt}")
+    ldx = _rows(x, "x", dt, index)
+    ldw, sw = _experts(W, name, dt, index)
+    R, K = x.shape
+    E, N, Kw = W.shape
+    if Kw != K:
+        raise ValueError(f"{name} has K={Kw}, x has K={K}")
+    return R, E, N, K, ldx, ldw, sw, dt, _offsets(offsets, E, index)
+
+
+def grouped_gemm(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """``y[r] = round(x[r] @ W[e].T)`` for the rows ``offsets[e]`` to ``offsets[e + 1] - 1``
+    of every expert e, sums in fp32. ``x`` [R, K] and ``W`` [E, N, K] bfloat16 or float16,
+    rows and experts may be strided (strides and K multiples of 8, 16-byte aligned);
+    ``offsets`` int32 [E + 1] on the device, ascending from 0 to at most R. Rows from
+    ``offsets[E]`` on are not written."""
+    index = _here(x, "x", stream)
+    if index < 0:
+        with _on(x.device, stream, x, W, offsets, y):
+            return grouped_gemm(x, W, offsets, y)
+    R, E, N, K, ldx, ldw, sw, dt, op = _grouped_operands(x, W, "W", offsets, index)
+    y, ldy = _out(y, "y", R, N, dt, index)
+    rc = load().kp_grouped_gemm(x.data_ptr(), ldx, W.data_ptr(), ldw, sw, y.data_ptr(), ldy, op, R, E, N, K, _DTYPES[dt],
+                                _raw_stream(index))
+    if rc:
+        _check(rc)
+    return y
+
+
+def grouped_gemm_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, stream=None):
+    """Gradients ``(dx, dW)`` of ``grouped_gemm`` for the gradient ``dy`` [R, N] of its
+    output (row stride a multiple of 8, 16-byte aligned). Rows of ``dx`` from
+    ``offsets[E]`` on are not written; an expert without rows gets a ``dW`` of zeros."""
+    index = _here(x, "x", stream)
+    if index < 0:
+        with _on(x.device, stream, dy, x, W, offsets):
+            return grouped_gemm_backward(dy, x, W, offsets)
+    R, E, N, K, ldx, ldw, sw, dt, op = _grouped_operands(x, W, "W", offsets, index)
+    lddy = _rows(dy, "dy", dt, index)
+    if dy.shape != (R, N):
+        raise ValueError(f"dy must be {(R, N)}, got {tuple(dy.shape)}")
+    dx, dW = x.new_empty((R, K)), x.new_empty((E, N, K))
+    rc = load().kp_grouped_gemm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, W.data_ptr(), ldw, sw, dx.data_ptr(), K,
+                                         dW.data_ptr(), op, R, E, N, K, _DTYPES[dt], _raw_stream(index))
+    if rc:
+        _check(rc)
+    return dx, dW
+
+
+def _grouped_gated_operands(x, Wg, Wu, offsets, index: int):
+    R, E, F, K, ldx, ldg, sg, dt, op = _grouped_operands(x, Wg, "Wg", offsets, index)
+    ldu, su = _experts(Wu, "Wu", dt, index)
+    if Wu.shape != Wg.shape:
+        raise ValueError(f"Wg {tuple(Wg.shape)} and Wu {tuple(Wu.shape)} must have the same shape")
+    return R, E, F, K, ldx, ldg, sg, ldu, su, dt, op
+
+
+def grouped_gated_ffn(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, offsets: torch.Tensor, act: str = "silu",
+                      h: torch.Tensor | None = None, save: bool = False, stream=None):
+    """``gated_ffn`` with an expert's weights for each row: ``h[r] = round(act(x[r] @
+    Wg[e].T) * (x[r] @ Wu[e].T))`` for the rows ``offsets[e]`` to ``offsets[e + 1] - 1`` of
+    every expert e. Operands as for ``grouped_gemm``; ``act`` and ``save`` as for
+    ``gated_ffn``. Rows from ``offsets[E]`` on are not written."""
+    index = _here(x, "x", stream)
+    if index < 0:
+        with _on(x.device, stream, x, Wg, Wu, offsets, h):
+            return grouped_gated_ffn(x, Wg, Wu, offsets, act, h, save)
+    code = _act_code(act)
+    R, E, F, K, ldx, ldg, sg, ldu, su, dt, op = _grouped_gated_operands(x, Wg, Wu, offsets, index)
+    h, ldh = _out(h, "h", R, F, dt, index)
+    g = u = gp = up = None
+    if save:
+        g = torch.empty((R, F), dtype=torch.float32, device=_device(index))
+        u = torch.empty((R, F), dtype=torch.float32, device=_device(index))
+        gp, up = g.data_ptr(), u.data_ptr()
+    rc = load().kp_grouped_gated_ffn(x.data_ptr(), ldx, Wg.data_ptr(), ldg, sg, Wu.data_ptr(), ldu, su, h.data_ptr(), ldh,
+                                     gp, up, op, R, E, F, K, code, _DTYPES[dt], _raw_stream(index))
+    if rc:
+        _check(rc)
+    return (h, g, u) if save else h
+
+
+def grouped_gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor,
+                               offsets: torch.Tensor, g: torch.Tensor, u: torch.Tensor, act: str = "silu",
+                               stream=None):
+    """Gradients ``(dx, dWg, dWu)`` of ``grouped_gated_ffn`` for the gradient ``dh`` of its
+    output, from its operands and the ``g`` and ``u`` it saved, computed as
+    ``gated_ffn_backward`` does. Rows of ``dx`` from ``offsets[E]`` on are not written; an
+    expert without rows gets weights' gradients of zeros."""
+    index = _here(x, "x", stream)
+    if index < 0:
+        with _on(x.device, stream, dh, x, Wg, Wu, offsets, g, u):
+            return grouped_gated_ffn_backward(dh, x, Wg, Wu, offsets, g, u, act)
+    code = _act_code(act)
+    R, E, F, K, ldx, ldg, sg, ldu, su, dt, op = _grouped_gated_operands(x, Wg, Wu, offsets, index)
+    lddh = _rows(dh, "dh", dt, index)
+    for t, name in ((g, "g"), (u, "u")):
+        _rows(t, name, torch.float32 if R else None, index)   # with no rows nothing is read
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
+        if t.shape != (R, F):
+            raise ValueError(f"{name} must be {(R, F)}, got {tuple(t.shape)}")
+    dx, dWg, dWu = x.new_empty((R, K)), x.new_empty((E, F, K)), x.new_empty((E, F, K))
+    work, wp, wn = _moe_work(MOE_GATED_BACKWARD, R, F, K, index)
+    rc = load().kp_grouped_gated_ffn_backward(dh.data_ptr(), lddh, x.data_ptr(), ldx, Wg.data_ptr(), ldg, sg,
+                                              Wu.data_ptr(), ldu, su, g.data_ptr(), u.data_ptr(), dx.data_ptr(), K,
+                                              dWg.data_ptr(), dWu.data_ptr(), op, R, E, F, K, code, _DTYPES[dt], wp, wn,
+                                              _raw_stream(index))
     if rc:
         _check(rc)
     return dx, dWg, dWu

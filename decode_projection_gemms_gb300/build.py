@@ -38,8 +38,12 @@ SOURCES = [
     "kp_ffn_tile.cu",
     "kp_ffn_bwd.cu",
     "kp_ffn_api.cu",
+    "kp_moe_route.cu",
+    "kp_moe_rows.cu",
+    "kp_moe_tile.cu",
+    "kp_moe_api.cu",
 ]
-HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh", "kp_ffn.cuh", "kp_mx4.cuh"]
+HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh", "kp_ffn.cuh", "kp_mx4.cuh", "kp_moe.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

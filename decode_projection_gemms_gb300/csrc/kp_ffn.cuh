@@ -119,11 +119,12 @@ bool ffn_use_tile(bool mx4, bool gated, int M, int N, int K, int sms);
 // dG = dh u act'(g), dU = dh act(g): the gradients of both products, [T, F]
 // with row stride ld (kp_ffn_bwd.cu). scaling (fp16; NULL: none): both come out as
 // multiples of a power of two, whose reciprocal goes to scaling[0]; the rest of its
-// ffn_gate_grad_scratch bytes is the kernels' own.
+// ffn_gate_grad_scratch bytes is the kernels' own. rows (NULL: all T): device count of
+// the rows that hold anything; the others are neither read nor written.
 size_t ffn_gate_grad_scratch(int sms);
 cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const float *g, const float *u, void *dg, void *du,
                                  int64_t ld, float *scaling, int T, int F, int act, int dtype, int sms,
-                                 cudaStream_t s);
+                                 cudaStream_t s, const int32_t *rows = nullptr);
 
 }  // namespace kp
 

@@ -79,14 +79,20 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t *sh) {
     return m;
 }
 
+// Rows that hold anything.
+__device__ __forceinline__ int64_t used_rows(const int32_t *rows, int T) {
+    return rows ? min(max(__ldg(rows), 0), T) : T;
+}
+
 // Each block's largest finite |dG|, |dU| (bits), to top[block].
 template <int kAct>
 __global__ void __launch_bounds__(kThreads)
     gate_max_kernel(const uint16_t *__restrict__ dh, int64_t lddh, const float *__restrict__ g,
-                    const float *__restrict__ u, uint32_t *__restrict__ top, int T, int F, int dtype, int vec) {
+                    const float *__restrict__ u, uint32_t *__restrict__ top, int T, int F, int dtype, int vec,
+                    const int32_t *__restrict__ rows) {
     __shared__ uint32_t sh[kThreads / 32];
     const int chunks = (F + 7) >> 3;
-    const int64_t total = static_cast<int64_t>(T) * chunks;
+    const int64_t total = used_rows(rows, T) * chunks;
     uint32_t m = 0;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * kThreads) {
@@ -112,7 +118,7 @@ __global__ void __launch_bounds__(kThreads)
     gate_grad_kernel(const uint16_t *__restrict__ dh, int64_t lddh, const float *__restrict__ g,
                      const float *__restrict__ u, uint16_t *__restrict__ dg, uint16_t *__restrict__ du,
                      int64_t ld, const uint32_t *__restrict__ top, int tops, float *__restrict__ back, int T, int F,
-                     int dtype, int vec) {
+                     int dtype, int vec, const int32_t *__restrict__ rows) {
     float scale = 1.f;
     if (tops) {
         __shared__ uint32_t sh[kThreads / 32];
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kThreads)
         scale = sh_scale;
     }
     const int chunks = (F + 7) >> 3;
-    const int64_t total = static_cast<int64_t>(T) * chunks;
+    const int64_t total = used_rows(rows, T) * chunks;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * kThreads) {
         const int64_t t = i / chunks;
@@ -156,15 +162,15 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int kAct>
 cudaError_t launch(const uint16_t *dh, int64_t lddh, const float *g, const float *u, uint16_t *dg, uint16_t *du,
-                   int64_t ld, float *scaling, int T, int F, int dtype, int grid, int vec, cudaStream_t s) {
+                   int64_t ld, float *scaling, int T, int F, int dtype, int grid, int vec, const int32_t *rows, cudaStream_t s) {
     uint32_t *top = scaling ? reinterpret_cast<uint32_t *>(scaling) + 1 : nullptr;
     if (scaling) {
-        gate_max_kernel<kAct><<<grid, kThreads, 0, s>>>(dh, lddh, g, u, top, T, F, dtype, vec);
+        gate_max_kernel<kAct><<<grid, kThreads, 0, s>>>(dh, lddh, g, u, top, T, F, dtype, vec, rows);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     gate_grad_kernel<kAct><<<grid, kThreads, 0, s>>>(dh, lddh, g, u, dg, du, ld, top, scaling ? grid : 0, scaling, T, F,
-                                                     dtype, vec);
+                                                     dtype, vec, rows);
     return cudaGetLastError();
 }
 
@@ -174,7 +180,7 @@ size_t ffn_gate_grad_scratch(int sms) { return (static_cast<size_t>(sms) * kBloc
 
 cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const float *g, const float *u, void *dg, void *du,
                                  int64_t ld, float *scaling, int T, int F, int act, int dtype, int sms,
-                                 cudaStream_t s) {
+                                 cudaStream_t s, const int32_t *rows) {
     const int64_t total = static_cast<int64_t>(T) * ((F + 7) / 8);
     const int64_t blocks = (total + kThreads - 1) / kThreads;
     const int64_t most = static_cast<int64_t>(sms) * kBlocksPerSm;
@@ -182,7 +188,7 @@ cudaError_t ffn_gate_grad_launch(const void *dh, int64_t lddh, const float *g, c
     const bool vec = F % 8 == 0 && lddh % 8 == 0 && (reinterpret_cast<uintptr_t>(dh) & 15) == 0;
     auto go = act == KP_ACT_SILU ? launch<KP_ACT_SILU> : act == KP_ACT_GELU ? launch<KP_ACT_GELU> : launch<KP_ACT_GELU_TANH>;
     return go(static_cast<const uint16_t *>(dh), lddh, g, u, static_cast<uint16_t *>(dg), static_cast<uint16_t *>(du), ld,
-              scaling, T, F, dtype, grid, vec, s);
+              scaling, T, F, dtype, grid, vec, rows, s);
 }
 
 }  // namespace kp

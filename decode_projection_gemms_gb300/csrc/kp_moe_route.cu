@@ -1,0 +1,378 @@
+// Router of the mixture-of-experts operators: each token's top-k experts, the weights
+// of their outputs, and the order that puts the chosen (token, slot) pairs expert by
+// expert, tokens ascending within each.
+//
+// A warp a token: a lane holds experts lane, lane + 32, ...; a choice is a maximum over
+// the warp of keys that order like the logits, then a minimum over the experts that
+// have it. The order is a counting sort: every block of kTokens tokens counts its
+// choices by expert, the counts of the blocks before it are summed, and a pair's row is
+// its expert's first row, plus those of the blocks before, plus the pairs before it
+// within the block. Counts are whole numbers, so nothing depends on timing.
+#include <algorithm>
+
+#include "kp_moe.cuh"
+
+namespace kp {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTokens = 32;   // of a block
+
+struct RouteParams {
+    MoeRouteArgs a;
+    int blocks;
+    int32_t *counts;   // [blocks][E]: choices of a block, then of the blocks before it
+    int32_t *totals;   // [E]
+};
+
+// A logit in fp32: NaN counts as minus infinity, plus infinity as the largest finite number.
+__device__ __forceinline__ float logit_of(const void *p, int64_t i, int dtype) {
+    const float v = dtype == KP_FP32 ? __ldg(static_cast<const float *>(p) + i)
+                                     : elem_widen(__ldg(static_cast<const uint16_t *>(p) + i), dtype);
+    return v != v ? -INFINITY : fminf(v, 3.402823466e38f);
+}
+// Bits that order like the value; 0 for minus infinity and NaN, which are not chosen.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);   // -0 like 0
+    if (!(v > -INFINITY)) return 0;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    if (!(v > -INFINITY)) return 0;
+    return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+    const uint32_t hi = warp_max(static_cast<uint32_t>(v >> 32));
+    const uint32_t lo = warp_max(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+// The k largest of the warp's keys (lane holds experts lane + 32 i), ties to the lowest
+// expert: lane j gets the j-th one's expert (-1: there is none) and, with kGap, whether
+// two of the k + 1 largest are nearer than fp32 sums of a score and a bias are exact.
+template <int NV, typename Key, bool kGap>
+__device__ __forceinline__ int choose(Key (&key)[NV], int k, int lane, bool &close) {
+    int mine = -1;
+    float last = 0.f;
+    close = false;
+    for (int j = 0; j < k + (kGap ? 1 : 0); ++j) {
+        Key best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (key[i] > best) best = key[i], at = i;
+        const Key top = warp_max(best);
+        if (top == 0) break;
+        const int e = static_cast<int>(__reduce_min_sync(
+            0xFFFFFFFFu, best == top ? static_cast<uint32_t>(lane + 32 * at) : 0xFFFFFFFFu));
+        if constexpr (kGap) {
+            const float v = value_of(top);
+            close = close || (j && last - v <= 2e-6f * fmaxf(1.f, fabsf(v)));
+            last = v;
+        }
+        if (j < k && lane == j) mine = e;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane + 32 * i == e) key[i] = 0;
+    }
+    return mine;
+}
+
+// Experts and weights of a token; lane j < k gets the j-th.
+template <int NV>
+__device__ __forceinline__ void route_token(const MoeRouteArgs &a, int64_t t, int lane, int &id, float &w) {
+    const int64_t row = t * a.ld;
+    float v[NV];
+    uint32_t key[NV];
+    bool close;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        v[i] = e < a.E ? logit_of(a.logits, row + e, a.dtype) : -INFINITY;
+        key[i] = order_key(v[i]);
+    }
+    if (!a.bias) {
+        id = choose<NV, uint32_t, false>(key, a.k, lane, close);
+    } else {
+        // Chosen by sigmoid plus bias. fp32 keys decide, but where two of them lie so
+        // near each other that fp32 does not, the token is chosen again in 64 bits.
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane + 32 * i;
+            if (key[i]) key[i] = order_key(1.f / (1.f + expf(-v[i])) + __ldg(a.bias + e));
+        }
+        id = choose<NV, uint32_t, true>(key, a.k, lane, close);
+        if (close) {
+            uint64_t wide[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = lane + 32 * i;
+                wide[i] = v[i] > -INFINITY
+                              ? order_key(1.0 / (1.0 + exp(-static_cast<double>(v[i]))) + static_cast<double>(__ldg(a.bias + e)))
+                              : 0;
+            }
+            id = choose<NV, uint64_t, false>(wide, a.k, lane, close);
+        }
+    }
+    const float l = id >= 0 ? logit_of(a.logits, row + id, a.dtype) : -INFINITY;
+    // the largest chosen logit
+    const uint32_t most = warp_max(order_key(l));
+    if (most == 0) {
+        w = 0.f;
+        return;
+    }
+    const float top = value_of(most);
+    float s = 0.f;
+    if (id >= 0) {
+        if (a.score == KP_SCORE_SIGMOID) {
+            // all scores times e^m, m = max(0, -top), so that they do not vanish together
+            const float m = fmaxf(0.f, -top);
+            s = 1.f / (expf(-m) + expf(-l - m));
+        } else {
+            s = expf(l - top);
+        }
+    }
+    float sum = s;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
+    w = s / sum;
+}
+
+// Exclusive sums of n <= kMoeMaxExperts whole numbers in shared memory, by the block;
+// returns the sum of all.
+__device__ int block_scan(int32_t *v, int n, int32_t *sums) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (n + kThreads - 1) / kThreads, at = threadIdx.x * per;
+    int mine = 0;
+    for (int i = 0; i < per; ++i)
+        if (at + i < n) mine += v[at + i];
+    int run = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, run, d);
+        if (lane >= d) run += o;
+    }
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += sums[i];
+        all += sums[i];
+    }
+    run += before - mine;
+    for (int i = 0; i < per; ++i)
+        if (at + i < n) {
+            const int x = v[at + i];
+            v[at + i] = run;
+            run += x;
+        }
+    __syncthreads();
+    return all;
+}
+
+// Rows of a block's choices: base[e] holds the first row of expert e for this block.
+// Slots are taken kThreads at a time in order; cnt [kWarps][E].
+__device__ void place(const RouteParams &p, int64_t first, int n, int32_t *base, int32_t *cnt) {
+    const int E = p.a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int s0 = 0; s0 < n; s0 += kThreads) {
+        for (int i = threadIdx.x; i < kWarps * E; i += kThreads) cnt[i] = 0;
+        __syncthreads();
+        const int i = s0 + threadIdx.x;
+        const int e = i < n ? p.a.ids[first + i] : -1;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        const int before = __popc(same & ((1u << lane) - 1));
+        if (e >= 0 && before == 0) cnt[warp * E + e] = __popc(same);
+        __syncthreads();
+        for (int x = threadIdx.x; x < E; x += kThreads) {
+            int run = base[x];
+            for (int q = 0; q < kWarps; ++q) {
+                const int c = cnt[q * E + x];
+                cnt[q * E + x] = run;
+                run += c;
+            }
+            base[x] = run;
+        }
+        __syncthreads();
+        if (i < n) {
+            int r = -1;
+            if (e >= 0) {
+                r = cnt[warp * E + e] + before;
+                p.a.order[r] = static_cast<int32_t>(first + i);
+            }
+            p.a.position[first + i] = r;
+        }
+        __syncthreads();
+    }
+}
+
+extern __shared__ int32_t route_smem[];
+
+// kAll: one block, which does everything.
+template <int NV, bool kAll>
+__global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams p) {
+    const MoeRouteArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t *hist = route_smem;
+    for (int i = threadIdx.x; i < a.E; i += kThreads) hist[i] = 0;
+    __syncthreads();
+    const int t0 = kAll ? 0 : static_cast<int>(blockIdx.x) * kTokens;
+    const int t1 = kAll ? a.T : min(t0 + kTokens, a.T);
+    for (int t = t0 + warp; t < t1; t += kWarps) {
+        int id;
+        float w;
+        route_token<NV>(a, t, lane, id, w);
+        if (lane < a.k) {
+            a.ids[static_cast<int64_t>(t) * a.k + lane] = id;
+            a.weights[static_cast<int64_t>(t) * a.k + lane] = w;
+            if (id >= 0) atomicAdd(hist + id, 1);
+        }
+    }
+    __syncthreads();
+    if constexpr (!kAll) {
+        for (int i = threadIdx.x; i < a.E; i += kThreads) p.counts[static_cast<int64_t>(blockIdx.x) * a.E + i] = hist[i];
+    } else {
+        int32_t *sums = hist + a.E, *cnt = sums + kWarps;
+        const int rows = block_scan(hist, a.E, sums);
+        for (int i = threadIdx.x; i < a.E; i += kThreads) a.offsets[i] = hist[i];
+        if (threadIdx.x == 0) a.offsets[a.E] = rows;
+        for (int i = rows + threadIdx.x; i < a.T * a.k; i += kThreads) a.order[i] = -1;
+        place(p, 0, a.T * a.k, hist, cnt);
+    }
+}
+
+// counts[b][e] -> sum of counts[0 .. b)[e]; a lane an expert, a warp a run of blocks.
+__global__ void __launch_bounds__(1024) route_scan_kernel(const RouteParams p) {
+    __shared__ int32_t part[32][33];
+    const int E = p.a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = blockIdx.x * 32 + lane;
+    const int per = (p.blocks + 31) / 32, b0 = warp * per, b1 = min(b0 + per, p.blocks);
+    int sum = 0;
+    if (e < E)
+        for (int b = b0; b < b1; ++b) sum += p.counts[static_cast<int64_t>(b) * E + e];
+    part[warp][lane] = sum;
+    __syncthreads();
+    int run = 0;
+    for (int i = 0; i < warp; ++i) run += part[i][lane];
+    if (e < E) {
+        for (int b = b0; b < b1; ++b) {
+            const int64_t i = static_cast<int64_t>(b) * E + e;
+            const int c = p.counts[i];
+            p.counts[i] = run;
+            run += c;
+        }
+        if (warp == 31) p.totals[e] = run;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams p) {
+    const MoeRouteArgs &a = p.a;
+    int32_t *base = route_smem, *sums = base + a.E, *cnt = sums + kWarps;
+    for (int i = threadIdx.x; i < a.E; i += kThreads) base[i] = p.totals[i];
+    __syncthreads();
+    const int rows = block_scan(base, a.E, sums);
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < a.E; i += kThreads) a.offsets[i] = base[i];
+        if (threadIdx.x == 0) a.offsets[a.E] = rows;
+    }
+    const int64_t slots = static_cast<int64_t>(a.T) * a.k;
+    for (int64_t i = rows + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < slots;
+         i += static_cast<int64_t>(gridDim.x) * kThreads)
+        a.order[i] = -1;
+    __syncthreads();   // offsets are written from base, which the placing moves on
+    for (int i = threadIdx.x; i < a.E; i += kThreads) base[i] += p.counts[static_cast<int64_t>(blockIdx.x) * a.E + i];
+    __syncthreads();
+    const int t0 = static_cast<int>(blockIdx.x) * kTokens;
+    place(p, static_cast<int64_t>(t0) * a.k, min(kTokens, a.T - t0) * a.k, base, cnt);
+}
+
+// dlogits: a warp a token. With w the weights and d = dw - sum_j w_j dw_j a chosen
+// expert gets w d (softmax) or w d (1 - s) (sigmoid); the others get 0.
+__global__ void __launch_bounds__(kThreads)
+    route_backward_kernel(const float *__restrict__ dweights, const void *__restrict__ logits, int64_t ld,
+                          const int32_t *__restrict__ ids, const float *__restrict__ weights, void *__restrict__ dlogits,
+                          int64_t ldd, int T, int E, int k, int score, int dtype) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5; t < T;
+         t += (static_cast<int64_t>(gridDim.x) * kThreads) >> 5) {
+        int id = -1;
+        float w = 0.f, dw = 0.f;
+        if (lane < k) {
+            id = __ldg(ids + t * k + lane);
+            if (id >= E) id = -1;
+            w = id >= 0 ? __ldg(weights + t * k + lane) : 0.f;
+            dw = id >= 0 ? __ldg(dweights + t * k + lane) : 0.f;
+        }
+        float sum = w * dw;
+#pragma unroll
+        for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
+        float d = w * (dw - sum);
+        if (score == KP_SCORE_SIGMOID && id >= 0) d *= 1.f / (1.f + expf(logit_of(logits, t * ld + id, dtype)));   // 1 - s
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            float v = 0.f;
+            for (int j = 0; j < k; ++j) {
+                const int ej = __shfl_sync(0xFFFFFFFFu, id, j);
+                const float dj = __shfl_sync(0xFFFFFFFFu, d, j);
+                if (ej == e) v = dj;
+            }
+            if (e < E) {
+                if (dtype == KP_FP32)
+                    static_cast<float *>(dlogits)[t * ldd + e] = v;
+                else
+                    static_cast<uint16_t *>(dlogits)[t * ldd + e] = elem_round(v, dtype);
+            }
+        }
+    }
+}
+
+int blocks_of(int T) { return (T + kTokens - 1) / kTokens; }
+
+}  // namespace
+
+size_t moe_route_scratch(int T, int E) {
+    const int b = blocks_of(T);
+    return b > 1 ? (static_cast<size_t>(b) + 1) * E * sizeof(int32_t) : 0;
+}
+
+cudaError_t moe_route_launch(const MoeRouteArgs &a, const FfnDev &, cudaStream_t s) {
+    using Fn = void (*)(RouteParams);
+    static const Fn kernels[2][6] = {
+        {route_kernel<1, false>, route_kernel<2, false>, route_kernel<4, false>, route_kernel<8, false>,
+         route_kernel<16, false>, route_kernel<32, false>},
+        {route_kernel<1, true>, route_kernel<2, true>, route_kernel<4, true>, route_kernel<8, true>,
+         route_kernel<16, true>, route_kernel<32, true>}};
+    RouteParams p;
+    p.a = a;
+    p.blocks = blocks_of(a.T);
+    p.counts = static_cast<int32_t *>(a.work);
+    p.totals = p.blocks > 1 ? p.counts + static_cast<int64_t>(p.blocks) * a.E : nullptr;
+    int v = 0;
+    while (32 << v < a.E) ++v;
+    const size_t place = (static_cast<size_t>(a.E) * (1 + kWarps) + kWarps) * sizeof(int32_t);
+    if (p.blocks == 1) {
+        kernels[1][v]<<<1, kThreads, place, s>>>(p);
+        return cudaGetLastError();
+    }
+    kernels[0][v]<<<p.blocks, kThreads, a.E * sizeof(int32_t), s>>>(p);
+    route_scan_kernel<<<(a.E + 31) / 32, 1024, 0, s>>>(p);
+    route_place_kernel<<<p.blocks, kThreads, place, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t moe_route_backward_launch(const float *dweights, const void *logits, int64_t ld, const int32_t *ids,
+                                      const float *weights, void *dlogits, int64_t ldd, int T, int E, int k,
+                                      int score, int dtype, const FfnDev &d, cudaStream_t s) {
+    const int64_t blocks = (static_cast<int64_t>(T) + kWarps - 1) / kWarps;
+    route_backward_kernel<<<static_cast<int>(std::min<int64_t>(blocks, static_cast<int64_t>(d.sms) * 8)), kThreads, 0, s>>>(
+        dweights, logits, ld, ids, weights, dlogits, ldd, T, E, k, score, dtype);
+    return cudaGetLastError();
+}
+
+}  // namespace kp

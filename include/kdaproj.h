@@ -418,6 +418,108 @@ KP_API int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, in
                                  void *work, size_t work_bytes, kp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Mixture-of-experts operators: the router, the tokens' rows on their way to their
+ * experts and back, and products grouped by expert, each with its gradients. A layer is
+ *   kp_moe_route -> kp_moe_dispatch -> kp_grouped_gated_ffn -> kp_grouped_gemm ->
+ *   kp_moe_combine.
+ *
+ * Common to all of them, as to the feed-forward operators: matrices are row-major with
+ * the given row stride in elements and may be views into wider ones; work is enqueued on
+ * `stream` alone; sums are held in fp32 and rounded once to the output's type; the
+ * library allocates nothing and keeps nothing; workspaces (kp_moe_workspace) are the
+ * caller's, 256-byte aligned, one for each call in flight; calls can be captured into
+ * CUDA graphs; outputs must not overlap inputs or each other; results do not vary from
+ * run to run. Rows and columns outside the outputs that a function names are left as
+ * they were. At most 1024 experts and 32 of them a token.
+ *
+ * Expert order: the chosen (token, slot) pairs, slot < k, expert by expert, ascending
+ * in token * k + slot within an expert. offsets[e] .. offsets[e + 1] - 1 are expert e's rows
+ * (E + 1 ascending numbers from 0 to at most R); rows from offsets[E] on belong to
+ * nobody. The grouped products take any such offsets, whoever made them; they lie in
+ * device memory, so they are not checked, but no value of theirs leads outside [0, R). */
+
+enum kp_moe_op {
+    KP_MOE_ROUTE = 0,            /* M tokens, N experts, top K */
+    KP_MOE_GATED_BACKWARD = 1    /* M rows, N features, K columns */
+};
+/* Bytes of `work`, on the current device. */
+KP_API int kp_moe_workspace(int op, int M, int N, int K, size_t *bytes);
+
+/* Scores that the weights are taken from: softmax over the experts, or each expert's
+ * 1 / (1 + e^-logit). */
+enum kp_moe_score {
+    KP_SCORE_SOFTMAX = 0,
+    KP_SCORE_SIGMOID = 1
+};
+
+/* Each token's k experts with the largest logits, ties to the lowest expert (bias [E]
+ * fp32, sigmoid only: with the largest score plus bias), and their weights, the chosen
+ * scores over their sum. Experts with a logit of minus infinity or NaN (or that plus a
+ * bias) are not chosen: a slot that none is left for has id and position -1 and weight 0.
+ * A logit of plus infinity counts as the largest finite number.
+ *   logits    [T, E] of KP_BF16, KP_FP16 or KP_FP32, row stride ld
+ *   ids       [T, k], by descending logit (score plus bias)
+ *   weights   [T, k] fp32
+ *   offsets   [E + 1]
+ *   order     [T k]: the pair token * k + slot of each row, -1 from offsets[E] on
+ *   position  [T, k]: the row of each pair */
+KP_API int kp_moe_route(const void *logits, int64_t ld, const float *bias, int T, int E, int k, int score,
+                        int dtype, int32_t *ids, float *weights, int32_t *offsets, int32_t *order,
+                        int32_t *position, void *work, size_t work_bytes, kp_stream_t stream);
+/* dlogits [T, E] (of the logits' type, row stride ldd) from dweights [T, k]: with
+ * d_j = w_j (dw_j - sum_i w_i dw_i), a chosen expert's is d_j (softmax) or d_j times one
+ * minus its score (sigmoid), the others' 0. */
+KP_API int kp_moe_route_backward(const float *dweights, const void *logits, int64_t ld, const int32_t *ids,
+                                 const float *weights, void *dlogits, int64_t ldd, int T, int E, int k, int score,
+                                 int dtype, kp_stream_t stream);
+
+/* rows[position[t, s]] = x[t] for every slot that has a position. x [T, K], rows
+ * [T k, K] of dtype KP_BF16 or KP_FP16, 2-byte aligned. Positions outside [0, T k) count
+ * as none. The gradient of x is kp_moe_combine of the rows' without weights. */
+KP_API int kp_moe_dispatch(const void *x, int64_t ldx, const int32_t *position, void *rows, int64_t ldr, int T,
+                           int k, int K, int dtype, kp_stream_t stream);
+/* y[t] = round( sum_s weights[t, s] rows[position[t, s]] ), slots ascending; weights
+ * NULL: ones. A token without experts gets zeros. */
+KP_API int kp_moe_combine(const void *rows, int64_t ldr, const float *weights, const int32_t *position, void *y,
+                          int64_t ldy, int T, int k, int K, int dtype, kp_stream_t stream);
+/* Its gradients: drows[position[t, s]] = round( weights[t, s] dy[t] ), dweights[t, s] =
+ * dy[t] . rows[position[t, s]] in fp32 (0 for a slot without a position). */
+KP_API int kp_moe_combine_backward(const void *dy, int64_t lddy, const void *rows, int64_t ldr,
+                                   const float *weights, const int32_t *position, void *drows, int64_t lddr,
+                                   float *dweights, int T, int k, int K, int dtype, kp_stream_t stream);
+
+/* y[r] = round( x[r] W_e^T ) for every row r of every expert e. x [R, K], y [R, N], W
+ * [E, N, K] with row stride ldw and expert stride sw, all of dtype KP_BF16 or KP_FP16; x
+ * and W 16-byte aligned with K and strides multiples of 8. */
+KP_API int kp_grouped_gemm(const void *x, int64_t ldx, const void *W, int64_t ldw, int64_t sw, void *y,
+                           int64_t ldy, const int32_t *offsets, int R, int E, int N, int K, int dtype,
+                           kp_stream_t stream);
+/* dx[r] = round( dy[r] W_e ) and dW_e = round( sum_r dy[r]^T x[r] ) over the expert's rows;
+ * dy [R, N] 16-byte aligned with a row stride that is a multiple of 8, dW [E, N, K]
+ * contiguous and 16-byte aligned. An expert without rows gets zeros. */
+KP_API int kp_grouped_gemm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *W,
+                                    int64_t ldw, int64_t sw, void *dx, int64_t lddx, void *dW,
+                                    const int32_t *offsets, int R, int E, int N, int K, int dtype,
+                                    kp_stream_t stream);
+
+/* The gated block, an expert's weights for each row: h[r] = round( act(x[r] Wg_e^T) *
+ * (x[r] Wu_e^T) ); operands as above, Wg and Wu [E, F, K]. g and u (both or neither;
+ * contiguous fp32 [R, F], 16-byte aligned) receive the sums of the two products for the
+ * backward pass. */
+KP_API int kp_grouped_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg, int64_t sg,
+                                const void *Wu, int64_t ldu, int64_t su, void *h, int64_t ldh, float *g, float *u,
+                                const int32_t *offsets, int R, int E, int F, int K, int act, int dtype,
+                                kp_stream_t stream);
+/* Its gradients, as kp_gated_ffn_backward computes them (dG and dU rounded to dtype, in
+ * fp16 as multiples of one power of two): dx [R, K], dWg and dWu [E, F, K] contiguous and
+ * 16-byte aligned. An expert without rows gets zeros. */
+KP_API int kp_grouped_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx,
+                                         const void *Wg, int64_t ldg, int64_t sg, const void *Wu, int64_t ldu,
+                                         int64_t su, const float *g, const float *u, void *dx, int64_t lddx,
+                                         void *dWg, void *dWu, const int32_t *offsets, int R, int E, int F, int K,
+                                         int act, int dtype, void *work, size_t work_bytes, kp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Diagnostics. */
 KP_API const char *kp_last_error(void);           /* thread-local, never NULL */
 KP_API int kp_version(void);                       /* KDAPROJ_VERSION */
