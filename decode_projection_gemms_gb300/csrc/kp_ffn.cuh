@@ -32,6 +32,9 @@ int ffn_device(FfnDev *out);   // KP_OK, or a status with the message set (KP_ED
 constexpr int kMapU8 = 16, kMapF32 = 17;
 cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld,
                            int box_rows, int box_cols, int dtype, bool swizzle = true);
+// The same for matrices [n][rows][cols] `step` elements apart, boxes of 64 columns.
+cudaError_t ffn_tensor_map3(CUtensorMap *map, const void *ptr, int64_t n, int64_t rows, int64_t cols, int64_t ld,
+                            int64_t step, int box_rows, int dtype);
 // The scale tiles of a microscaled matrix, 512 bytes each, boxes of two.
 cudaError_t ffn_scale_map(CUtensorMap *map, const void *scales, int64_t tiles);
 // Shared memory to request for a CTA that holds `cols` TMEM columns: at least

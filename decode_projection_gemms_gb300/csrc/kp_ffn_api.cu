@@ -54,6 +54,22 @@ cudaError_t ffn_tensor_map(CUtensorMap *map, const void *ptr, int64_t rows, int6
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t ffn_tensor_map3(CUtensorMap *map, const void *ptr, int64_t n, int64_t rows, int64_t cols, int64_t ld,
+                            int64_t step, int box_rows, int dtype) {
+    EncodeFn enc;
+    cudaError_t e = encoder(&enc);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(n > 1 ? step : ld * rows) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, dtype == KP_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                           const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t ffn_scale_map(CUtensorMap *map, const void *scales, int64_t tiles) {
     EncodeFn enc;
     cudaError_t e = encoder(&enc);

@@ -72,18 +72,3 @@ struct GroupedArgs {
 cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s);
 
 }  // namespace kp
-
-#if defined(__CUDACC__)
-
-namespace kp {
-
-// Rows [first, first + count) of expert e. Offsets come from device memory: whatever
-// they hold, the rows lie within [0, R).
-__device__ __forceinline__ void expert_rows(const int32_t *offsets, int e, int R, int &first, int &count) {
-    first = min(max(__ldg(offsets + e), 0), R);
-    count = max(min(max(__ldg(offsets + e + 1), 0), R) - first, 0);
-}
-
-}  // namespace kp
-
-#endif  // __CUDACC__

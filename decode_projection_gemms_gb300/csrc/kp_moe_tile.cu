@@ -1,111 +1,620 @@
-// Products grouped by expert.
+// Products grouped by expert: out[n, m] = sum_k A[m, k] B[n, k] with fp32 accumulation,
+// where n runs over an expert's rows (the weights' gradients: over features) and m along
+// a row of the output.
+//
+// The features lie on the MMA's 256 rows and the tokens on its columns, so that a
+// tile is as wide as its expert has rows, in steps of 32: ragged sizes cost little, and
+// with a row or two an expert the kernel streams weights. Two CTAs of a cluster (an SM
+// pair) compute one 256 x nt tile (nt up to 256) with tcgen05.mma.cta_group::2: each
+// holds 128 rows of A, half of B's nt rows and the accumulator of its own A. The
+// leader's warp 1 issues every MMA; both CTAs' copies complete on the leader's barriers,
+// and tcgen05.commit returns stages and accumulators to both. Clusters are persistent: a
+// cluster takes items c, c + n, ... of a list that every CTA reads off the experts'
+// offsets in device memory; the host knows only how many rows there may be.
+//
+//   PLAIN   A = W_e (K contiguous), B = rows of x.
+//   GATED   A = 64 rows of Wg_e and the same ones of Wu_e per CTA: gates are in
+//           accumulator lanes 0 .. 63 and their factors in lanes 64 .. 127, and the warps
+//           that read them swap halves through shared memory, eight rows at a time.
+//   DGRAD   A = W_e read along its rows (the MMA's transposed operand), B = rows of the
+//           output's gradient; two products into one accumulator for the gated block.
+//   WGRAD   A = x, B = the output's gradient, both transposed, contracted over the
+//           expert's rows. The block of 64 that an expert's rows end in also brings rows
+//           of others: MMA steps of 16 past the end are left out, and in the step that
+//           the end is in, warp 10 of both CTAs clears the others' rows first.
+//
+// An accumulator's lanes are columns of the output: a warp stores 32 of them (64 bytes)
+// of two rows at a time.
+//
+// Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 9: epilogue; warp 10: WGRAD.
+#include <algorithm>
+#include <mutex>
+
 #include "kp_moe.cuh"
 
 namespace kp {
 
 namespace {
 
-constexpr int kT = 64, kKb = 16;
+constexpr int kThreads = 320, kThreadsW = 352;
+constexpr int kTile = 256;                // rows of A per cluster; of B at most
+constexpr uint32_t kHalf = 128 * 128;     // bytes of 128 rows of a K block (128 bytes of K)
+constexpr size_t kMaxSmem = 227 * 1024;
+constexpr int kMaxStages = 12;
+constexpr uint32_t kSwap = 1024;          // gated: eight rows of 32 gates or factors
+constexpr uint32_t kSwapBytes = 8 * 2 * kSwap;
+constexpr size_t kBarBytes = (3 * kMaxStages + 4) * 8 + 16;
 
-struct GroupedParams {
-    GroupedArgs a;
-    int tiles_m;
+struct GroupedMaps {
+    CUtensorMap a0, a1, b0, b1;
 };
 
-// out[n][m] = sum_k A[m, k] B[n, k] for one 64 x 64 tile; n the rows (WGRAD: features).
-template <int kForm>
-__global__ void __launch_bounds__(256) grouped_kernel(const GroupedParams p) {
-    const GroupedArgs &a = p.a;
-    __shared__ float sa[2][kKb][kT + 1], sb[2][kKb][kT + 1];
-    const uint16_t *x = static_cast<const uint16_t *>(a.x);
-    const int e = blockIdx.z;
-    int first, count;
-    expert_rows(a.offsets, e, a.R, first, count);
-    const int tm = blockIdx.x * kT;
-    const int cols = kForm == GROUPED_DGRAD || kForm == GROUPED_WGRAD ? a.K : a.N;
-    const int rows = kForm == GROUPED_WGRAD ? a.N : count;
-    const int depth = kForm == GROUPED_WGRAD ? count : kForm == GROUPED_DGRAD ? a.N : a.K;
-    const bool two = kForm == GROUPED_GATED || a.d1;
-    const float scale = a.scale ? __ldg(a.scale) : 1.f;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int tn = blockIdx.y * kT; tn < rows; tn += gridDim.y * kT) {
-        float acc[2][4][4] = {};
-        for (int q = 0; q < (two ? 2 : 1); ++q) {
-            const MoeMat &w = q ? a.w1 : a.w0;
-            const uint16_t *W = static_cast<const uint16_t *>(w.p) + e * w.se;
-            const uint16_t *d = static_cast<const uint16_t *>(q ? a.d1 : a.d0);
-            for (int k0 = 0; k0 < depth; k0 += kKb) {
-                for (int i = threadIdx.x; i < kT * kKb; i += 256) {
-                    const int m = kForm == GROUPED_PLAIN || kForm == GROUPED_GATED ? i / kKb : i % kT;
-                    const int k = kForm == GROUPED_PLAIN || kForm == GROUPED_GATED ? i % kKb : i / kT;
-                    float va = 0.f, vb = 0.f;
-                    if (k0 + k < depth && tm + m < cols) {
-                        const uint16_t *s = kForm == GROUPED_WGRAD   ? x + static_cast<int64_t>(first + k0 + k) * a.ldx + tm + m
-                                            : kForm == GROUPED_DGRAD ? W + static_cast<int64_t>(k0 + k) * w.ld + tm + m
-                                                                     : W + static_cast<int64_t>(tm + m) * w.ld + k0 + k;
-                        va = elem_widen(*s, a.dtype);
-                    }
-                    if (k0 + k < depth && tn + m < rows) {
-                        const uint16_t *s = kForm == GROUPED_WGRAD   ? d + static_cast<int64_t>(first + k0 + k) * a.ldd + tn + m
-                                            : kForm == GROUPED_DGRAD ? d + static_cast<int64_t>(first + tn + m) * a.ldd + k0 + k
-                                                                     : x + static_cast<int64_t>(first + tn + m) * a.ldx + k0 + k;
-                        vb = elem_widen(*s, a.dtype);
-                    }
-                    sa[0][k][m] = va;
-                    sb[0][k][m] = vb;
-                }
-                __syncthreads();
-                float(&c)[4][4] = acc[kForm == GROUPED_DGRAD ? 0 : q];
+struct GroupedParams {
+    const int32_t *offsets;
+    uint16_t *y0, *y1;
+    float *g, *u;
+    int64_t ldy;
+    const float *scale;
+    int *err;
+    int R, E, N;
+    int M;                // columns of the output
+    int rows_n;           // WGRAD: rows of the output (features)
+    int tiles_m, tiles_n; // WGRAD: tiles along both
+    int products;         // DGRAD: into one accumulator; WGRAD: outputs
+    int KB, K;            // K blocks (DGRAD: of one product) and columns of the contraction (not WGRAD)
+    int nt;               // WGRAD: B's rows per tile; else at most
+    int box;              // rows of a copy of B
+    int stages;
+    uint32_t stage_bytes, idesc;
+    int act, dtype;
+    int pairs;            // the output's rows start on 4 bytes
+};
+
+__device__ __forceinline__ void pair_load2(uint32_t dst, const void *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void pair_load3(uint32_t dst, const void *map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+// On a barrier of this CTA.
+__device__ __forceinline__ void own_load2(uint32_t dst, const void *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint32_t bar) {   // the same barrier in both CTAs
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {   // shared::cluster address
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// Operand stored with M / N contiguous, 128-byte swizzle: 64-element groups 8 KB apart
+// (64 K rows of 128 bytes), 8 K rows 1 KB apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(8192 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+
+// n columns' sums of this thread's accumulator lane, column m of the output, into rows
+// 0 .. n - 1 from dst on (those below `rows`). Two lanes swap a value, so that each
+// stores two columns of every other row.
+template <int N>
+__device__ __forceinline__ void put_columns(uint16_t *dst, int64_t ld, const float (&v)[N], int m, int M, int rows,
+                                            int dtype, bool pairs) {
+    if (pairs) {
+        const bool odd = m & 1;
+        const int me = m & ~1;
+        uint16_t *d = dst + me + (odd ? ld : 0);
 #pragma unroll
-                for (int k = 0; k < kKb; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) c[i][j] = fmaf(sb[0][k][ty * 4 + i], sa[0][k][tx + 16 * j], c[i][j]);
-                __syncthreads();
+        for (int j = 0; j < N; j += 2) {
+            const uint32_t lo = elem_round(v[j], dtype), hi = elem_round(v[j + 1], dtype);
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
+            const uint32_t w = odd ? other | hi << 16 : lo | other << 16;
+            if (j + (odd ? 1 : 0) < rows) {
+                if (me + 1 < M)
+                    *reinterpret_cast<uint32_t *>(d + j * ld) = w;
+                else if (me < M)
+                    d[j * ld] = static_cast<uint16_t>(w);
             }
         }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int n = tn + ty * 4 + i, m = tm + tx + 16 * j;
-                if (n >= rows || m >= cols) continue;
-                if (kForm == GROUPED_WGRAD) {
-                    const int64_t at = (static_cast<int64_t>(e) * a.N + n) * a.K + m;
-                    static_cast<uint16_t *>(a.y0)[at] = elem_round(acc[0][i][j] * scale, a.dtype);
-                    if (two) static_cast<uint16_t *>(a.y1)[at] = elem_round(acc[1][i][j] * scale, a.dtype);
-                } else {
-                    float v = acc[0][i][j] * scale;
-                    if (kForm == GROUPED_GATED) {
-                        const float ga[1] = {acc[0][i][j]}, ub[1] = {acc[1][i][j]};
-                        float h[1];
-                        ffn_gate(ga, ub, a.act, h);
-                        v = h[0];
-                        if (a.g) {
-                            a.g[static_cast<int64_t>(first + n) * a.N + m] = ga[0];
-                            a.u[static_cast<int64_t>(first + n) * a.N + m] = ub[0];
-                        }
-                    }
-                    static_cast<uint16_t *>(a.y0)[(first + n) * a.ldy + m] = elem_round(v, a.dtype);
-                }
-            }
+    } else if (m < M) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < rows) dst[j * ld + m] = elem_round(v[j], dtype);
     }
 }
+
+template <int kForm>
+__global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads, 1) __cluster_dims__(2, 1, 1)
+    grouped_kernel(const __grid_constant__ GroupedMaps tm, const GroupedParams p) {
+    constexpr bool kGated = kForm == GROUPED_GATED;
+    constexpr bool kD = kForm == GROUPED_DGRAD;
+    constexpr bool kW = kForm == GROUPED_WGRAD;
+
+    extern __shared__ uint8_t gt_smem_raw[];
+    const uint32_t raw = smem_u32(gt_smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = gt_smem_raw + (base - raw);
+    const int S = p.stages;
+    const uint32_t swap0 = base + S * p.stage_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + S * p.stage_bytes + (kGated ? kSwapBytes : 0));
+    uint64_t *empty = full + kMaxStages;
+    uint64_t *ends = empty + kMaxStages;      // WGRAD: copies of a block that an expert's rows end in
+    uint64_t *accf = ends + kMaxStages;
+    uint64_t *acce = accf + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int32_t *first = reinterpret_cast<int32_t *>(tmem_slot + 4);   // [E] of each expert's rows,
+    int32_t *count = first + p.E;                                  // [E] how many,
+    int32_t *tiles = count + p.E;                                  // [E + 1] tiles of the experts before
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int cid = static_cast<int>(blockIdx.x) >> 1;
+    const int nclu = static_cast<int>(gridDim.x) >> 1;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(full + s), kW ? 2 : 1);
+            mbar_init(smem_u32(empty + s), 1);
+            mbar_init(smem_u32(ends + s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(accf + i), 1);
+            mbar_init(smem_u32(acce + i), 16);   // eight epilogue warps of each CTA
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (warp == 2) {   // the experts' rows, and the sums of their tiles
+        // Whatever the offsets hold, the rows lie within [0, R) and no two experts
+        // have the same: an expert's begin at the largest number up to its own.
+        int run = 0, most = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            int f = e <= p.E ? min(max(__ldg(p.offsets + e), 0), p.R) : 0;
+            f = max(f, most);
+            int next = e < p.E ? min(__ldg(p.offsets + e + 1), p.R) : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) f = max(f, __shfl_up_sync(0xFFFFFFFFu, f, d));
+            next = max(next, f);
+            most = __shfl_sync(0xFFFFFFFFu, next, 31);
+            const int c = e < p.E ? next - f : 0;
+            int t = (c + kTile - 1) / kTile;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
+                if (lane >= d) t += o;
+            }
+            if (e < p.E) {
+                first[e] = f;
+                count[e] = c;
+                tiles[e + 1] = run + t;
+            }
+            run += __shfl_sync(0xFFFFFFFFu, t, 31);
+        }
+        if (lane == 0) tiles[0] = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync_all();   // barriers of both CTAs exist
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    struct Item {
+        int e, z;             // expert; WGRAD: which output
+        int m0, n0, rows;     // first row of A, first row of B, rows of B that count
+        int nt, kb;           // MMA columns, K blocks
+    };
+    // The i-th item of this cluster, e at or behind `it`'s last; false when there is none.
+    auto get = [&](int i, Item &it) {
+        const int j = cid + i * nclu;
+        if constexpr (kW) {
+            const int per = p.tiles_m * p.tiles_n * p.products;
+            it.e = j / per;
+            if (it.e >= p.E) return false;
+            int l = j - it.e * per;
+            it.z = l / (p.tiles_m * p.tiles_n);
+            l -= it.z * p.tiles_m * p.tiles_n;
+            it.m0 = l % p.tiles_m * kTile;
+            it.n0 = l / p.tiles_m * p.nt;
+            it.rows = min(p.rows_n - it.n0, p.nt);
+            it.nt = p.nt;
+            it.kb = (count[it.e] + 63) >> 6;
+        } else {
+            const int t = j / p.tiles_m;
+            if (t >= tiles[p.E]) return false;
+            while (tiles[it.e + 1] <= t) ++it.e;
+            const int n = tiles[it.e + 1] - tiles[it.e];
+            const int l = j - tiles[it.e] * p.tiles_m;
+            const int c = count[it.e];
+            const int per = ((c + n - 1) / n + 31) & ~31;   // rows of a tile, about even; 256 at most,
+                                                             // so that the last one has some
+            it.m0 = l / n * (kGated ? 128 : kTile);
+            it.n0 = l % n * per;
+            it.rows = min(c - it.n0, per);
+            it.nt = (it.rows + 31) & ~31;
+            it.kb = p.KB * (kD ? p.products : 1);
+        }
+        return true;
+    };
+
+    if (warp == 0) {
+        const bool mine = elect_one();
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0);   // the leader's barriers
+        int stage = 0;
+        uint32_t phase = 1;   // a fresh barrier passes a wait for the phase before its first
+        Item it = {};
+        for (int i = 0; get(i, it); ++i) {
+            const int row0 = first[it.e];
+            const int half = it.nt >> 1;
+            const int boxes = kW ? half >> 6 : (half + p.box - 1) / p.box;
+            const uint32_t bytes = kHalf + static_cast<uint32_t>(boxes) * (kW ? 8192u : static_cast<uint32_t>(p.box) * 128u);
+            const int left = kW ? count[it.e] & 15 : 0;          // an end within an MMA's 16 rows
+            for (int kb = 0; kb < it.kb; ++kb) {
+                mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
+                const uint32_t st = base + stage * p.stage_bytes;
+                const uint32_t bar = full0 + 8 * stage;
+                const int s = stage;
+                if (++stage == S) stage = 0, phase ^= 1;
+                if (!mine) continue;
+                if constexpr (kW) {
+                    const int m = it.m0 + rank * 128, n = it.n0 + rank * half;
+                    const int r = row0 + kb * 64;
+                    const CUtensorMap *mb = it.z ? &tm.b1 : &tm.b0;
+                    if (left && kb == it.kb - 1) {   // on a barrier of this CTA's, which warp 10 waits for
+                        const uint32_t own = smem_u32(ends + s);
+                        mbar_expect_tx(own, bytes);
+                        own_load2(st, &tm.a0, own, m, r);
+                        own_load2(st + 8192, &tm.a0, own, m + 64, r);
+                        for (int b = 0; b < boxes; ++b) own_load2(st + kHalf + b * 8192, mb, own, n + b * 64, r);
+                        continue;
+                    }
+                    if (rank == 0)
+                        mbar_expect_tx(smem_u32(full + s), 2 * bytes);
+                    else
+                        remote_arrive(bar);
+                    pair_load2(st, &tm.a0, bar, m, r);
+                    pair_load2(st + 8192, &tm.a0, bar, m + 64, r);
+                    for (int b = 0; b < boxes; ++b) pair_load2(st + kHalf + b * 8192, mb, bar, n + b * 64, r);
+                } else {
+                    if (rank == 0) mbar_expect_tx(smem_u32(full + s), 2 * bytes);
+                    const bool second = kD && kb >= p.KB;
+                    const int k = (second ? kb - p.KB : kb) * 64;
+                    const CUtensorMap *ma = second ? &tm.a1 : &tm.a0;
+                    if constexpr (kGated) {
+                        const int f = it.m0 + rank * 64;
+                        pair_load3(st, &tm.a0, bar, k, f, it.e);
+                        pair_load3(st + 8192, &tm.a1, bar, k, f, it.e);
+                    } else if constexpr (kD) {
+                        const int m = it.m0 + rank * 128;
+                        pair_load3(st, ma, bar, m, k, it.e);
+                        pair_load3(st + 8192, ma, bar, m + 64, k, it.e);
+                    } else {
+                        pair_load3(st, ma, bar, k, it.m0 + rank * 128, it.e);
+                    }
+                    const int n = row0 + it.n0 + rank * half;
+                    const CUtensorMap *mb = second ? &tm.b1 : &tm.b0;
+                    for (int b = 0; b < boxes; ++b) pair_load2(st + kHalf + b * p.box * 128, mb, bar, k, n + b * p.box);
+                }
+            }
+        }
+        // Every copy of this CTA has landed, and every MMA that reads its shared memory
+        // has completed, before it leaves: each stage's last round was returned (a stage
+        // without a round passes at once). After a wait that ran out MMAs are issued, and
+        // their stages returned, without their copies: the leader, which the other CTA
+        // does not leave before, waits for those of both as well.
+        for (int t = 0; t < S; ++t) {
+            ffn_drain_wait(smem_u32(empty + stage), phase);
+            if (rank == 0) ffn_drain_wait(smem_u32(full + stage), phase);
+            if (++stage == S) stage = 0, phase ^= 1;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // As in the tile kernel of the feed-forward operators: the next stage is
+            // waited for before the last MMA of this one is issued.
+            const bool mine = elect_one();
+            int stage = 0, as = 0;
+            uint32_t phase = 0, aphase = 1;
+            auto prepare = [&](int s, uint32_t ph, const Item &x, int kb) {
+                mbar_wait_bounded(smem_u32(full + s), ph, abort_flag, p.err, DEV_TIMEOUT_FULL);
+                if (kW && kb == x.kb - 1 && (count[x.e] & 15)) acquire_cluster();   // rows cleared by the other CTA
+                tc_fence_after();
+            };
+            // the next item with a contraction
+            auto find = [&](int &i, Item &it) {
+                while (get(i, it)) {
+                    if (it.kb) return true;
+                    ++i;
+                }
+                return false;
+            };
+            Item it = {}, next;
+            int i = 0;
+            bool more_items = find(i, it);
+            if (more_items) prepare(0, 0, it, 0);
+            while (more_items) {
+                next = it;
+                ++i;
+                more_items = find(i, next);
+                const uint32_t idesc = p.idesc | static_cast<uint32_t>(it.nt >> 3) << 17;
+                const int depth = kW ? count[it.e] : p.K;
+                mbar_wait_bounded(smem_u32(acce + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(as) * 256;
+                for (int kb = 0; kb < it.kb; ++kb) {
+                    const uint32_t st = base + stage * p.stage_bytes;
+                    const uint64_t ad = kW || kD ? desc_mn(st) : desc_kmajor(st);
+                    const uint64_t bd = kW ? desc_mn(st + kHalf) : desc_kmajor(st + kHalf);
+                    const uint32_t bar = smem_u32(empty + stage);
+                    const int at = kD && kb >= p.KB ? kb - p.KB : kb;
+                    const int steps = min(4, (depth - at * 64 + 15) >> 4);
+                    auto mma = [&](int kk) {
+                        if (mine)
+                            pair_mma(d, ad + kk * (kW || kD ? 128 : 2), bd + kk * (kW ? 128 : 2), idesc, kb > 0 || kk > 0);
+                    };
+#pragma unroll
+                    for (int kk = 0; kk < 3; ++kk)
+                        if (kk < steps) mma(kk);
+                    if (++stage == S) stage = 0, phase ^= 1;
+                    if (kb + 1 < it.kb)
+                        prepare(stage, phase, it, kb + 1);
+                    else if (more_items)
+                        prepare(stage, phase, next, 0);
+                    if (steps > 3) mma(3);
+                    if (mine) pair_commit(bar);
+                }
+                if (mine) pair_commit(smem_u32(accf + as));
+                if (++as == 2) as = 0, aphase ^= 1;
+                it = next;
+            }
+        }
+        __syncwarp();
+    } else if (warp < 10) {
+        // Two warps for each quarter of the accumulator's lanes, every other 32 columns each.
+        const int q = warp & 3;
+        const int half = warp >= 6;
+        const float scale = p.scale ? __ldg(p.scale) : 1.f;   // a power of two
+        int as = 0;
+        uint32_t aphase = 0;
+        uint32_t parity = 0;
+        Item it = {};
+        for (int i = 0; get(i, it); ++i) {
+            const int m = it.m0 + (kGated ? rank * 64 + (q & 1) * 32 : rank * 128 + q * 32) + lane;
+            uint16_t *dst = p.y0;
+            if constexpr (kW)
+                dst = (it.z ? p.y1 : p.y0) + (static_cast<int64_t>(it.e) * p.rows_n + it.n0) * p.ldy;
+            else
+                dst += static_cast<int64_t>(first[it.e] + it.n0) * p.ldy;
+            if (kW && it.kb == 0) {   // an expert without rows
+                const float zero[32] = {};
+                for (int c = 32 * half; c < it.nt; c += 64)
+                    put_columns(dst + c * p.ldy, p.ldy, zero, m, p.M, it.rows - c, p.dtype, p.pairs);
+                continue;
+            }
+            mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
+            tc_fence_after();
+            const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16);
+            for (int c = 32 * half; c < it.nt; c += 64) {
+                uint32_t v[32];
+                tmem_ld32(t + c, v);
+                tmem_ld_wait();
+                if constexpr (kGated) {
+                    // Partner q ^ 2 has the factors of these gates: this warp takes the first
+                    // eight of every 16 rows, the other the last.
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t mine = swap0 + (static_cast<uint32_t>(warp - 2) * 2 + parity) * kSwap + lane * 4;
+                        const uint32_t theirs = swap0 + (static_cast<uint32_t>((warp - 2) ^ 2) * 2 + parity) * kSwap + lane * 4;
+                        float own[8], got[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t lo = v[16 * s + j], hi = v[16 * s + 8 + j];
+                            own[j] = __uint_as_float(q < 2 ? lo : hi);
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + j * 128), "r"(q < 2 ? hi : lo) : "memory");
+                        }
+                        named_bar_sync(1 + 2 * half + (q & 1), 64);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(got[j]) : "r"(theirs + j * 128) : "memory");
+                        parity ^= 1;
+                        float a[8], b[8], h[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            a[j] = q < 2 ? own[j] : got[j];
+                            b[j] = q < 2 ? got[j] : own[j];
+                        }
+                        const int n = c + 16 * s + (q < 2 ? 0 : 8);
+                        const int rows = it.rows - n;
+                        if (rows <= 0) continue;
+                        if (p.g && m < p.M) {
+                            const int64_t at = static_cast<int64_t>(first[it.e] + it.n0 + n) * p.M + m;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (j < rows) {
+                                    p.g[at + static_cast<int64_t>(j) * p.M] = a[j];
+                                    p.u[at + static_cast<int64_t>(j) * p.M] = b[j];
+                                }
+                        }
+                        ffn_gate(a, b, p.act, h);
+                        put_columns(dst + n * p.ldy, p.ldy, h, m, p.M, rows, p.dtype, p.pairs);
+                    }
+                } else {
+                    float a[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(v[j]) * scale;
+                    put_columns(dst + c * p.ldy, p.ldy, a, m, p.M, it.rows - c, p.dtype, p.pairs);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) remote_arrive(mapa_shared(smem_u32(acce + as), 0));
+            if (++as == 2) as = 0, aphase ^= 1;
+        }
+        __syncwarp();
+    } else if constexpr (kW) {
+        // Rows of others behind an expert's last one, within the MMA step that it is in.
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        uint32_t seen = 0;   // phases of `ends`, a bit a stage
+        int64_t at = 0;      // K blocks before this item
+        Item it = {};
+        for (int i = 0; get(i, it); ++i) {
+            const int left = count[it.e] & 15;
+            at += it.kb;
+            if (!it.kb || !left) continue;
+            const int s = static_cast<int>((at - 1) % S);
+            mbar_wait_bounded(smem_u32(ends + s), (seen >> s) & 1, abort_flag, p.err, DEV_TIMEOUT_FULL);
+            seen ^= 1u << s;
+            const int r0 = count[it.e] & 63, n = 16 - left;      // K rows r0 .. r0 + n - 1 of every 8 KB group
+            const int groups = 2 + (it.nt >> 7);
+            for (int x = lane; x < groups * n * 8; x += 32) {
+                const int gr = x / (n * 8), y = x - gr * n * 8;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 base + s * p.stage_bytes + gr * 8192 + r0 * 128 + y * 16),
+                             "r"(0)
+                             : "memory");
+            }
+            // the tensor cores read them through the asynchronous proxy
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) remote_arrive(full0 + 8 * s);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync_all();   // the peer is done with this CTA's barriers and memory
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+std::mutex g_mu;
+bool g_ready[64];   // devices whose kernels have their shared memory raised
 
 }  // namespace
 
 cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s) {
-    GroupedParams p;
-    p.a = a;
-    const bool wgrad = a.form == GROUPED_WGRAD;
-    const int cols = wgrad || a.form == GROUPED_DGRAD ? a.K : a.N;
-    const int rows = wgrad ? a.N : a.R;
-    const dim3 grid((cols + kT - 1) / kT, rows < 64 * kT ? (rows + kT - 1) / kT : 64, a.E);
-    switch (a.form) {
-    case GROUPED_PLAIN: grouped_kernel<GROUPED_PLAIN><<<grid, 256, 0, s>>>(p); break;
-    case GROUPED_GATED: grouped_kernel<GROUPED_GATED><<<grid, 256, 0, s>>>(p); break;
-    case GROUPED_DGRAD: grouped_kernel<GROUPED_DGRAD><<<grid, 256, 0, s>>>(p); break;
-    default: grouped_kernel<GROUPED_WGRAD><<<grid, 256, 0, s>>>(p); break;
+    using Fn = void (*)(GroupedMaps, GroupedParams);
+    static const Fn kernels[] = {grouped_kernel<GROUPED_PLAIN>, grouped_kernel<GROUPED_GATED>,
+                                 grouped_kernel<GROUPED_DGRAD>, grouped_kernel<GROUPED_WGRAD>};
+    cudaError_t e = cudaSuccess;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (d.dev >= 64 || !g_ready[d.dev]) {
+            for (Fn f : kernels)
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
+            if (e != cudaSuccess) return e;
+            if (d.dev < 64) g_ready[d.dev] = true;
+        }
     }
+    const bool gated = a.form == GROUPED_GATED, dgrad = a.form == GROUPED_DGRAD, wgrad = a.form == GROUPED_WGRAD;
+    GroupedParams p = {};
+    p.offsets = a.offsets;
+    p.y0 = static_cast<uint16_t *>(a.y0);
+    p.y1 = static_cast<uint16_t *>(a.y1);
+    p.g = a.g;
+    p.u = a.u;
+    p.ldy = a.ldy;
+    p.scale = a.scale;
+    p.err = a.err;
+    p.R = a.R;
+    p.E = a.E;
+    p.N = a.N;
+    p.M = dgrad || wgrad ? a.K : a.N;
+    p.rows_n = a.N;
+    p.tiles_m = cdiv(p.M, gated ? 128 : kTile);
+    p.products = a.d1 ? 2 : 1;
+    p.K = dgrad ? a.N : a.K;
+    p.KB = cdiv(p.K, 64);
+    p.act = a.act;
+    p.dtype = a.dtype;
+    p.pairs = ((reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1) | static_cast<uintptr_t>(a.ldy * 2)) & 3) == 0;
+    p.idesc = idesc_f16(a.dtype, 256, 0, dgrad || wgrad, wgrad);
+    int64_t items;
+    int half;   // rows of B that a CTA holds at most
+    if (wgrad) {
+        p.nt = a.N <= 128 ? 128 : kTile;
+        p.tiles_n = cdiv(a.N, p.nt);
+        half = p.nt / 2;
+        items = static_cast<int64_t>(a.E) * p.tiles_m * p.tiles_n * p.products;
+    } else {
+        // copies of B: as few as there are rows for, without many rows of other experts
+        p.nt = a.R < kTile ? (a.R + 31) / 32 * 32 : kTile;
+        const int mean = a.R / a.E;
+        p.box = std::min(mean >= 128 ? 64 : mean >= 32 ? 32 : 16, p.nt / 2);
+        half = cdiv(p.nt / 2, p.box) * p.box;
+        items = (static_cast<int64_t>(a.R) / kTile + std::min(a.E, a.R)) * p.tiles_m;
+    }
+    if (items > (1 << 30)) return cudaErrorInvalidValue;
+    p.stage_bytes = kHalf + static_cast<uint32_t>(half) * 128;
+    const size_t fixed = 1024 + (gated ? kSwapBytes : 0) + kBarBytes + (3 * static_cast<size_t>(a.E) + 1) * sizeof(int32_t);
+    p.stages = std::min<int>(kMaxStages, static_cast<int>((kMaxSmem - fixed) / p.stage_bytes));
+
+    GroupedMaps tm = {};
+    auto experts = [&](CUtensorMap *m, const MoeMat &w, int box_rows) {
+        if (e == cudaSuccess) e = ffn_tensor_map3(m, w.p, a.E, a.N, a.K, w.ld, w.se, box_rows, a.dtype);
+    };
+    auto rows = [&](CUtensorMap *m, const void *ptr, int cols, int64_t ld, int box_rows) {
+        if (e == cudaSuccess) e = ffn_tensor_map(m, ptr, a.R, cols, ld, box_rows, 64, a.dtype);
+    };
+    if (wgrad) {
+        rows(&tm.a0, a.x, a.K, a.ldx, 64);
+        rows(&tm.b0, a.d0, a.N, a.ldd, 64);
+        if (a.d1) rows(&tm.b1, a.d1, a.N, a.ldd, 64);
+    } else if (dgrad) {
+        experts(&tm.a0, a.w0, 64);
+        rows(&tm.b0, a.d0, a.N, a.ldd, p.box);
+        if (a.d1) {
+            experts(&tm.a1, a.w1, 64);
+            rows(&tm.b1, a.d1, a.N, a.ldd, p.box);
+        }
+    } else {
+        experts(&tm.a0, a.w0, gated ? 64 : 128);
+        if (gated) experts(&tm.a1, a.w1, 64);
+        rows(&tm.b0, a.x, a.K, a.ldx, p.box);
+    }
+    if (e != cudaSuccess) return e;
+    size_t smem = 0;
+    if ((e = ffn_smem_for_tmem(d.dev, 512, fixed + static_cast<size_t>(p.stages) * p.stage_bytes, &smem)) != cudaSuccess)
+        return e;
+    const int clusters = static_cast<int>(std::min<int64_t>(items, d.sms / 2));
+    kernels[a.form]<<<2 * clusters, wgrad ? kThreadsW : kThreads, smem, s>>>(tm, p);
     return cudaGetLastError();
 }
 

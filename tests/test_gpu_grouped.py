@@ -289,7 +289,7 @@ def test_a_layer():
     # rounding, relative to the whole
     for name, got, want in (("y", y, ref), ("dx", dx, v["x"].grad), ("dWg", dWg, v["Wg"].grad), ("dWu", dWu, v["Wu"].grad),
                             ("dWd", dWd, v["Wd"].grad), ("dlogits", dl, v["l"].grad)):
-        err = float((got.double() - want.detach()).norm() / want.norm())
+        err = float((got.double() - want.detach()).norm() / want.detach().norm())
         assert err < 6 * 2.0 ** -8, (name, err)
     assert (y[100:] == 0).all() and (dx[100:] == 0).all() and (dl[100:] == 0).all()
     quiet()
