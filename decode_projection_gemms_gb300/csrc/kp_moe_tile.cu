@@ -15,7 +15,7 @@
 //   PLAIN   A = W_e (K contiguous), B = rows of x.
 //   GATED   A = 64 rows of Wg_e and the same ones of Wu_e per CTA: gates are in
 //           accumulator lanes 0 .. 63 and their factors in lanes 64 .. 127, and the warps
-//           that read them swap halves through shared memory, eight rows at a time.
+//           that read them swap halves through shared memory.
 //   DGRAD   A = W_e read along its rows (the MMA's transposed operand), B = rows of the
 //           output's gradient; two products into one accumulator for the gated block.
 //   WGRAD   A = x, B = the output's gradient, both transposed, contracted over the
@@ -23,8 +23,10 @@
 //           of others: MMA steps of 16 past the end are left out, and in the step that
 //           the end is in, warp 10 of both CTAs clears the others' rows first.
 //
-// An accumulator's lanes are columns of the output: a warp stores 32 of them (64 bytes)
-// of two rows at a time.
+// An accumulator's lanes are columns of the output: it is read in 8 x 8 fragments, which
+// stmatrix lays down transposed in a warp's box, and leaves in pieces of 64 bytes of eight
+// rows a store (with two columns of two rows a store, swapped between lanes, a 256 x 256
+// tile took 13000 cycles on its way out, as long as 25 K blocks).
 //
 // Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 9: epilogue; warp 10: WGRAD.
 #include <algorithm>
@@ -41,8 +43,7 @@ constexpr int kTile = 256;                // rows of A per cluster; of B at most
 constexpr uint32_t kHalf = 128 * 128;     // bytes of 128 rows of a K block (128 bytes of K)
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr int kMaxStages = 12;
-constexpr uint32_t kSwap = 1024;          // gated: eight rows of 32 gates or factors
-constexpr uint32_t kSwapBytes = 8 * 2 * kSwap;
+constexpr uint32_t kBox = 2048;           // of a warp on an accumulator's way out
 constexpr size_t kBarBytes = (3 * kMaxStages + 4) * 8 + 16;
 
 struct GroupedMaps {
@@ -67,7 +68,7 @@ struct GroupedParams {
     int stages;
     uint32_t stage_bytes, idesc;
     int act, dtype;
-    int pairs;            // the output's rows start on 4 bytes
+    int vec;              // the output's rows start on 16 (2) or 4 (1) bytes
 };
 
 __device__ __forceinline__ void pair_load2(uint32_t dst, const void *map, uint32_t bar, int c0, int c1) {
@@ -109,7 +110,12 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {   // shared::cluster address
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// The same where no write has to be seen behind it. (A releasing arrival waits for the
+// stores before it: an epilogue that gives its accumulator back after a tile's stores, or a
+// copying warp at every stage, then lags behind by their latency.)
+__device__ __forceinline__ void remote_arrive_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // Operand stored with M / N contiguous, 128-byte swizzle: 64-element groups 8 KB apart
 // (64 K rows of 128 bytes), 8 K rows 1 KB apart.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
@@ -118,33 +124,96 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
            (static_cast<uint64_t>(2) << 61);
 }
 
-// n columns' sums of this thread's accumulator lane, column m of the output, into rows
-// 0 .. n - 1 from dst on (those below `rows`). Two lanes swap a value, so that each
-// stores two columns of every other row.
-template <int N>
-__device__ __forceinline__ void put_columns(uint16_t *dst, int64_t ld, const float (&v)[N], int m, int M, int rows,
-                                            int dtype, bool pairs) {
-    if (pairs) {
-        const bool odd = m & 1;
-        const int me = m & ~1;
-        uint16_t *d = dst + me + (odd ? ld : 0);
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-            const uint32_t lo = elem_round(v[j], dtype), hi = elem_round(v[j + 1], dtype);
-            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
-            const uint32_t w = odd ? other | hi << 16 : lo | other << 16;
-            if (j + (odd ? 1 : 0) < rows) {
-                if (me + 1 < M)
-                    *reinterpret_cast<uint32_t *>(d + j * ld) = w;
-                else if (me < M)
-                    d[j * ld] = static_cast<uint16_t>(w);
-            }
-        }
-    } else if (m < M) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j < rows) dst[j * ld + m] = elem_round(v[j], dtype);
+// 16 accumulator lanes x 32 columns. A thread gets, of every eight columns c, lanes t / 4
+// (0, 1) and t / 4 + 8 (2, 3) at columns 2 (t % 4) and the one behind it: the fragments
+// that stmatrix takes.
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Four 8 x 8 fragments, transposed: thread t's address is row t % 8 of fragment t / 8.
+__device__ __forceinline__ void store_fragments(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
+    if (dtype == KP_FP16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A warp's box in shared memory: rows of 32 elements (64 bytes), whose 16-byte pieces are
+// permuted so that neither fragments nor rows meet in a bank.
+__device__ __forceinline__ uint32_t box_at(uint32_t box, int n, int piece) {
+    return box + n * 64 + ((piece ^ ((n >> 1) & 3)) << 4);
+}
+// Its first `rows` rows to rows of the output from dst on, columns m .. m + 31 below M;
+// vec 2: rows of 16-byte pieces, 1: of 4-byte ones, 0: of single elements.
+template <int N>
+__device__ __forceinline__ void put_box(uint16_t *dst, int64_t ld, uint32_t box, int m, int M, int rows, int lane,
+                                        int vec) {
+    __syncwarp();
+    if (vec == 2) {
+        const int c = m + 8 * (lane & 3);
+        uint16_t *d = dst + (lane >> 2) * ld + c;
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) {
+            const int n = (lane >> 2) + 8 * i;
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(box_at(box, n, lane & 3))
+                         : "memory");
+            if (n < rows) {
+                if (c + 8 <= M) {
+                    *reinterpret_cast<uint4 *>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (c + k < M) d[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+                }
+            }
+            d += 8 * ld;
+        }
+    } else if (vec == 1) {
+        const int c = m + 2 * (lane & 15);
+        uint16_t *d = dst + (lane >> 4) * ld + c;
+#pragma unroll 4
+        for (int n = lane >> 4; n < N; n += 2, d += 2 * ld) {
+            uint32_t w;
+            asm volatile("ld.shared.b32 %0, [%1];"
+                         : "=r"(w)
+                         : "r"(box_at(box, n, (lane & 15) >> 2) + 4 * (lane & 3))
+                         : "memory");
+            if (n >= rows) break;
+            if (c + 2 <= M)
+                *reinterpret_cast<uint32_t *>(d) = w;
+            else if (c < M)
+                *d = static_cast<uint16_t>(w);
+        }
+    } else {
+        uint16_t *d = dst + m + lane;
+#pragma unroll 4
+        for (int n = 0; n < N; ++n, d += ld) {
+            uint16_t w;
+            asm volatile("ld.shared.u16 %0, [%1];"
+                         : "=h"(w)
+                         : "r"(box_at(box, n, lane >> 3) + 2 * (lane & 7))
+                         : "memory");
+            if (n >= rows) break;
+            if (m + lane < M) *d = w;
+        }
+    }
+    __syncwarp();   // the box is free
 }
 
 template <int kForm>
@@ -159,8 +228,8 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = gt_smem_raw + (base - raw);
     const int S = p.stages;
-    const uint32_t swap0 = base + S * p.stage_bytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + S * p.stage_bytes + (kGated ? kSwapBytes : 0));
+    const uint32_t boxes0 = base + S * p.stage_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(gbase + S * p.stage_bytes + 8 * kBox);
     uint64_t *empty = full + kMaxStages;
     uint64_t *ends = empty + kMaxStages;      // WGRAD: copies of a block that an expert's rows end in
     uint64_t *accf = ends + kMaxStages;
@@ -303,7 +372,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
                     if (rank == 0)
                         mbar_expect_tx(smem_u32(full + s), 2 * bytes);
                     else
-                        remote_arrive(bar);
+                        remote_arrive_relaxed(bar);
                     pair_load2(st, &tm.a0, bar, m, r);
                     pair_load2(st + 8192, &tm.a0, bar, m + 64, r);
                     for (int b = 0; b < boxes; ++b) pair_load2(st + kHalf + b * 8192, mb, bar, n + b * 64, r);
@@ -347,9 +416,10 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
             const bool mine = elect_one();
             int stage = 0, as = 0;
             uint32_t phase = 0, aphase = 1;
-            auto prepare = [&](int s, uint32_t ph, const Item &x, int kb) {
+            // (Rows that warp 10 clears are handed to the asynchronous proxy by its own fence;
+            // this thread reads nothing of them.)
+            auto prepare = [&](int s, uint32_t ph) {
                 mbar_wait_bounded(smem_u32(full + s), ph, abort_flag, p.err, DEV_TIMEOUT_FULL);
-                if (kW && kb == x.kb - 1 && (count[x.e] & 15)) acquire_cluster();   // rows cleared by the other CTA
                 tc_fence_after();
             };
             // the next item with a contraction
@@ -363,7 +433,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
             Item it = {}, next;
             int i = 0;
             bool more_items = find(i, it);
-            if (more_items) prepare(0, 0, it, 0);
+            if (more_items) prepare(0, 0);
             while (more_items) {
                 next = it;
                 ++i;
@@ -388,10 +458,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
                     for (int kk = 0; kk < 3; ++kk)
                         if (kk < steps) mma(kk);
                     if (++stage == S) stage = 0, phase ^= 1;
-                    if (kb + 1 < it.kb)
-                        prepare(stage, phase, it, kb + 1);
-                    else if (more_items)
-                        prepare(stage, phase, next, 0);
+                    if (kb + 1 < it.kb || more_items) prepare(stage, phase);
                     if (steps > 3) mma(3);
                     if (mine) pair_commit(bar);
                 }
@@ -408,78 +475,102 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
         const float scale = p.scale ? __ldg(p.scale) : 1.f;   // a power of two
         int as = 0;
         uint32_t aphase = 0;
-        uint32_t parity = 0;
+        const uint32_t box = boxes0 + static_cast<uint32_t>(warp - 2) * kBox;
+        const uint32_t other = boxes0 + static_cast<uint32_t>((warp - 2) ^ 2) * kBox;   // gated: the partner's
         Item it = {};
         for (int i = 0; get(i, it); ++i) {
-            const int m = it.m0 + (kGated ? rank * 64 + (q & 1) * 32 : rank * 128 + q * 32) + lane;
+            const int m = it.m0 + (kGated ? rank * 64 + (q & 1) * 32 : rank * 128 + q * 32);
             uint16_t *dst = p.y0;
             if constexpr (kW)
                 dst = (it.z ? p.y1 : p.y0) + (static_cast<int64_t>(it.e) * p.rows_n + it.n0) * p.ldy;
             else
                 dst += static_cast<int64_t>(first[it.e] + it.n0) * p.ldy;
             if (kW && it.kb == 0) {   // an expert without rows
-                const float zero[32] = {};
-                for (int c = 32 * half; c < it.nt; c += 64)
-                    put_columns(dst + c * p.ldy, p.ldy, zero, m, p.M, it.rows - c, p.dtype, p.pairs);
+                const uint32_t zero[4] = {};
+                for (int c = 0; c < 4; ++c) store_fragments(box_at(box, 8 * c + (lane & 7), lane >> 3), zero);
+                for (int c = 32 * half; c < it.rows; c += 64)
+                    put_box<32>(dst + c * p.ldy, p.ldy, box, m, p.M, it.rows - c, lane, p.vec);
                 continue;
             }
             mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
             tc_fence_after();
             const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16);
             for (int c = 32 * half; c < it.nt; c += 64) {
-                uint32_t v[32];
-                tmem_ld32(t + c, v);
+                uint32_t v[2][16];   // lanes 0 .. 15 and 16 .. 31
+                tmem_ld16x32(t + c, v[0]);
+                tmem_ld16x32(t + c + (16u << 16), v[1]);
                 tmem_ld_wait();
                 if constexpr (kGated) {
                     // Partner q ^ 2 has the factors of these gates: this warp takes the first
-                    // eight of every 16 rows, the other the last.
+                    // 16 of the 32 rows, the other the last.
+                    float a[16], b[16], h[16];   // eight of accumulator lanes 0 .. 15, eight of 16 .. 31
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const uint32_t mine = swap0 + (static_cast<uint32_t>(warp - 2) * 2 + parity) * kSwap + lane * 4;
-                        const uint32_t theirs = swap0 + (static_cast<uint32_t>((warp - 2) ^ 2) * 2 + parity) * kSwap + lane * 4;
-                        float own[8], got[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t lo = v[16 * s + j], hi = v[16 * s + 8 + j];
-                            own[j] = __uint_as_float(q < 2 ? lo : hi);
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + j * 128), "r"(q < 2 ? hi : lo) : "memory");
-                        }
-                        named_bar_sync(1 + 2 * half + (q & 1), 64);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(got[j]) : "r"(theirs + j * 128) : "memory");
-                        parity ^= 1;
-                        float a[8], b[8], h[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            a[j] = q < 2 ? own[j] : got[j];
-                            b[j] = q < 2 ? got[j] : own[j];
-                        }
-                        const int n = c + 16 * s + (q < 2 ? 0 : 8);
-                        const int rows = it.rows - n;
-                        if (rows <= 0) continue;
-                        if (p.g && m < p.M) {
-                            const int64_t at = static_cast<int64_t>(first[it.e] + it.n0 + n) * p.M + m;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (j < rows) {
-                                    p.g[at + static_cast<int64_t>(j) * p.M] = a[j];
-                                    p.u[at + static_cast<int64_t>(j) * p.M] = b[j];
-                                }
-                        }
-                        ffn_gate(a, b, p.act, h);
-                        put_columns(dst + n * p.ldy, p.ldy, h, m, p.M, rows, p.dtype, p.pairs);
+                    for (int i = 0; i < 4; ++i) {
+                        const int g = i >> 1, x = 4 * (i & 1);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + i * 512 + lane * 16),
+                                     "r"(q < 2 ? v[g][8 + x] : v[g][x]), "r"(q < 2 ? v[g][9 + x] : v[g][1 + x]),
+                                     "r"(q < 2 ? v[g][10 + x] : v[g][2 + x]), "r"(q < 2 ? v[g][11 + x] : v[g][3 + x])
+                                     : "memory");
                     }
-                } else {
-                    float a[32];
+                    named_bar_sync(1 + 2 * half + (q & 1), 64);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(v[j]) * scale;
-                    put_columns(dst + c * p.ldy, p.ldy, a, m, p.M, it.rows - c, p.dtype, p.pairs);
+                    for (int i = 0; i < 4; ++i) {
+                        const int g = i >> 1, x = 4 * (i & 1);
+                        float got[4];
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(got[0]), "=f"(got[1]), "=f"(got[2]), "=f"(got[3])
+                                     : "r"(other + i * 512 + lane * 16)
+                                     : "memory");
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float own = __uint_as_float(q < 2 ? v[g][x + k] : v[g][8 + x + k]);
+                            a[8 * g + x + k] = q < 2 ? own : got[k];
+                            b[8 * g + x + k] = q < 2 ? got[k] : own;
+                        }
+                    }
+                    named_bar_sync(1 + 2 * half + (q & 1), 64);   // both have read
+                    const int n = c + (q < 2 ? 0 : 16);
+                    const int rows = it.rows - n;
+                    if (p.g) {
+                        const int64_t at = static_cast<int64_t>(first[it.e] + it.n0 + n) * p.M + m + (lane >> 2);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int r = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1), mo = 16 * g + 8 * ((i >> 1) & 1);
+                                if (r < rows && m + mo + (lane >> 2) < p.M) {
+                                    p.g[at + static_cast<int64_t>(r) * p.M + mo] = a[8 * g + i];
+                                    p.u[at + static_cast<int64_t>(r) * p.M + mo] = b[8 * g + i];
+                                }
+                            }
+                    }
+                    ffn_gate(a, b, p.act, h);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            r[k] = pack2(h[8 * (k >> 1) + 4 * i + 2 * (k & 1)], h[8 * (k >> 1) + 4 * i + 2 * (k & 1) + 1],
+                                         p.dtype);
+                        store_fragments(box_at(box, 8 * i + (lane & 7), lane >> 3), r);
+                    }
+                    put_box<16>(dst + n * p.ldy, p.ldy, box, m, p.M, rows, lane, p.vec);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            r[k] = pack2(__uint_as_float(v[k >> 1][4 * i + 2 * (k & 1)]) * scale,
+                                         __uint_as_float(v[k >> 1][4 * i + 2 * (k & 1) + 1]) * scale, p.dtype);
+                        store_fragments(box_at(box, 8 * i + (lane & 7), lane >> 3), r);
+                    }
+                    put_box<32>(dst + c * p.ldy, p.ldy, box, m, p.M, it.rows - c, lane, p.vec);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) remote_arrive(mapa_shared(smem_u32(acce + as), 0));
+            if (lane == 0) remote_arrive_relaxed(mapa_shared(smem_u32(acce + as), 0));
             if (++as == 2) as = 0, aphase ^= 1;
         }
         __syncwarp();
@@ -487,23 +578,22 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
         // Rows of others behind an expert's last one, within the MMA step that it is in.
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);
         uint32_t seen = 0;   // phases of `ends`, a bit a stage
-        int64_t at = 0;      // K blocks before this item
+        int end = 0;         // the stage behind the last one of the item before
         Item it = {};
         for (int i = 0; get(i, it); ++i) {
             const int left = count[it.e] & 15;
-            at += it.kb;
+            end = (end + it.kb) % S;
             if (!it.kb || !left) continue;
-            const int s = static_cast<int>((at - 1) % S);
+            const int s = end ? end - 1 : S - 1;
             mbar_wait_bounded(smem_u32(ends + s), (seen >> s) & 1, abort_flag, p.err, DEV_TIMEOUT_FULL);
             seen ^= 1u << s;
             const int r0 = count[it.e] & 63, n = 16 - left;      // K rows r0 .. r0 + n - 1 of every 8 KB group
             const int groups = 2 + (it.nt >> 7);
-            for (int x = lane; x < groups * n * 8; x += 32) {
-                const int gr = x / (n * 8), y = x - gr * n * 8;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 base + s * p.stage_bytes + gr * 8192 + r0 * 128 + y * 16),
-                             "r"(0)
-                             : "memory");
+            for (int gr = 0; gr < groups; ++gr) {
+                const uint32_t to = base + s * p.stage_bytes + gr * 8192 + r0 * 128;
+#pragma unroll
+                for (int x = lane; x < 15 * 8; x += 32)
+                    if (x < n * 8) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + x * 16), "r"(0) : "memory");
             }
             // the tensor cores read them through the asynchronous proxy
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -564,7 +654,8 @@ cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s
     p.KB = cdiv(p.K, 64);
     p.act = a.act;
     p.dtype = a.dtype;
-    p.pairs = ((reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1) | static_cast<uintptr_t>(a.ldy * 2)) & 3) == 0;
+    const uintptr_t starts = reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1) | static_cast<uintptr_t>(a.ldy * 2);
+    p.vec = starts % 16 == 0 ? 2 : starts % 4 == 0 ? 1 : 0;
     p.idesc = idesc_f16(a.dtype, 256, 0, dgrad || wgrad, wgrad);
     int64_t items;
     int half;   // rows of B that a CTA holds at most
@@ -583,7 +674,7 @@ cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s
     }
     if (items > (1 << 30)) return cudaErrorInvalidValue;
     p.stage_bytes = kHalf + static_cast<uint32_t>(half) * 128;
-    const size_t fixed = 1024 + (gated ? kSwapBytes : 0) + kBarBytes + (3 * static_cast<size_t>(a.E) + 1) * sizeof(int32_t);
+    const size_t fixed = 1024 + 8 * kBox + kBarBytes + (3 * static_cast<size_t>(a.E) + 1) * sizeof(int32_t);
     p.stages = std::min<int>(kMaxStages, static_cast<int>((kMaxSmem - fixed) / p.stage_bytes));
 
     GroupedMaps tm = {};
