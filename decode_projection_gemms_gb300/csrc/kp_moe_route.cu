@@ -9,6 +9,7 @@
 // its expert's first row, plus those of the blocks before, plus the pairs before it
 // within the block. Counts are whole numbers, so nothing depends on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "kp_moe.cuh"
 
@@ -17,8 +18,9 @@ namespace kp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kTokens = 32;   // of a block
+constexpr int kChoosers = 512;   // threads of a block that chooses
+constexpr int kTokens = 32;      // of a block
+constexpr int kAllThreads = 1024, kAllTokens = 64;   // of the one block that does everything
 
 struct RouteParams {
     MoeRouteArgs a;
@@ -57,70 +59,83 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // The k largest of the warp's keys (lane holds experts lane + 32 i), ties to the lowest
 // expert: lane j gets the j-th one's expert (-1: there is none) and, with kGap, whether
 // two of the k + 1 largest are nearer than fp32 sums of a score and a bias are exact.
+// A lane has its two best ready, and looks for more when both are taken; what is taken
+// lies above the last choice, so nothing is marked.
 template <int NV, typename Key, bool kGap>
-__device__ __forceinline__ int choose(Key (&key)[NV], int k, int lane, bool &close) {
+__device__ __forceinline__ int choose(const Key (&key)[NV], int k, int lane, bool &close) {
     int mine = -1;
     float last = 0.f;
     close = false;
-    for (int j = 0; j < k + (kGap ? 1 : 0); ++j) {
-        Key best = 0;
-        int at = 0;
+    Key best = 0, next = 0;   // of this lane, 0: none; and their experts
+    int at = lane, at_next = lane;
+    auto put = [&](Key x, int e) {   // e ascending
+        if (x > best)
+            next = best, at_next = at, best = x, at = e;
+        else if (x > next)
+            next = x, at_next = e;
+    };
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (key[i] > best) best = key[i], at = i;
+    for (int i = 0; i < NV; ++i) put(key[i], lane + 32 * i);
+    for (int j = 0; j < k + (kGap ? 1 : 0); ++j) {
         const Key top = warp_max(best);
         if (top == 0) break;
-        const int e = static_cast<int>(__reduce_min_sync(
-            0xFFFFFFFFu, best == top ? static_cast<uint32_t>(lane + 32 * at) : 0xFFFFFFFFu));
+        const int e = static_cast<int>(
+            __reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
         if constexpr (kGap) {
             const float v = value_of(top);
             close = close || (j && last - v <= 2e-6f * fmaxf(1.f, fabsf(v)));
             last = v;
         }
         if (j < k && lane == j) mine = e;
+        if (at == e && best == top) {
+            best = next, at = at_next, next = 0;
+            if (NV > 2 && best == 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (lane + 32 * i == e) key[i] = 0;
+                for (int i = 0; i < NV; ++i) {
+                    const int x = lane + 32 * i;
+                    if (key[i] < top || (key[i] == top && x > e)) put(key[i], x);
+                }
+            }
+        }
     }
     return mine;
 }
 
-// Experts and weights of a token; lane j < k gets the j-th.
+// The choice by sigmoid plus bias in 64 bits, for the few tokens that fp32 leaves open.
 template <int NV>
+__device__ __noinline__ int choose_exactly(const void *logits, int64_t row, const float *bias, int E, int k, int dtype,
+                                            int lane) {
+    uint64_t key[NV];
+    bool close;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        const float v = e < E ? logit_of(logits, row + e, dtype) : -INFINITY;
+        key[i] = v > -INFINITY ? order_key(1.0 / (1.0 + exp(-static_cast<double>(v))) + static_cast<double>(__ldg(bias + e)))
+                               : 0;
+    }
+    return choose<NV, uint64_t, false>(key, k, lane, close);
+}
+
+// Experts and weights of a token; lane j < k gets the j-th.
+template <int NV, bool kBias>
 __device__ __forceinline__ void route_token(const MoeRouteArgs &a, int64_t t, int lane, int &id, float &w) {
     const int64_t row = t * a.ld;
-    float v[NV];
     uint32_t key[NV];
     bool close;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = lane + 32 * i;
-        v[i] = e < a.E ? logit_of(a.logits, row + e, a.dtype) : -INFINITY;
-        key[i] = order_key(v[i]);
+        const float v = e < a.E ? logit_of(a.logits, row + e, a.dtype) : -INFINITY;
+        key[i] = order_key(v);
+        // By sigmoid plus bias: fp32 keys decide, off by less than 1e-6 (the exponential's
+        // argument is rounded by at most 2^-24 |v|, a quarter of which reaches the score);
+        // but where two of them lie so near each other that fp32 does not, the token is
+        // chosen again in 64 bits (0.3 % of 16384 tokens with 256 experts).
+        if (kBias && key[i]) key[i] = order_key(__fdividef(1.f, 1.f + __expf(-v)) + __ldg(a.bias + e));
     }
-    if (!a.bias) {
-        id = choose<NV, uint32_t, false>(key, a.k, lane, close);
-    } else {
-        // Chosen by sigmoid plus bias. fp32 keys decide, but where two of them lie so
-        // near each other that fp32 does not, the token is chosen again in 64 bits.
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = lane + 32 * i;
-            if (key[i]) key[i] = order_key(1.f / (1.f + expf(-v[i])) + __ldg(a.bias + e));
-        }
-        id = choose<NV, uint32_t, true>(key, a.k, lane, close);
-        if (close) {
-            uint64_t wide[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int e = lane + 32 * i;
-                wide[i] = v[i] > -INFINITY
-                              ? order_key(1.0 / (1.0 + exp(-static_cast<double>(v[i]))) + static_cast<double>(__ldg(a.bias + e)))
-                              : 0;
-            }
-            id = choose<NV, uint64_t, false>(wide, a.k, lane, close);
-        }
-    }
+    id = choose<NV, uint32_t, kBias>(key, a.k, lane, close);
+    if (kBias && close) id = choose_exactly<NV>(a.logits, row, a.bias, a.E, a.k, a.dtype, lane);
     const float l = id >= 0 ? logit_of(a.logits, row + id, a.dtype) : -INFINITY;
     // the largest chosen logit
     const uint32_t most = warp_max(order_key(l));
@@ -145,11 +160,12 @@ __device__ __forceinline__ void route_token(const MoeRouteArgs &a, int64_t t, in
     w = s / sum;
 }
 
-// Exclusive sums of n <= kMoeMaxExperts whole numbers in shared memory, by the block;
-// returns the sum of all.
+// Exclusive sums of n <= kMoeMaxExperts whole numbers in shared memory, by a block of kT
+// threads; returns the sum of all.
+template <int kT>
 __device__ int block_scan(int32_t *v, int n, int32_t *sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (n + kThreads - 1) / kThreads, at = threadIdx.x * per;
+    const int per = (n + kT - 1) / kT, at = threadIdx.x * per;
     int mine = 0;
     for (int i = 0; i < per; ++i)
         if (at + i < n) mine += v[at + i];
@@ -162,7 +178,7 @@ __device__ int block_scan(int32_t *v, int n, int32_t *sums) {
     if (lane == 31) sums[warp] = run;
     __syncthreads();
     int before = 0, all = 0;
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < kT / 32; ++i) {
         if (i < warp) before += sums[i];
         all += sums[i];
     }
@@ -178,11 +194,13 @@ __device__ int block_scan(int32_t *v, int n, int32_t *sums) {
 }
 
 // Rows of a block's choices: base[e] holds the first row of expert e for this block.
-// Slots are taken kThreads at a time in order; cnt [kWarps][E].
+// Slots are taken kT at a time in order; cnt [kT / 32][E].
+template <int kT>
 __device__ void place(const RouteParams &p, int64_t first, int n, int32_t *base, int32_t *cnt) {
     const int E = p.a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int s0 = 0; s0 < n; s0 += kThreads) {
-        for (int i = threadIdx.x; i < kWarps * E; i += kThreads) cnt[i] = 0;
+    for (int s0 = 0; s0 < n; s0 += kT) {
+        const int warps = min((n - s0 + 31) >> 5, kT / 32);
+        for (int i = threadIdx.x; i < warps * E; i += kT) cnt[i] = 0;
         __syncthreads();
         const int i = s0 + threadIdx.x;
         const int e = i < n ? p.a.ids[first + i] : -1;
@@ -190,9 +208,9 @@ __device__ void place(const RouteParams &p, int64_t first, int n, int32_t *base,
         const int before = __popc(same & ((1u << lane) - 1));
         if (e >= 0 && before == 0) cnt[warp * E + e] = __popc(same);
         __syncthreads();
-        for (int x = threadIdx.x; x < E; x += kThreads) {
+        for (int x = threadIdx.x; x < E; x += kT) {
             int run = base[x];
-            for (int q = 0; q < kWarps; ++q) {
+            for (int q = 0; q < warps; ++q) {
                 const int c = cnt[q * E + x];
                 cnt[q * E + x] = run;
                 run += c;
@@ -215,19 +233,21 @@ __device__ void place(const RouteParams &p, int64_t first, int n, int32_t *base,
 extern __shared__ int32_t route_smem[];
 
 // kAll: one block, which does everything.
-template <int NV, bool kAll>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams p) {
+template <int NV, bool kBias, bool kAll>
+__global__ void __launch_bounds__(kAll ? kAllThreads : kChoosers, kAll || NV > 8 ? 1 : 3)
+    route_kernel(const RouteParams p) {
+    constexpr int kT = kAll ? kAllThreads : kChoosers;
     const MoeRouteArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t *hist = route_smem;
-    for (int i = threadIdx.x; i < a.E; i += kThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < a.E; i += kT) hist[i] = 0;
     __syncthreads();
     const int t0 = kAll ? 0 : static_cast<int>(blockIdx.x) * kTokens;
     const int t1 = kAll ? a.T : min(t0 + kTokens, a.T);
-    for (int t = t0 + warp; t < t1; t += kWarps) {
+    for (int t = t0 + warp; t < t1; t += kT / 32) {
         int id;
         float w;
-        route_token<NV>(a, t, lane, id, w);
+        route_token<NV, kBias>(a, t, lane, id, w);
         if (lane < a.k) {
             a.ids[static_cast<int64_t>(t) * a.k + lane] = id;
             a.weights[static_cast<int64_t>(t) * a.k + lane] = w;
@@ -236,14 +256,15 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteParams p) {
     }
     __syncthreads();
     if constexpr (!kAll) {
-        for (int i = threadIdx.x; i < a.E; i += kThreads) p.counts[static_cast<int64_t>(blockIdx.x) * a.E + i] = hist[i];
+        for (int i = threadIdx.x; i < a.E; i += kT) p.counts[static_cast<int64_t>(blockIdx.x) * a.E + i] = hist[i];
     } else {
-        int32_t *sums = hist + a.E, *cnt = sums + kWarps;
-        const int rows = block_scan(hist, a.E, sums);
-        for (int i = threadIdx.x; i < a.E; i += kThreads) a.offsets[i] = hist[i];
+        int32_t *sums = hist + a.E, *cnt = sums + kT / 32;
+        const int rows = block_scan<kT>(hist, a.E, sums);
+        for (int i = threadIdx.x; i < a.E; i += kT) a.offsets[i] = hist[i];
         if (threadIdx.x == 0) a.offsets[a.E] = rows;
-        for (int i = rows + threadIdx.x; i < a.T * a.k; i += kThreads) a.order[i] = -1;
-        place(p, 0, a.T * a.k, hist, cnt);
+        for (int i = rows + threadIdx.x; i < a.T * a.k; i += kT) a.order[i] = -1;
+        __syncthreads();   // offsets are written from hist, which the placing moves on
+        place<kT>(p, 0, a.T * a.k, hist, cnt);
     }
 }
 
@@ -273,10 +294,10 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const RouteParams p) {
 
 __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams p) {
     const MoeRouteArgs &a = p.a;
-    int32_t *base = route_smem, *sums = base + a.E, *cnt = sums + kWarps;
+    int32_t *base = route_smem, *sums = base + a.E, *cnt = sums + kThreads / 32;
     for (int i = threadIdx.x; i < a.E; i += kThreads) base[i] = p.totals[i];
     __syncthreads();
-    const int rows = block_scan(base, a.E, sums);
+    const int rows = block_scan<kThreads>(base, a.E, sums);
     if (blockIdx.x == 0) {
         for (int i = threadIdx.x; i < a.E; i += kThreads) a.offsets[i] = base[i];
         if (threadIdx.x == 0) a.offsets[a.E] = rows;
@@ -289,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams
     for (int i = threadIdx.x; i < a.E; i += kThreads) base[i] += p.counts[static_cast<int64_t>(blockIdx.x) * a.E + i];
     __syncthreads();
     const int t0 = static_cast<int>(blockIdx.x) * kTokens;
-    place(p, static_cast<int64_t>(t0) * a.k, min(kTokens, a.T - t0) * a.k, base, cnt);
+    place<kThreads>(p, static_cast<int64_t>(t0) * a.k, min(kTokens, a.T - t0) * a.k, base, cnt);
 }
 
 // dlogits: a warp a token. With w the weights and d = dw - sum_j w_j dw_j a chosen
@@ -299,6 +320,7 @@ __global__ void __launch_bounds__(kThreads)
                           const int32_t *__restrict__ ids, const float *__restrict__ weights, void *__restrict__ dlogits,
                           int64_t ldd, int T, int E, int k, int score, int dtype) {
     const int lane = threadIdx.x & 31;
+    const int es = dtype == KP_FP32 ? 4 : 2;
     for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5; t < T;
          t += (static_cast<int64_t>(gridDim.x) * kThreads) >> 5) {
         int id = -1;
@@ -314,25 +336,28 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
         float d = w * (dw - sum);
         if (score == KP_SCORE_SIGMOID && id >= 0) d *= 1.f / (1.f + expf(logit_of(logits, t * ld + id, dtype)));   // 1 - s
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            float v = 0.f;
-            for (int j = 0; j < k; ++j) {
-                const int ej = __shfl_sync(0xFFFFFFFFu, id, j);
-                const float dj = __shfl_sync(0xFFFFFFFFu, d, j);
-                if (ej == e) v = dj;
-            }
-            if (e < E) {
-                if (dtype == KP_FP32)
-                    static_cast<float *>(dlogits)[t * ldd + e] = v;
-                else
-                    static_cast<uint16_t *>(dlogits)[t * ldd + e] = elem_round(v, dtype);
-            }
+        // zeros in the row, then the chosen experts' over them
+        const int64_t at = t * ldd;
+        char *out = static_cast<char *>(dlogits) + at * es;
+        const int bytes = E * es;
+        int head = static_cast<int>(-reinterpret_cast<intptr_t>(out) & 15);
+        head = min(head, bytes);
+        const int body = (bytes - head) >> 4;
+        for (int i = lane; i < body; i += 32) reinterpret_cast<uint4 *>(out + head)[i] = make_uint4(0, 0, 0, 0);
+        const int edge = bytes - 16 * body;   // bytes before and behind
+        for (int i = lane * 2; i < edge; i += 64)
+            *reinterpret_cast<uint16_t *>(out + (i < head ? i : 16 * body + i)) = 0;
+        __syncwarp();
+        if (id >= 0) {
+            if (dtype == KP_FP32)
+                static_cast<float *>(dlogits)[at + id] = d;
+            else
+                static_cast<uint16_t *>(dlogits)[at + id] = elem_round(d, dtype);
         }
     }
 }
 
-int blocks_of(int T) { return (T + kTokens - 1) / kTokens; }
+int blocks_of(int T) { return T <= kAllTokens ? 1 : (T + kTokens - 1) / kTokens; }
 
 }  // namespace
 
@@ -343,33 +368,48 @@ size_t moe_route_scratch(int T, int E) {
 
 cudaError_t moe_route_launch(const MoeRouteArgs &a, const FfnDev &, cudaStream_t s) {
     using Fn = void (*)(RouteParams);
-    static const Fn kernels[2][6] = {
-        {route_kernel<1, false>, route_kernel<2, false>, route_kernel<4, false>, route_kernel<8, false>,
-         route_kernel<16, false>, route_kernel<32, false>},
-        {route_kernel<1, true>, route_kernel<2, true>, route_kernel<4, true>, route_kernel<8, true>,
-         route_kernel<16, true>, route_kernel<32, true>}};
+    auto pick = [&](auto all) -> Fn {
+        constexpr bool kAll = decltype(all)::value;
+        static const Fn kernels[2][6] = {
+            {route_kernel<1, false, kAll>, route_kernel<2, false, kAll>, route_kernel<4, false, kAll>,
+             route_kernel<8, false, kAll>, route_kernel<16, false, kAll>, route_kernel<32, false, kAll>},
+            {route_kernel<1, true, kAll>, route_kernel<2, true, kAll>, route_kernel<4, true, kAll>,
+             route_kernel<8, true, kAll>, route_kernel<16, true, kAll>, route_kernel<32, true, kAll>}};
+        int v = 0;
+        while (32 << v < a.E) ++v;
+        return kernels[a.bias != nullptr][v];
+    };
     RouteParams p;
     p.a = a;
     p.blocks = blocks_of(a.T);
     p.counts = static_cast<int32_t *>(a.work);
     p.totals = p.blocks > 1 ? p.counts + static_cast<int64_t>(p.blocks) * a.E : nullptr;
-    int v = 0;
-    while (32 << v < a.E) ++v;
-    const size_t place = (static_cast<size_t>(a.E) * (1 + kWarps) + kWarps) * sizeof(int32_t);
+    // base, the scan's sums, and each warp's counts by expert
+    auto place = [&](int threads, int64_t slots) {
+        const int warps = static_cast<int>(std::min<int64_t>((slots + 31) / 32, threads / 32));
+        return (static_cast<size_t>(a.E) * (1 + warps) + threads / 32) * sizeof(int32_t);
+    };
     if (p.blocks == 1) {
-        kernels[1][v]<<<1, kThreads, place, s>>>(p);
+        const size_t smem = place(kAllThreads, static_cast<int64_t>(a.T) * a.k);
+        Fn f = pick(std::true_type());
+        if (smem > 48 * 1024) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            if (e != cudaSuccess) return e;
+        }
+        f<<<1, kAllThreads, smem, s>>>(p);
         return cudaGetLastError();
     }
-    kernels[0][v]<<<p.blocks, kThreads, a.E * sizeof(int32_t), s>>>(p);
+    pick(std::false_type())<<<p.blocks, kChoosers, a.E * sizeof(int32_t), s>>>(p);
     route_scan_kernel<<<(a.E + 31) / 32, 1024, 0, s>>>(p);
-    route_place_kernel<<<p.blocks, kThreads, place, s>>>(p);
+    route_place_kernel<<<p.blocks, kThreads, place(kThreads, kTokens * a.k), s>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t moe_route_backward_launch(const float *dweights, const void *logits, int64_t ld, const int32_t *ids,
                                       const float *weights, void *dlogits, int64_t ldd, int T, int E, int k,
                                       int score, int dtype, const FfnDev &d, cudaStream_t s) {
-    const int64_t blocks = (static_cast<int64_t>(T) + kWarps - 1) / kWarps;
+    const int64_t blocks = (static_cast<int64_t>(T) + kThreads / 32 - 1) / (kThreads / 32);
     route_backward_kernel<<<static_cast<int>(std::min<int64_t>(blocks, static_cast<int64_t>(d.sms) * 8)), kThreads, 0, s>>>(
         dweights, logits, ld, ids, weights, dlogits, ldd, T, E, k, score, dtype);
     return cudaGetLastError();
