@@ -17,9 +17,10 @@ namespace kp {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kChoosers = 512;   // threads of a block that chooses
-constexpr int kTokens = 32;      // of a block
+constexpr int kThreads = 256;    // of the gradient's blocks
+constexpr int kTokens = 16;      // of a block
+constexpr int kChoosers = 32 * kTokens, kPlacers = 128;   // threads of a block that chooses, that places
+constexpr int kScanExperts = 8;  // of a block that sums counts
 constexpr int kAllThreads = 1024, kAllTokens = 64;   // of the one block that does everything
 
 struct RouteParams {
@@ -123,16 +124,33 @@ __device__ __forceinline__ void route_token(const MoeRouteArgs &a, int64_t t, in
     const int64_t row = t * a.ld;
     uint32_t key[NV];
     bool close;
+    float x[NV];
+    if (a.dtype == KP_FP32) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            x[i] = lane + 32 * i < a.E ? __ldg(static_cast<const float *>(a.logits) + row + lane + 32 * i) : -INFINITY;
+    } else {
+        uint16_t h[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            h[i] = lane + 32 * i < a.E ? __ldg(static_cast<const uint16_t *>(a.logits) + row + lane + 32 * i) : 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = lane + 32 * i < a.E ? elem_widen(h[i], a.dtype) : -INFINITY;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = lane + 32 * i;
-        const float v = e < a.E ? logit_of(a.logits, row + e, a.dtype) : -INFINITY;
-        key[i] = order_key(v);
+        const float v = x[i];
+        key[i] = order_key(fminf(v, 3.402823466e38f));
+        if (v != v) key[i] = 0;
         // By sigmoid plus bias: fp32 keys decide, off by less than 1e-6 (the exponential's
         // argument is rounded by at most 2^-24 |v|, a quarter of which reaches the score);
         // but where two of them lie so near each other that fp32 does not, the token is
-        // chosen again in 64 bits (0.3 % of 16384 tokens with 256 experts).
-        if (kBias && key[i]) key[i] = order_key(__fdividef(1.f, 1.f + __expf(-v)) + __ldg(a.bias + e));
+        // chosen again in 64 bits (one in 2000 of 16384 tokens with 256 experts).
+        if (kBias && e < a.E) {
+            const uint32_t biased = order_key(__fdividef(1.f, 1.f + __expf(-v)) + __ldg(a.bias + e));
+            key[i] = key[i] ? biased : 0;
+        }
     }
     id = choose<NV, uint32_t, kBias>(key, a.k, lane, close);
     if (kBias && close) id = choose_exactly<NV>(a.logits, row, a.bias, a.E, a.k, a.dtype, lane);
@@ -268,49 +286,72 @@ __global__ void __launch_bounds__(kAll ? kAllThreads : kChoosers, kAll || NV > 8
     }
 }
 
-// counts[b][e] -> sum of counts[0 .. b)[e]; a lane an expert, a warp a run of blocks.
+// counts[b][e] -> sum of counts[0 .. b)[e]: a block for eight experts, a warp's lanes
+// eight experts by four runs of blocks.
 __global__ void __launch_bounds__(1024) route_scan_kernel(const RouteParams p) {
-    __shared__ int32_t part[32][33];
-    const int E = p.a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int e = blockIdx.x * 32 + lane;
-    const int per = (p.blocks + 31) / 32, b0 = warp * per, b1 = min(b0 + per, p.blocks);
+    constexpr int kRuns = 1024 / kScanExperts;
+    __shared__ int32_t part[kRuns][kScanExperts];
+    const int E = p.a.E, x = threadIdx.x % kScanExperts, y = threadIdx.x / kScanExperts;
+    const int e = blockIdx.x * kScanExperts + x;
+    const int per = (p.blocks + kRuns - 1) / kRuns, b0 = y * per, b1 = min(b0 + per, p.blocks);
+    int32_t *const at = p.counts + e;
     int sum = 0;
-    if (e < E)
-        for (int b = b0; b < b1; ++b) sum += p.counts[static_cast<int64_t>(b) * E + e];
-    part[warp][lane] = sum;
-    __syncthreads();
-    int run = 0;
-    for (int i = 0; i < warp; ++i) run += part[i][lane];
     if (e < E) {
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b) sum += at[static_cast<int64_t>(b) * E];
+    }
+    part[y][x] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32 * kScanExperts) {   // a warp an expert: sums of the runs before each
+        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        int v[kRuns / 32], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kRuns / 32; ++i) v[i] = part[lane * (kRuns / 32) + i][w], mine += v[i];
+        int run = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, run, d);
+            if (lane >= d) run += o;
+        }
+        if (lane == 31 && blockIdx.x * kScanExperts + w < E) p.totals[blockIdx.x * kScanExperts + w] = run;
+        run -= mine;
+#pragma unroll
+        for (int i = 0; i < kRuns / 32; ++i) {
+            part[lane * (kRuns / 32) + i][w] = run;
+            run += v[i];
+        }
+    }
+    __syncthreads();
+    if (e < E) {
+        int run = part[y][x];
+#pragma unroll 8
         for (int b = b0; b < b1; ++b) {
-            const int64_t i = static_cast<int64_t>(b) * E + e;
-            const int c = p.counts[i];
-            p.counts[i] = run;
+            const int c = at[static_cast<int64_t>(b) * E];
+            at[static_cast<int64_t>(b) * E] = run;
             run += c;
         }
-        if (warp == 31) p.totals[e] = run;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(kPlacers) route_place_kernel(const RouteParams p) {
     const MoeRouteArgs &a = p.a;
-    int32_t *base = route_smem, *sums = base + a.E, *cnt = sums + kThreads / 32;
-    for (int i = threadIdx.x; i < a.E; i += kThreads) base[i] = p.totals[i];
+    int32_t *base = route_smem, *sums = base + a.E, *cnt = sums + kPlacers / 32;
+    for (int i = threadIdx.x; i < a.E; i += kPlacers) base[i] = p.totals[i];
     __syncthreads();
-    const int rows = block_scan<kThreads>(base, a.E, sums);
+    const int rows = block_scan<kPlacers>(base, a.E, sums);
     if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < a.E; i += kThreads) a.offsets[i] = base[i];
+        for (int i = threadIdx.x; i < a.E; i += kPlacers) a.offsets[i] = base[i];
         if (threadIdx.x == 0) a.offsets[a.E] = rows;
     }
     const int64_t slots = static_cast<int64_t>(a.T) * a.k;
-    for (int64_t i = rows + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < slots;
-         i += static_cast<int64_t>(gridDim.x) * kThreads)
+    for (int64_t i = rows + static_cast<int64_t>(blockIdx.x) * kPlacers + threadIdx.x; i < slots;
+         i += static_cast<int64_t>(gridDim.x) * kPlacers)
         a.order[i] = -1;
     __syncthreads();   // offsets are written from base, which the placing moves on
-    for (int i = threadIdx.x; i < a.E; i += kThreads) base[i] += p.counts[static_cast<int64_t>(blockIdx.x) * a.E + i];
+    for (int i = threadIdx.x; i < a.E; i += kPlacers) base[i] += p.counts[static_cast<int64_t>(blockIdx.x) * a.E + i];
     __syncthreads();
     const int t0 = static_cast<int>(blockIdx.x) * kTokens;
-    place<kThreads>(p, static_cast<int64_t>(t0) * a.k, min(kTokens, a.T - t0) * a.k, base, cnt);
+    place<kPlacers>(p, static_cast<int64_t>(t0) * a.k, min(kTokens, a.T - t0) * a.k, base, cnt);
 }
 
 // dlogits: a warp a token. With w the weights and d = dw - sum_j w_j dw_j a chosen
@@ -401,8 +442,8 @@ cudaError_t moe_route_launch(const MoeRouteArgs &a, const FfnDev &, cudaStream_t
         return cudaGetLastError();
     }
     pick(std::false_type())<<<p.blocks, kChoosers, a.E * sizeof(int32_t), s>>>(p);
-    route_scan_kernel<<<(a.E + 31) / 32, 1024, 0, s>>>(p);
-    route_place_kernel<<<p.blocks, kThreads, place(kThreads, kTokens * a.k), s>>>(p);
+    route_scan_kernel<<<(a.E + kScanExperts - 1) / kScanExperts, 1024, 0, s>>>(p);
+    route_place_kernel<<<p.blocks, kPlacers, place(kPlacers, kTokens * a.k), s>>>(p);
     return cudaGetLastError();
 }
 
