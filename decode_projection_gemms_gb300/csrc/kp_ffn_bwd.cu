@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads)
                      const float *__restrict__ u, uint16_t *__restrict__ dg, uint16_t *__restrict__ du,
                      int64_t ld, const uint32_t *__restrict__ top, int tops, float *__restrict__ back, int T, int F,
                      int dtype, int vec, const int32_t *__restrict__ rows) {
+    pdl_trigger();   // a product launched programmatically behind this waits for it all the same
     float scale = 1.f;
     if (tops) {
         __shared__ uint32_t sh[kThreads / 32];

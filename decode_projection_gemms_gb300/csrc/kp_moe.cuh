@@ -48,25 +48,26 @@ struct MoeMat {
     int64_t ld = 0, se = 0;
 };
 enum GroupedForm {
-    GROUPED_PLAIN,   // y[r] = x[r] W_e^T
-    GROUPED_GATED,   // h[r] = act(x[r] Wg_e^T) * (x[r] Wu_e^T); g, u
-    GROUPED_DGRAD,   // dx[r] = d0[r] W0_e (+ d1[r] W1_e)
-    GROUPED_WGRAD    // dW0_e = d0^T x over the expert's rows (and dW1_e = d1^T x)
+    GROUPED_PLAIN,     // y[r] = x[r] W_e^T
+    GROUPED_GATED,     // h[r] = act(x[r] Wg_e^T) * (x[r] Wu_e^T); g, u
+    GROUPED_BACKWARD   // dx[r] = d0[r] W0_e (+ d1[r] W1_e); dW0_e = d0^T x over the expert's rows (and dW1_e = d1^T x)
 };
 struct GroupedArgs {
     int form = GROUPED_PLAIN;
     int act = 0, dtype = KP_BF16;
     const int32_t *offsets = nullptr;
     int R = 0, E = 0, N = 0, K = 0;      // rows, experts, features, columns of x
-    const void *x = nullptr;             // [R, K] (not of DGRAD)
+    const void *x = nullptr;             // [R, K]
     int64_t ldx = 0;
-    MoeMat w0, w1;                       // [E][N][K] (not of WGRAD)
-    const void *d0 = nullptr, *d1 = nullptr;   // [R, N], of DGRAD and WGRAD; d1 may be NULL
+    MoeMat w0, w1;                       // [E][N][K]
+    const void *d0 = nullptr, *d1 = nullptr;   // backward: [R, N]; d1 may be NULL
     int64_t ldd = 0;
-    void *y0 = nullptr, *y1 = nullptr;   // y, h, dx; dW0, dW1
+    void *y = nullptr;                   // y, h, dx
     int64_t ldy = 0;
-    float *g = nullptr, *u = nullptr;    // [R, N]
-    const float *scale = nullptr;        // device factor of every sum (NULL: 1)
+    void *dw0 = nullptr, *dw1 = nullptr; // backward: [E][N][K], contiguous
+    float *g = nullptr, *u = nullptr;    // gated: [R, N]
+    const float *scale = nullptr;        // backward: device factor of every sum (NULL: 1)
+    bool pdl = false;                    // launched behind a kernel that writes only d0, d1 and scale
     int *err = nullptr;
 };
 cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s);

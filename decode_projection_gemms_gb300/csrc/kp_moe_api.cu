@@ -251,7 +251,7 @@ int kp_grouped_gemm(const void *x, int64_t ldx, const void *W, int64_t ldw, int6
     a.x = x;
     a.ldx = ldx;
     a.w0 = {W, ldw, sw};
-    a.y0 = y;
+    a.y = y;
     a.ldy = ldy;
     a.err = d.err;
     const cudaError_t e = grouped_launch(a, d, stream);
@@ -277,7 +277,7 @@ int kp_grouped_gemm_backward(const void *dy, int64_t lddy, const void *x, int64_
         (rc = check_ints(fn, "offsets", offsets)) || (rc = ffn_device(&d)))
         return rc;
     GroupedArgs a;
-    a.form = GROUPED_DGRAD;
+    a.form = GROUPED_BACKWARD;
     a.dtype = dtype;
     a.offsets = offsets;
     a.R = R;
@@ -289,15 +289,11 @@ int kp_grouped_gemm_backward(const void *dy, int64_t lddy, const void *x, int64_
     a.w0 = {W, ldw, sw};
     a.d0 = dy;
     a.ldd = lddy;
-    a.y0 = dx;
+    a.y = dx;
     a.ldy = lddx;
+    a.dw0 = dW;
     a.err = d.err;
-    cudaError_t e = grouped_launch(a, d, stream);
-    if (e != cudaSuccess) return cuda_failed(e, fn);
-    a.form = GROUPED_WGRAD;
-    a.y0 = dW;
-    a.ldy = K;
-    e = grouped_launch(a, d, stream);
+    const cudaError_t e = grouped_launch(a, d, stream);
     return e == cudaSuccess ? KP_OK : cuda_failed(e, fn);
 }
 
@@ -331,7 +327,7 @@ int kp_grouped_gated_ffn(const void *x, int64_t ldx, const void *Wg, int64_t ldg
     a.ldx = ldx;
     a.w0 = {Wg, ldg, sg};
     a.w1 = {Wu, ldu, su};
-    a.y0 = h;
+    a.y = h;
     a.ldy = ldh;
     a.g = g;
     a.u = u;
@@ -375,7 +371,7 @@ int kp_grouped_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, i
                              offsets + E);
     if (e != cudaSuccess) return cuda_failed(e, fn);
     GroupedArgs a;
-    a.form = GROUPED_DGRAD;
+    a.form = GROUPED_BACKWARD;
     a.dtype = dtype;
     a.offsets = offsets;
     a.R = R;
@@ -389,15 +385,13 @@ int kp_grouped_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, i
     a.d0 = base;
     a.d1 = base + w.du;
     a.ldd = w.ld;
-    a.y0 = dx;
+    a.y = dx;
     a.ldy = lddx;
+    a.dw0 = dWg;
+    a.dw1 = dWu;
     a.scale = scaling;
+    a.pdl = true;
     a.err = d.err;
-    if ((e = grouped_launch(a, d, stream)) != cudaSuccess) return cuda_failed(e, fn);
-    a.form = GROUPED_WGRAD;
-    a.y0 = dWg;
-    a.y1 = dWu;
-    a.ldy = K;
     e = grouped_launch(a, d, stream);
     return e == cudaSuccess ? KP_OK : cuda_failed(e, fn);
 }

@@ -16,9 +16,10 @@
 //   GATED   A = 64 rows of Wg_e and the same ones of Wu_e per CTA: gates are in
 //           accumulator lanes 0 .. 63 and their factors in lanes 64 .. 127, and the warps
 //           that read them swap halves through shared memory.
-//   DGRAD   A = W_e read along its rows (the MMA's transposed operand), B = rows of the
-//           output's gradient; two products into one accumulator for the gated block.
-//   WGRAD   A = x, B = the output's gradient, both transposed, contracted over the
+//   BACKWARD  one list of the tiles of dx and of the weights' gradients.
+//           dx: A = W_e read along its rows (the MMA's transposed operand), B = rows of
+//           the output's gradient; two products into one accumulator for the gated block.
+//           dW: A = x, B = the output's gradient, both transposed, contracted over the
 //           expert's rows. The block of 64 that an expert's rows end in also brings rows
 //           of others: MMA steps of 16 past the end are left out, and in the step that
 //           the end is in, warp 10 of both CTAs clears the others' rows first.
@@ -28,7 +29,7 @@
 // rows a store (with two columns of two rows a store, swapped between lanes, a 256 x 256
 // tile took 13000 cycles on its way out, as long as 25 K blocks).
 //
-// Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 9: epilogue; warp 10: WGRAD.
+// Warp 0: copies; warp 1: TMEM, MMA (leader); warps 2 .. 9: epilogue; warp 10: BACKWARD.
 #include <algorithm>
 #include <mutex>
 
@@ -38,7 +39,7 @@ namespace kp {
 
 namespace {
 
-constexpr int kThreads = 320, kThreadsW = 352;
+constexpr int kThreads = 320, kThreadsBack = 352;
 constexpr int kTile = 256;                // rows of A per cluster; of B at most
 constexpr uint32_t kHalf = 128 * 128;     // bytes of 128 rows of a K block (128 bytes of K)
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -47,28 +48,29 @@ constexpr uint32_t kBox = 2048;           // of a warp on an accumulator's way o
 constexpr size_t kBarBytes = (3 * kMaxStages + 4) * 8 + 16;
 
 struct GroupedMaps {
-    CUtensorMap a0, a1, b0, b1;
+    CUtensorMap a0, a1, b0, b1;   // W (gated: Wg, Wu; dx: of either product), rows of x or of the gradients
+    CUtensorMap ax, bw0, bw1;     // dW: x, the gradients
 };
 
 struct GroupedParams {
     const int32_t *offsets;
-    uint16_t *y0, *y1;
+    uint16_t *y[3];       // y, h or dx; dW0, dW1
     float *g, *u;
     int64_t ldy;
     const float *scale;
     int *err;
     int R, E, N;
-    int M;                // columns of the output
-    int rows_n;           // WGRAD: rows of the output (features)
-    int tiles_m, tiles_n; // WGRAD: tiles along both
-    int products;         // DGRAD: into one accumulator; WGRAD: outputs
-    int KB, K;            // K blocks (DGRAD: of one product) and columns of the contraction (not WGRAD)
-    int nt;               // WGRAD: B's rows per tile; else at most
-    int box;              // rows of a copy of B
+    int M;                // columns of the outputs
+    int tiles_m;          // tiles along them
+    int cap;              // rows of B in a tile at most (dW: not)
+    int box;              // rows of a copy of B (dW: 64)
+    int KB, K;            // K blocks and columns of the contraction (dx: of one product; dW: not)
+    int products;         // dx: into one accumulator; dW: outputs
+    int tiles_n, nt;      // dW: tiles along the features, and their width
     int stages;
     uint32_t stage_bytes, idesc;
     int act, dtype;
-    int vec;              // the output's rows start on 16 (2) or 4 (1) bytes
+    int vec[2];           // the output's (dW's) rows start on 16 (2) or 4 (1) bytes
 };
 
 __device__ __forceinline__ void pair_load2(uint32_t dst, const void *map, uint32_t bar, int c0, int c1) {
@@ -217,11 +219,10 @@ __device__ __forceinline__ void put_box(uint16_t *dst, int64_t ld, uint32_t box,
 }
 
 template <int kForm>
-__global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kThreads, 1) __cluster_dims__(2, 1, 1)
     grouped_kernel(const __grid_constant__ GroupedMaps tm, const GroupedParams p) {
     constexpr bool kGated = kForm == GROUPED_GATED;
-    constexpr bool kD = kForm == GROUPED_DGRAD;
-    constexpr bool kW = kForm == GROUPED_WGRAD;
+    constexpr bool kBack = kForm == GROUPED_BACKWARD;
 
     extern __shared__ uint8_t gt_smem_raw[];
     const uint32_t raw = smem_u32(gt_smem_raw);
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
     const uint32_t boxes0 = base + S * p.stage_bytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(gbase + S * p.stage_bytes + 8 * kBox);
     uint64_t *empty = full + kMaxStages;
-    uint64_t *ends = empty + kMaxStages;      // WGRAD: copies of a block that an expert's rows end in
+    uint64_t *ends = empty + kMaxStages;      // dW: copies of a block that an expert's rows end in
     uint64_t *accf = ends + kMaxStages;
     uint64_t *acce = accf + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(full + s), kW ? 2 : 1);
+            mbar_init(smem_u32(full + s), kBack ? 2 : 1);
             mbar_init(smem_u32(empty + s), 1);
             mbar_init(smem_u32(ends + s), 1);
         }
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
             next = max(next, f);
             most = __shfl_sync(0xFFFFFFFFu, next, 31);
             const int c = e < p.E ? next - f : 0;
-            int t = (c + kTile - 1) / kTile;
+            int t = (c + p.cap - 1) / p.cap;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
@@ -299,43 +300,49 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
     cluster_sync_all();   // barriers of both CTAs exist
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait();   // the kernel before may still write gradients and their scale; nothing above reads them
 
     struct Item {
-        int e, z;             // expert; WGRAD: which output
+        int e, z;             // expert; 0: y, h or dx; 1, 2: a weight's gradient
         int m0, n0, rows;     // first row of A, first row of B, rows of B that count
         int nt, kb;           // MMA columns, K blocks
     };
-    // The i-th item of this cluster, e at or behind `it`'s last; false when there is none.
+    // The i-th item of this cluster, e at or behind `it`'s last but for the gradients of
+    // the weights; false when there is none.
     auto get = [&](int i, Item &it) {
-        const int j = cid + i * nclu;
-        if constexpr (kW) {
-            const int per = p.tiles_m * p.tiles_n * p.products;
-            it.e = j / per;
-            if (it.e >= p.E) return false;
-            int l = j - it.e * per;
-            it.z = l / (p.tiles_m * p.tiles_n);
-            l -= it.z * p.tiles_m * p.tiles_n;
-            it.m0 = l % p.tiles_m * kTile;
-            it.n0 = l / p.tiles_m * p.nt;
-            it.rows = min(p.rows_n - it.n0, p.nt);
-            it.nt = p.nt;
-            it.kb = (count[it.e] + 63) >> 6;
-        } else {
-            const int t = j / p.tiles_m;
-            if (t >= tiles[p.E]) return false;
+        int j = cid + i * nclu;
+        const int t = j / p.tiles_m;
+        if (t < tiles[p.E]) {
             while (tiles[it.e + 1] <= t) ++it.e;
             const int n = tiles[it.e + 1] - tiles[it.e];
             const int l = j - tiles[it.e] * p.tiles_m;
             const int c = count[it.e];
-            const int per = ((c + n - 1) / n + 31) & ~31;   // rows of a tile, about even; 256 at most,
+            const int per = ((c + n - 1) / n + 31) & ~31;   // rows of a tile, about even; `cap` at most,
                                                              // so that the last one has some
+            it.z = 0;
             it.m0 = l / n * (kGated ? 128 : kTile);
             it.n0 = l % n * per;
             it.rows = min(c - it.n0, per);
             it.nt = (it.rows + 31) & ~31;
-            it.kb = p.KB * (kD ? p.products : 1);
+            it.kb = p.KB * (kBack ? p.products : 1);
+            return true;
         }
-        return true;
+        if constexpr (kBack) {
+            j -= tiles[p.E] * p.tiles_m;
+            const int per = p.tiles_m * p.tiles_n;
+            it.e = j / (per * p.products);
+            if (it.e >= p.E) return false;
+            j -= it.e * per * p.products;
+            it.z = 1 + j / per;
+            j -= (it.z - 1) * per;
+            it.m0 = j % p.tiles_m * kTile;
+            it.n0 = j / p.tiles_m * p.nt;
+            it.rows = min(p.N - it.n0, p.nt);
+            it.nt = p.nt;
+            it.kb = (count[it.e] + 63) >> 6;
+            return true;
+        }
+        return false;
     };
 
     if (warp == 0) {
@@ -347,9 +354,11 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
         for (int i = 0; get(i, it); ++i) {
             const int row0 = first[it.e];
             const int half = it.nt >> 1;
-            const int boxes = kW ? half >> 6 : (half + p.box - 1) / p.box;
-            const uint32_t bytes = kHalf + static_cast<uint32_t>(boxes) * (kW ? 8192u : static_cast<uint32_t>(p.box) * 128u);
-            const int left = kW ? count[it.e] & 15 : 0;          // an end within an MMA's 16 rows
+            const bool dw = kBack && it.z;
+            const int box = dw ? 64 : p.box;
+            const int boxes = (half + box - 1) / box;
+            const uint32_t bytes = kHalf + static_cast<uint32_t>(boxes * box) * 128u;
+            const bool left = dw && (count[it.e] & 15);          // an end within an MMA's 16 rows
             for (int kb = 0; kb < it.kb; ++kb) {
                 mbar_wait_bounded(smem_u32(empty + stage), phase, abort_flag, p.err, DEV_TIMEOUT_EMPTY);
                 const uint32_t st = base + stage * p.stage_bytes;
@@ -357,44 +366,43 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
                 const int s = stage;
                 if (++stage == S) stage = 0, phase ^= 1;
                 if (!mine) continue;
-                if constexpr (kW) {
-                    const int m = it.m0 + rank * 128, n = it.n0 + rank * half;
-                    const int r = row0 + kb * 64;
-                    const CUtensorMap *mb = it.z ? &tm.b1 : &tm.b0;
-                    if (left && kb == it.kb - 1) {   // on a barrier of this CTA's, which warp 10 waits for
-                        const uint32_t own = smem_u32(ends + s);
-                        mbar_expect_tx(own, bytes);
-                        own_load2(st, &tm.a0, own, m, r);
-                        own_load2(st + 8192, &tm.a0, own, m + 64, r);
-                        for (int b = 0; b < boxes; ++b) own_load2(st + kHalf + b * 8192, mb, own, n + b * 64, r);
-                        continue;
-                    }
-                    if (rank == 0)
-                        mbar_expect_tx(smem_u32(full + s), 2 * bytes);
-                    else
-                        remote_arrive_relaxed(bar);
-                    pair_load2(st, &tm.a0, bar, m, r);
-                    pair_load2(st + 8192, &tm.a0, bar, m + 64, r);
-                    for (int b = 0; b < boxes; ++b) pair_load2(st + kHalf + b * 8192, mb, bar, n + b * 64, r);
+                const int m = it.m0 + rank * (kGated ? 64 : 128);
+                if (left && kb == it.kb - 1) {   // on a barrier of this CTA's, which warp 10 waits for
+                    const uint32_t own = smem_u32(ends + s);
+                    const int n = it.n0 + rank * half, r = row0 + kb * 64;
+                    mbar_expect_tx(own, bytes);
+                    own_load2(st, &tm.ax, own, m, r);
+                    own_load2(st + 8192, &tm.ax, own, m + 64, r);
+                    for (int b = 0; b < boxes; ++b)
+                        own_load2(st + kHalf + b * 8192, it.z == 2 ? &tm.bw1 : &tm.bw0, own, n + b * 64, r);
+                    continue;
+                }
+                if (rank == 0)
+                    mbar_expect_tx(smem_u32(full + s), 2 * bytes);
+                else if (kBack)
+                    remote_arrive_relaxed(bar);
+                if (dw) {
+                    const int n = it.n0 + rank * half, r = row0 + kb * 64;
+                    pair_load2(st, &tm.ax, bar, m, r);
+                    pair_load2(st + 8192, &tm.ax, bar, m + 64, r);
+                    for (int b = 0; b < boxes; ++b)
+                        pair_load2(st + kHalf + b * 8192, it.z == 2 ? &tm.bw1 : &tm.bw0, bar, n + b * 64, r);
                 } else {
-                    if (rank == 0) mbar_expect_tx(smem_u32(full + s), 2 * bytes);
-                    const bool second = kD && kb >= p.KB;
+                    const bool second = kBack && kb >= p.KB;
                     const int k = (second ? kb - p.KB : kb) * 64;
                     const CUtensorMap *ma = second ? &tm.a1 : &tm.a0;
                     if constexpr (kGated) {
-                        const int f = it.m0 + rank * 64;
-                        pair_load3(st, &tm.a0, bar, k, f, it.e);
-                        pair_load3(st + 8192, &tm.a1, bar, k, f, it.e);
-                    } else if constexpr (kD) {
-                        const int m = it.m0 + rank * 128;
+                        pair_load3(st, &tm.a0, bar, k, m, it.e);
+                        pair_load3(st + 8192, &tm.a1, bar, k, m, it.e);
+                    } else if constexpr (kBack) {
                         pair_load3(st, ma, bar, m, k, it.e);
                         pair_load3(st + 8192, ma, bar, m + 64, k, it.e);
                     } else {
-                        pair_load3(st, ma, bar, k, it.m0 + rank * 128, it.e);
+                        pair_load3(st, ma, bar, k, m, it.e);
                     }
                     const int n = row0 + it.n0 + rank * half;
                     const CUtensorMap *mb = second ? &tm.b1 : &tm.b0;
-                    for (int b = 0; b < boxes; ++b) pair_load2(st + kHalf + b * p.box * 128, mb, bar, k, n + b * p.box);
+                    for (int b = 0; b < boxes; ++b) pair_load2(st + kHalf + b * box * 128, mb, bar, k, n + b * box);
                 }
             }
         }
@@ -438,21 +446,23 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
                 next = it;
                 ++i;
                 more_items = find(i, next);
-                const uint32_t idesc = p.idesc | static_cast<uint32_t>(it.nt >> 3) << 17;
-                const int depth = kW ? count[it.e] : p.K;
+                const bool dw = kBack && it.z;
+                const uint32_t idesc = p.idesc | static_cast<uint32_t>(it.nt >> 3) << 17 | (dw ? 1u << 16 : 0u);
+                const int depth = dw ? count[it.e] : p.K;
+                const uint32_t bstep = dw ? 128 : 2;
                 mbar_wait_bounded(smem_u32(acce + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
                 tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(as) * 256;
                 for (int kb = 0; kb < it.kb; ++kb) {
                     const uint32_t st = base + stage * p.stage_bytes;
-                    const uint64_t ad = kW || kD ? desc_mn(st) : desc_kmajor(st);
-                    const uint64_t bd = kW ? desc_mn(st + kHalf) : desc_kmajor(st + kHalf);
+                    const uint64_t ad = kBack ? desc_mn(st) : desc_kmajor(st);
+                    const uint64_t bd = dw ? desc_mn(st + kHalf) : desc_kmajor(st + kHalf);
                     const uint32_t bar = smem_u32(empty + stage);
-                    const int at = kD && kb >= p.KB ? kb - p.KB : kb;
+                    const int at = kBack && !dw && kb >= p.KB ? kb - p.KB : kb;
                     const int steps = min(4, (depth - at * 64 + 15) >> 4);
                     auto mma = [&](int kk) {
                         if (mine)
-                            pair_mma(d, ad + kk * (kW || kD ? 128 : 2), bd + kk * (kW ? 128 : 2), idesc, kb > 0 || kk > 0);
+                            pair_mma(d, ad + kk * (kBack ? 128 : 2), bd + kk * bstep, idesc, kb > 0 || kk > 0);
                     };
 #pragma unroll
                     for (int kk = 0; kk < 3; ++kk)
@@ -480,16 +490,16 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
         Item it = {};
         for (int i = 0; get(i, it); ++i) {
             const int m = it.m0 + (kGated ? rank * 64 + (q & 1) * 32 : rank * 128 + q * 32);
-            uint16_t *dst = p.y0;
-            if constexpr (kW)
-                dst = (it.z ? p.y1 : p.y0) + (static_cast<int64_t>(it.e) * p.rows_n + it.n0) * p.ldy;
-            else
-                dst += static_cast<int64_t>(first[it.e] + it.n0) * p.ldy;
-            if (kW && it.kb == 0) {   // an expert without rows
+            const bool dw = kBack && it.z;
+            const int64_t ldy = dw ? p.M : p.ldy;
+            const int vec = p.vec[dw];
+            uint16_t *dst = p.y[kBack ? it.z : 0] +
+                            (dw ? static_cast<int64_t>(it.e) * p.N + it.n0 : static_cast<int64_t>(first[it.e] + it.n0)) * ldy;
+            if (kBack && it.kb == 0) {   // an expert without rows
                 const uint32_t zero[4] = {};
                 for (int c = 0; c < 4; ++c) store_fragments(box_at(box, 8 * c + (lane & 7), lane >> 3), zero);
                 for (int c = 32 * half; c < it.rows; c += 64)
-                    put_box<32>(dst + c * p.ldy, p.ldy, box, m, p.M, it.rows - c, lane, p.vec);
+                    put_box<32>(dst + c * ldy, ldy, box, m, p.M, it.rows - c, lane, vec);
                 continue;
             }
             mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
@@ -554,7 +564,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
                                          p.dtype);
                         store_fragments(box_at(box, 8 * i + (lane & 7), lane >> 3), r);
                     }
-                    put_box<16>(dst + n * p.ldy, p.ldy, box, m, p.M, rows, lane, p.vec);
+                    put_box<16>(dst + n * ldy, ldy, box, m, p.M, rows, lane, vec);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -565,7 +575,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
                                          __uint_as_float(v[k >> 1][4 * i + 2 * (k & 1) + 1]) * scale, p.dtype);
                         store_fragments(box_at(box, 8 * i + (lane & 7), lane >> 3), r);
                     }
-                    put_box<32>(dst + c * p.ldy, p.ldy, box, m, p.M, it.rows - c, lane, p.vec);
+                    put_box<32>(dst + c * ldy, ldy, box, m, p.M, it.rows - c, lane, vec);
                 }
             }
             tc_fence_before();
@@ -574,7 +584,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
             if (++as == 2) as = 0, aphase ^= 1;
         }
         __syncwarp();
-    } else if constexpr (kW) {
+    } else if constexpr (kBack) {
         // Rows of others behind an expert's last one, within the MMA step that it is in.
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);
         uint32_t seen = 0;   // phases of `ends`, a bit a stage
@@ -583,7 +593,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_WGRAD ? kThreadsW : kThreads,
         for (int i = 0; get(i, it); ++i) {
             const int left = count[it.e] & 15;
             end = (end + it.kb) % S;
-            if (!it.kb || !left) continue;
+            if (!it.z || !it.kb || !left) continue;
             const int s = end ? end - 1 : S - 1;
             mbar_wait_bounded(smem_u32(ends + s), (seen >> s) & 1, abort_flag, p.err, DEV_TIMEOUT_FULL);
             seen ^= 1u << s;
@@ -618,10 +628,34 @@ bool g_ready[64];   // devices whose kernels have their shared memory raised
 
 }  // namespace
 
+// SM cycles of a tile: its K blocks, each bound by its MMAs or by the copies of its operands
+// (about 70 bytes a cycle reach an SM), the accumulator's way out where that is longer, and
+// what neither hides.
+static float tile_cycles(int nt, float kb) {
+    const float block = std::max(2.f * nt, (16384.f + 64.f * nt) / 70.f);
+    return std::max(kb * block, 800.f + 18.f * nt) + 1500.f;
+}
+
+// The width of the tiles that `rows` rows in each of `groups` groups are cut into: the
+// rounds of tiles over the SM pairs times a tile's cycles. How many rows a group really
+// has is on the device; even groups are as good a guess as any.
+static int tile_cap(int64_t groups, int64_t rows, int64_t tiles_m, float kb, int pairs) {
+    int best = kTile;
+    float least = -1.f;
+    for (int cap = kTile; cap >= 64; cap -= 32) {
+        const int64_t n = (rows + cap - 1) / cap;
+        const int nt = static_cast<int>(((rows + n - 1) / n + 31) / 32 * 32);
+        const float rounds = static_cast<float>(groups * n * tiles_m) / pairs;
+        const float cost = (rounds <= 1.f ? 1.f : rounds + 0.5f) * tile_cycles(nt, kb);
+        if (least < 0 || cost < 0.98f * least) least = cost, best = cap;
+    }
+    return best;
+}
+
 cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s) {
     using Fn = void (*)(GroupedMaps, GroupedParams);
     static const Fn kernels[] = {grouped_kernel<GROUPED_PLAIN>, grouped_kernel<GROUPED_GATED>,
-                                 grouped_kernel<GROUPED_DGRAD>, grouped_kernel<GROUPED_WGRAD>};
+                                 grouped_kernel<GROUPED_BACKWARD>};
     cudaError_t e = cudaSuccess;
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -633,11 +667,12 @@ cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s
             if (d.dev < 64) g_ready[d.dev] = true;
         }
     }
-    const bool gated = a.form == GROUPED_GATED, dgrad = a.form == GROUPED_DGRAD, wgrad = a.form == GROUPED_WGRAD;
+    const bool gated = a.form == GROUPED_GATED, back = a.form == GROUPED_BACKWARD;
     GroupedParams p = {};
     p.offsets = a.offsets;
-    p.y0 = static_cast<uint16_t *>(a.y0);
-    p.y1 = static_cast<uint16_t *>(a.y1);
+    p.y[0] = static_cast<uint16_t *>(a.y);
+    p.y[1] = static_cast<uint16_t *>(a.dw0);
+    p.y[2] = static_cast<uint16_t *>(a.dw1);
     p.g = a.g;
     p.u = a.u;
     p.ldy = a.ldy;
@@ -646,31 +681,36 @@ cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s
     p.R = a.R;
     p.E = a.E;
     p.N = a.N;
-    p.M = dgrad || wgrad ? a.K : a.N;
-    p.rows_n = a.N;
+    p.M = back ? a.K : a.N;
     p.tiles_m = cdiv(p.M, gated ? 128 : kTile);
-    p.products = a.d1 ? 2 : 1;
-    p.K = dgrad ? a.N : a.K;
+    p.products = back && a.d1 ? 2 : 1;
+    p.K = back ? a.N : a.K;
     p.KB = cdiv(p.K, 64);
     p.act = a.act;
     p.dtype = a.dtype;
-    const uintptr_t starts = reinterpret_cast<uintptr_t>(a.y0) | reinterpret_cast<uintptr_t>(a.y1) | static_cast<uintptr_t>(a.ldy * 2);
-    p.vec = starts % 16 == 0 ? 2 : starts % 4 == 0 ? 1 : 0;
-    p.idesc = idesc_f16(a.dtype, 256, 0, dgrad || wgrad, wgrad);
-    int64_t items;
-    int half;   // rows of B that a CTA holds at most
-    if (wgrad) {
-        p.nt = a.N <= 128 ? 128 : kTile;
+    auto starts = [](const void *y, int64_t ld) {
+        const uintptr_t v = reinterpret_cast<uintptr_t>(y) | static_cast<uintptr_t>(ld * 2);
+        return v % 16 == 0 ? 2 : v % 4 == 0 ? 1 : 0;
+    };
+    p.vec[0] = starts(a.y, a.ldy);
+    p.vec[1] = starts(a.dw0, a.K);
+    p.idesc = idesc_f16(a.dtype, 256, 0, back);
+    // Tiles of rows: as few as there are, copied in as few pieces as do not bring many of
+    // other experts.
+    const int used = std::min(a.E, a.R), mean = a.R / used;
+    p.cap = tile_cap(used, mean, p.tiles_m, static_cast<float>(p.KB) * p.products, d.sms / 2);
+    p.cap = std::min(p.cap, (a.R + 31) / 32 * 32);
+    p.box = std::min(mean >= 128 ? 64 : mean >= 32 ? 32 : 16, p.cap / 2);
+    int half = cdiv(p.cap / 2, p.box) * p.box;   // rows of B that a CTA holds at most
+    int64_t items = (static_cast<int64_t>(a.R) / p.cap + used) * p.tiles_m;
+    if (back) {
+        p.nt = a.N <= 128 || tile_cap(static_cast<int64_t>(a.E) * p.products, a.N, p.tiles_m, static_cast<float>(cdiv(mean, 64)),
+                                      d.sms / 2) <= 128
+                   ? 128
+                   : kTile;
         p.tiles_n = cdiv(a.N, p.nt);
-        half = p.nt / 2;
-        items = static_cast<int64_t>(a.E) * p.tiles_m * p.tiles_n * p.products;
-    } else {
-        // copies of B: as few as there are rows for, without many rows of other experts
-        p.nt = a.R < kTile ? (a.R + 31) / 32 * 32 : kTile;
-        const int mean = a.R / a.E;
-        p.box = std::min(mean >= 128 ? 64 : mean >= 32 ? 32 : 16, p.nt / 2);
-        half = cdiv(p.nt / 2, p.box) * p.box;
-        items = (static_cast<int64_t>(a.R) / kTile + std::min(a.E, a.R)) * p.tiles_m;
+        half = std::max(half, p.nt / 2);
+        items += static_cast<int64_t>(a.E) * p.tiles_m * p.tiles_n * p.products;
     }
     if (items > (1 << 30)) return cudaErrorInvalidValue;
     p.stage_bytes = kHalf + static_cast<uint32_t>(half) * 128;
@@ -684,29 +724,34 @@ cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s
     auto rows = [&](CUtensorMap *m, const void *ptr, int cols, int64_t ld, int box_rows) {
         if (e == cudaSuccess) e = ffn_tensor_map(m, ptr, a.R, cols, ld, box_rows, 64, a.dtype);
     };
-    if (wgrad) {
-        rows(&tm.a0, a.x, a.K, a.ldx, 64);
-        rows(&tm.b0, a.d0, a.N, a.ldd, 64);
-        if (a.d1) rows(&tm.b1, a.d1, a.N, a.ldd, 64);
-    } else if (dgrad) {
-        experts(&tm.a0, a.w0, 64);
+    experts(&tm.a0, a.w0, gated || back ? 64 : 128);
+    if (gated || p.products == 2) experts(&tm.a1, a.w1, 64);
+    if (back) {
         rows(&tm.b0, a.d0, a.N, a.ldd, p.box);
-        if (a.d1) {
-            experts(&tm.a1, a.w1, 64);
+        rows(&tm.bw0, a.d0, a.N, a.ldd, 64);
+        if (p.products == 2) {
             rows(&tm.b1, a.d1, a.N, a.ldd, p.box);
+            rows(&tm.bw1, a.d1, a.N, a.ldd, 64);
         }
+        rows(&tm.ax, a.x, a.K, a.ldx, 64);
     } else {
-        experts(&tm.a0, a.w0, gated ? 64 : 128);
-        if (gated) experts(&tm.a1, a.w1, 64);
         rows(&tm.b0, a.x, a.K, a.ldx, p.box);
     }
     if (e != cudaSuccess) return e;
     size_t smem = 0;
     if ((e = ffn_smem_for_tmem(d.dev, 512, fixed + static_cast<size_t>(p.stages) * p.stage_bytes, &smem)) != cudaSuccess)
         return e;
-    const int clusters = static_cast<int>(std::min<int64_t>(items, d.sms / 2));
-    kernels[a.form]<<<2 * clusters, wgrad ? kThreadsW : kThreads, smem, s>>>(tm, p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u * static_cast<unsigned>(std::min<int64_t>(items, d.sms / 2)), 1, 1);
+    cfg.blockDim = dim3(back ? kThreadsBack : kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernels[a.form], tm, p);
 }
 
 }  // namespace kp
