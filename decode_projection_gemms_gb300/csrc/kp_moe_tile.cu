@@ -62,11 +62,11 @@ struct GroupedParams {
     int R, E, N;
     int M;                // columns of the outputs
     int tiles_m;          // tiles along them
-    int cap;              // rows of B in a tile at most (dW: not)
+    int cap;              // rows of B in a tile that a stage has room for (dW: not)
     int box;              // rows of a copy of B (dW: 64)
     int KB, K;            // K blocks and columns of the contraction (dx: of one product; dW: not)
     int products;         // dx: into one accumulator; dW: outputs
-    int tiles_n, nt;      // dW: tiles along the features, and their width
+    int tiles_n, nt, KBw; // dW: tiles along the features, their width, about how many K blocks
     int stages;
     uint32_t stage_bytes, idesc;
     int act, dtype;
@@ -218,6 +218,17 @@ __device__ __forceinline__ void put_box(uint16_t *dst, int64_t ld, uint32_t box,
     __syncwarp();   // the box is free
 }
 
+// Widths that tiles of rows are cut to.
+constexpr int kCaps = 7;
+__host__ __device__ constexpr int cap_of(int i) { return kTile - 32 * i; }
+// SM cycles of a tile: its K blocks, each bound by its MMAs or by the copies of its operands
+// (about 70 bytes a cycle reach an SM), the accumulator's way out where that is longer, and
+// what neither hides.
+__host__ __device__ __forceinline__ float tile_cycles(float nt, float kb) {
+    const float block = fmaxf(2.f * nt, (16384.f + 64.f * nt) / 70.f);
+    return fmaxf(kb * block, 800.f + 18.f * nt) + 1500.f;
+}
+
 template <int kForm>
 __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kThreads, 1) __cluster_dims__(2, 1, 1)
     grouped_kernel(const __grid_constant__ GroupedMaps tm, const GroupedParams p) {
@@ -268,7 +279,8 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
     if (warp == 2) {   // the experts' rows, and the sums of their tiles
         // Whatever the offsets hold, the rows lie within [0, R) and no two experts
         // have the same: an expert's begin at the largest number up to its own.
-        int run = 0, most = 0;
+        int most = 0, all = 0;
+        int n[kCaps] = {};
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
             int f = e <= p.E ? min(max(__ldg(p.offsets + e), 0), p.R) : 0;
@@ -279,17 +291,48 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
             next = max(next, f);
             most = __shfl_sync(0xFFFFFFFFu, next, 31);
             const int c = e < p.E ? next - f : 0;
-            int t = (c + p.cap - 1) / p.cap;
+            all += c;
+#pragma unroll
+            for (int i = 0; i < kCaps; ++i) n[i] += (c + cap_of(i) - 1) / cap_of(i);
+            if (e < p.E) {
+                first[e] = f;
+                count[e] = c;
+            }
+        }
+        // The width that tiles of rows are cut to: the one whose rounds of tiles over the
+        // clusters take least. (4003 rows on 8 experts, 1000 x 1416: 128 or 256 columns,
+        // as the rounds fall.)
+        int cap = p.cap;
+        if (cap > cap_of(kCaps - 1)) {   // a lane a width
+            const float rows = static_cast<float>(__reduce_add_sync(0xFFFFFFFFu, all)) * p.tiles_m;
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < kCaps; ++i) {
+                const int v = __reduce_add_sync(0xFFFFFFFFu, n[i]);
+                if (lane == i) t = static_cast<float>(v) * p.tiles_m;
+            }
+            const float one = tile_cycles(__fdividef(rows, fmaxf(t, 1.f)), static_cast<float>(p.KB * (kBack ? p.products : 1)));
+            float cost = ceilf(__fdividef(t, nclu)) * one;
+            if constexpr (kBack) {
+                const float w = static_cast<float>(p.E * p.products) * (p.tiles_m * p.tiles_n);
+                const float one_w = tile_cycles(p.nt, static_cast<float>(p.KBw));
+                cost = fmaxf(one, __fdividef(t * one + w * one_w, nclu) + (t + w > nclu ? 0.5f * one_w : 0.f));
+            }
+            // (positive floats order like their bits; the wider one where they are about equal)
+            cost = lane < kCaps && kTile - 32 * lane <= p.cap ? cost * (1.f + 0.004f * lane) : 3e38f;
+            const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, __float_as_uint(cost));
+            cap = kTile - 32 * (__ffs(__ballot_sync(0xFFFFFFFFu, __float_as_uint(cost) == least)) - 1);
+        }
+        int run = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            int t = e < p.E ? (count[e] + cap - 1) / cap : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
                 if (lane >= d) t += o;
             }
-            if (e < p.E) {
-                first[e] = f;
-                count[e] = c;
-                tiles[e + 1] = run + t;
-            }
+            if (e < p.E) tiles[e + 1] = run + t;
             run += __shfl_sync(0xFFFFFFFFu, t, 31);
         }
         if (lane == 0) tiles[0] = 0;
@@ -628,30 +671,6 @@ bool g_ready[64];   // devices whose kernels have their shared memory raised
 
 }  // namespace
 
-// SM cycles of a tile: its K blocks, each bound by its MMAs or by the copies of its operands
-// (about 70 bytes a cycle reach an SM), the accumulator's way out where that is longer, and
-// what neither hides.
-static float tile_cycles(int nt, float kb) {
-    const float block = std::max(2.f * nt, (16384.f + 64.f * nt) / 70.f);
-    return std::max(kb * block, 800.f + 18.f * nt) + 1500.f;
-}
-
-// The width of the tiles that `rows` rows in each of `groups` groups are cut into: the
-// rounds of tiles over the SM pairs times a tile's cycles. How many rows a group really
-// has is on the device; even groups are as good a guess as any.
-static int tile_cap(int64_t groups, int64_t rows, int64_t tiles_m, float kb, int pairs) {
-    int best = kTile;
-    float least = -1.f;
-    for (int cap = kTile; cap >= 64; cap -= 32) {
-        const int64_t n = (rows + cap - 1) / cap;
-        const int nt = static_cast<int>(((rows + n - 1) / n + 31) / 32 * 32);
-        const float rounds = static_cast<float>(groups * n * tiles_m) / pairs;
-        const float cost = (rounds <= 1.f ? 1.f : rounds + 0.5f) * tile_cycles(nt, kb);
-        if (least < 0 || cost < 0.98f * least) least = cost, best = cap;
-    }
-    return best;
-}
-
 cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s) {
     using Fn = void (*)(GroupedMaps, GroupedParams);
     static const Fn kernels[] = {grouped_kernel<GROUPED_PLAIN>, grouped_kernel<GROUPED_GATED>,
@@ -695,19 +714,20 @@ cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s
     p.vec[0] = starts(a.y, a.ldy);
     p.vec[1] = starts(a.dw0, a.K);
     p.idesc = idesc_f16(a.dtype, 256, 0, back);
-    // Tiles of rows: as few as there are, copied in as few pieces as do not bring many of
-    // other experts.
+    // Copies of rows: in as few pieces as do not bring many of other experts.
     const int used = std::min(a.E, a.R), mean = a.R / used;
-    p.cap = tile_cap(used, mean, p.tiles_m, static_cast<float>(p.KB) * p.products, d.sms / 2);
-    p.cap = std::min(p.cap, (a.R + 31) / 32 * 32);
+    p.cap = a.R < kTile ? (a.R + 31) / 32 * 32 : kTile;
     p.box = std::min(mean >= 128 ? 64 : mean >= 32 ? 32 : 16, p.cap / 2);
     int half = cdiv(p.cap / 2, p.box) * p.box;   // rows of B that a CTA holds at most
-    int64_t items = (static_cast<int64_t>(a.R) / p.cap + used) * p.tiles_m;
+    int64_t items = (static_cast<int64_t>(a.R) / std::min(p.cap, cap_of(kCaps - 1)) + used) * p.tiles_m;
     if (back) {
-        p.nt = a.N <= 128 || tile_cap(static_cast<int64_t>(a.E) * p.products, a.N, p.tiles_m, static_cast<float>(cdiv(mean, 64)),
-                                      d.sms / 2) <= 128
-                   ? 128
-                   : kTile;
+        // the weights' gradients in tiles of 256 or 128 features, by rounds times a tile's cycles
+        p.KBw = cdiv(a.R, 64ll * a.E);
+        auto cost = [&](int nt) {
+            const float tiles = static_cast<float>(a.E) * (p.products * p.tiles_m) * cdiv(a.N, nt);
+            return std::max(1.f, tiles / (d.sms / 2)) * tile_cycles(nt, static_cast<float>(p.KBw));
+        };
+        p.nt = cost(128) < cost(kTile) ? 128 : kTile;
         p.tiles_n = cdiv(a.N, p.nt);
         half = std::max(half, p.nt / 2);
         items += static_cast<int64_t>(a.E) * p.tiles_m * p.tiles_n * p.products;
