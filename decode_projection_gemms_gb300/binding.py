@@ -789,8 +789,10 @@ def _experts(W, name: str, dtype, index: int):
         raise ValueError(f"{name} must be on CUDA device {index}, is on {W.device}")
     if W.dim() != 3:
         raise ValueError(f"{name} must be a 3-D tensor [experts, features, columns]")
-    se, ld, inner = W.stride()
     E, rows, cols = W.shape
+    if W.is_contiguous() and cols & 7 == 0:
+        return cols, rows * cols
+    se, ld, inner = W.stride()
     if rows <= 1:   # the stride of a single row, and of a single expert, says nothing
         ld = (cols + 7) // 8 * 8
     if E <= 1:
@@ -1022,7 +1024,8 @@ def grouped_gemm_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, of
     lddy = _rows(dy, "dy", dt, index)
     if dy.shape != (R, N):
         raise ValueError(f"dy must be {(R, N)}, got {tuple(dy.shape)}")
-    dx, dW = x.new_empty((R, K)), x.new_empty((E, N, K))
+    dev = _device(index)
+    dx, dW = torch.empty((R, K), dtype=dt, device=dev), torch.empty((E, N, K), dtype=dt, device=dev)
     rc = load().kp_grouped_gemm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, W.data_ptr(), ldw, sw, dx.data_ptr(), K,
                                          dW.data_ptr(), op, R, E, N, K, _DTYPES[dt], _raw_stream(index))
     if rc:
@@ -1084,7 +1087,9 @@ def grouped_gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tens
     for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
         if t.shape != (R, F):
             raise ValueError(f"{name} must be {(R, F)}, got {tuple(t.shape)}")
-    dx, dWg, dWu = x.new_empty((R, K)), x.new_empty((E, F, K)), x.new_empty((E, F, K))
+    dev = _device(index)
+    dx = torch.empty((R, K), dtype=dt, device=dev)
+    dWg, dWu = torch.empty((E, F, K), dtype=dt, device=dev), torch.empty((E, F, K), dtype=dt, device=dev)
     work, wp, wn = _moe_work(MOE_GATED_BACKWARD, R, F, K, index)
     rc = load().kp_grouped_gated_ffn_backward(dh.data_ptr(), lddh, x.data_ptr(), ldx, Wg.data_ptr(), ldg, sg,
                                               Wu.data_ptr(), ldu, su, g.data_ptr(), u.data_ptr(), dx.data_ptr(), K,
