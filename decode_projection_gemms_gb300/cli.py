@@ -6,6 +6,8 @@ library's choice of kernel.
     python -m decode_projection_gemms_gb300.cli --kda --M 1 16 128 [--layers 4] [--reps 1]
     python -m decode_projection_gemms_gb300.cli --ffn --M 1 16 512 [--F 2048] [--K 7168]
         [--act silu] [--steps 4] [--fp16]
+    python -m decode_projection_gemms_gb300.cli --moe --M 1 16 512 [--experts 32] [--top-k 4]
+        [--F 1024] [--K 4096] [--score softmax] [--act silu] [--steps 4] [--fp16]
 
 GEMM: prints the configuration used (the table's or the built-in rule's
 choice, or the one given with --cfg as comma-separated kp_cfg fields) and the
@@ -18,6 +20,10 @@ feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T. It is trained for `steps`
 steps on a batch of the largest M (towards a teacher block's outputs, on Wg and
 Wu), its weights are converted to microscaled 4 bits, and both forms then serve
 each M: times per call and how far the 4-bit outputs are from the 16-bit ones.
+--moe: a mixture-of-experts layer, y = sum over a token's top-k experts e of w_e (act(x
+Wg_e^T) * (x Wu_e^T)) Wd_e^T with experts and weights from router logits x Wr^T. It is
+trained for `steps` steps on a batch of the largest M (towards a teacher layer's outputs, on
+all four weights) and then serves each M: time per call and rows of the busiest expert.
 Inputs are seeded synthetic bf16 (or fp16 with --fp16).
 """
 from __future__ import annotations
@@ -140,12 +146,86 @@ def run_ffn(m_list, F: int, K: int, act: str, steps: int, reps: int, dtype):
     return losses
 
 
+def moe_layer(x, Wr, Wg, Wu, Wd, top_k: int, act: str = "silu", score: str = "softmax", save: bool = False):
+    """A mixture-of-experts layer's outputs; with ``save`` also what ``moe_layer_backward``
+    needs."""
+    logits = binding.skinny_gemm_ex(x, Wr)
+    route = binding.moe_route(logits, top_k, score=score)
+    rows = binding.moe_dispatch(x, route)
+    if not save:
+        h = binding.grouped_gated_ffn(rows, Wg, Wu, route.offsets, act=act)
+        return binding.moe_combine(binding.grouped_gemm(h, Wd, route.offsets), route), route
+    h, g, u = binding.grouped_gated_ffn(rows, Wg, Wu, route.offsets, act=act, save=True)
+    out = binding.grouped_gemm(h, Wd, route.offsets)
+    return binding.moe_combine(out, route), (logits, route, rows, h, g, u, out)
+
+
+def moe_layer_backward(dy, x, Wr, Wg, Wu, Wd, saved, act: str = "silu"):
+    """Gradients (dx, dWr, dWg, dWu, dWd) of ``moe_layer`` for the gradient of its outputs."""
+    logits, route, rows, h, g, u, out = saved
+    dout, dweights = binding.moe_combine_backward(dy, out, route)
+    dh, dWd = binding.grouped_gemm_backward(dout, h, Wd, route.offsets)
+    drows, dWg, dWu = binding.grouped_gated_ffn_backward(dh, rows, Wg, Wu, route.offsets, g, u, act=act)
+    dlogits = binding.moe_route_backward(dweights, logits, route)
+    # the products of the router: their contractions in whole groups of eight
+    pad = torch.nn.functional.pad
+    T, E = dlogits.shape
+    t, e = -T % 8, -E % 8
+    dWr = binding.skinny_gemm_ex(pad(dlogits.t(), (0, t)).contiguous(), pad(x.t(), (0, t)).contiguous())
+    dx = binding.skinny_gemm_ex(pad(dlogits, (0, e)).contiguous(), pad(Wr.t(), (0, e)).contiguous(),
+                                binding.moe_dispatch_backward(drows, route))
+    return dx, dWr, dWg, dWu, dWd
+
+
+def run_moe(m_list, E: int, top_k: int, F: int, K: int, score: str, act: str, steps: int, reps: int, dtype):
+    dev = torch.device("cuda", torch.cuda.current_device())
+
+    def layer(seed):
+        g = torch.Generator(device=dev).manual_seed(seed)
+
+        def w(*shape):
+            v = torch.empty(shape, dtype=dtype, device=dev)
+            return v.normal_(0.0, shape[-1] ** -0.5, generator=g)
+
+        return w(E, K), w(E, F, K), w(E, F, K), w(E, K, F)
+
+    weights, teacher = layer(1), layer(2)
+    T = max(m_list)
+    x = gen_x(T, K, seed=4, device=dev, dtype=dtype)
+    target, _ = moe_layer(x, weights[0], *teacher[1:], top_k, act, score)   # other experts, the same router
+    losses = []
+    for step in range(steps + 1):
+        y, saved = moe_layer(x, *weights, top_k, act, score, save=True)
+        diff = y - target
+        losses.append(float(diff.float().square().mean()))
+        if step == steps:
+            break
+        grads = moe_layer_backward(diff, x, *weights, saved, act)[1:]
+        for W, dW in zip(weights, grads):   # a step of fixed length along the gradient
+            W.add_(dW, alpha=-0.05 * float(W.float().norm() / (dW.float().norm() + 1e-30)))
+    print(json.dumps({"training": {"tokens": T, "experts": E, "top_k": top_k, "F": F, "K": K, "score": score, "act": act,
+                                   "losses": [round(v, 5) for v in losses]}}))
+    for M in m_list:
+        xs = x[:M]
+        _, route = moe_layer(xs, *weights, top_k, act, score)
+        n = (route.offsets[1:] - route.offsets[:-1]).tolist()
+        us = _time_us(lambda: moe_layer(xs, *weights, top_k, act, score), reps)
+        print(json.dumps({"M": M, "us": round(us, 2), "rows": sum(n), "busiest_expert": max(n),
+                          "experts_used": sum(v > 0 for v in n),
+                          "tflops": round(6.0 * sum(n) * F * K / us / 1e6, 2), "device_error": binding.device_error()}))
+    return losses
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--kda", action="store_true", help="run the KDA projection instead of one GEMM")
     ap.add_argument("--ffn", action="store_true", help="train and serve a gated feed-forward block")
+    ap.add_argument("--moe", action="store_true", help="train and serve a mixture-of-experts layer")
     ap.add_argument("--M", type=int, nargs="+", required=True)
-    ap.add_argument("--F", type=int, default=2048, help="--ffn: features of the block")
+    ap.add_argument("--F", type=int, default=None, help="--ffn, --moe: features of a block (2048, 1024)")
+    ap.add_argument("--experts", type=int, default=32, help="--moe")
+    ap.add_argument("--top-k", type=int, default=4, help="--moe: experts of a token")
+    ap.add_argument("--score", default="softmax", choices=sorted(binding.SCORES), help="--moe")
     ap.add_argument("--act", default="silu", choices=sorted(binding.ACTIVATIONS))
     ap.add_argument("--steps", type=int, default=4, help="--ffn: training steps")
     ap.add_argument("--N", type=int)
@@ -164,8 +244,12 @@ def main(argv=None):
         run_kda(args.M, args.layers, args.reps)
         return
     if args.ffn:
-        run_ffn(args.M, args.F, args.K or 7168, args.act, args.steps, args.reps,
+        run_ffn(args.M, args.F or 2048, args.K or 7168, args.act, args.steps, args.reps,
                 torch.float16 if args.fp16 else torch.bfloat16)
+        return
+    if args.moe:
+        run_moe(args.M, args.experts, args.top_k, args.F or 1024, args.K or 4096, args.score, args.act, args.steps,
+                args.reps, torch.float16 if args.fp16 else torch.bfloat16)
         return
     if args.N is None or args.K is None or len(args.M) != 1:
         ap.error("a GEMM needs one --M and --N, --K")
