@@ -72,6 +72,9 @@ static int check_grouped(const char *fn, int R, int E, int N, int K, int dtype) 
     if (!is16(dtype)) return set_error(KP_EINVAL, "%s: unknown element type %d", fn, dtype);
     if (E > kMoeMaxExperts) return set_error(KP_ESHAPE, "%s: %d experts: at most %d", fn, E, kMoeMaxExperts);
     if (K & 7) return set_error(KP_ESHAPE, "%s: K=%d is not a multiple of 8", fn, K);
+    // (tiles reach past the end by less than their size, in 32 bits)
+    if (R > (1 << 30) || N > (1 << 30) || K > (1 << 30))
+        return set_error(KP_ESHAPE, "%s: %d rows, %d features, %d columns: at most 2^30", fn, R, N, K);
     return KP_OK;
 }
 

@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
             }
         }
         // The width that tiles of rows are cut to: the one whose rounds of tiles over the
-        // clusters take least. (4003 rows on 8 experts, 1000 x 1416: 128 or 256 columns,
-        // as the rounds fall.)
+        // clusters take least. (Gated, 1021 rows on 12 experts, 331 features: 18 us with 256
+        // columns, 11 with 64; 4003 rows on 8 experts, 1000 x 1416: 16.2 with 256, 19.7 with 128.)
         int cap = p.cap;
         if (cap > cap_of(kCaps - 1)) {   // a lane a width
             const float rows = static_cast<float>(__reduce_add_sync(0xFFFFFFFFu, all)) * p.tiles_m;
@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);   // the leader's barriers
         int stage = 0;
         uint32_t phase = 1;   // a fresh barrier passes a wait for the phase before its first
+        uint32_t own_used = 0, own_odd = 0;   // of `ends`, a bit a stage: in use, an odd number of times
         Item it = {};
         for (int i = 0; get(i, it); ++i) {
             const int row0 = first[it.e];
@@ -408,9 +409,11 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
                 const uint32_t bar = full0 + 8 * stage;
                 const int s = stage;
                 if (++stage == S) stage = 0, phase ^= 1;
+                const bool last = left && kb == it.kb - 1;
+                if (last) own_used |= 1u << s, own_odd ^= 1u << s;
                 if (!mine) continue;
                 const int m = it.m0 + rank * (kGated ? 64 : 128);
-                if (left && kb == it.kb - 1) {   // on a barrier of this CTA's, which warp 10 waits for
+                if (last) {   // on a barrier of this CTA's, which warp 10 waits for
                     const uint32_t own = smem_u32(ends + s);
                     const int n = it.n0 + rank * half, r = row0 + kb * 64;
                     mbar_expect_tx(own, bytes);
@@ -457,6 +460,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
         for (int t = 0; t < S; ++t) {
             ffn_drain_wait(smem_u32(empty + stage), phase);
             if (rank == 0) ffn_drain_wait(smem_u32(full + stage), phase);
+            if (kBack && (own_used >> stage & 1)) ffn_drain_wait(smem_u32(ends + stage), (own_odd >> stage & 1) ^ 1);
             if (++stage == S) stage = 0, phase ^= 1;
         }
         __syncwarp();
@@ -638,7 +642,10 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
             end = (end + it.kb) % S;
             if (!it.z || !it.kb || !left) continue;
             const int s = end ? end - 1 : S - 1;
-            mbar_wait_bounded(smem_u32(ends + s), (seen >> s) & 1, abort_flag, p.err, DEV_TIMEOUT_FULL);
+            // This warp has nothing to do while dx is computed, which may take its time: it gives
+            // up by itself after 100 s only, but at once when another wait of the CTA did, and
+            // those go with the stages.
+            mbar_wait_bounded(smem_u32(ends + s), (seen >> s) & 1, abort_flag, p.err, DEV_TIMEOUT_FULL, 100000000000ull);
             seen ^= 1u << s;
             const int r0 = count[it.e] & 63, n = 16 - left;      // K rows r0 .. r0 + n - 1 of every 8 KB group
             const int groups = 2 + (it.nt >> 7);

@@ -436,7 +436,8 @@ KP_API int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, in
  * in token * k + slot within an expert. offsets[e] .. offsets[e + 1] - 1 are expert e's rows
  * (E + 1 ascending numbers from 0 to at most R); rows from offsets[E] on belong to
  * nobody. The grouped products take any such offsets, whoever made them; they lie in
- * device memory, so they are not checked, but no value of theirs leads outside [0, R). */
+ * device memory, so they are not checked, but no value of theirs leads outside [0, R).
+ * The grouped products take at most 2^30 rows, features and columns. */
 
 enum kp_moe_op {
     KP_MOE_ROUTE = 0,            /* M tokens, N experts, top K */
@@ -456,7 +457,7 @@ enum kp_moe_score {
  * fp32, sigmoid only: with the largest score plus bias), and their weights, the chosen
  * scores over their sum. Experts with a logit of minus infinity or NaN (or that plus a
  * bias) are not chosen: a slot that none is left for has id and position -1 and weight 0.
- * A logit of plus infinity counts as the largest finite number.
+ * A logit of plus infinity counts as the largest finite fp32 number.
  *   logits    [T, E] of KP_BF16, KP_FP16 or KP_FP32, row stride ld
  *   ids       [T, k], by descending logit (score plus bias)
  *   weights   [T, k] fp32

@@ -94,6 +94,9 @@ def test_grouped_argument_errors(lib):
     assert gemm(R=0) == OK
     assert gemm(R=-1) == EINVAL and gemm(E=0) == EINVAL and gemm(N=0) == EINVAL and gemm(K=0) == EINVAL
     assert gemm(E=1025) == ESHAPE and gemm(K=12) == ESHAPE and gemm(dtype=2) == EINVAL
+    big = 2 ** 30 + 8
+    assert gemm(R=big) == ESHAPE and gemm(N=big, ldy=big) == ESHAPE
+    assert gemm(K=big, ldx=big, ldw=big, sw=8 * big) == ESHAPE
     assert gemm(x=None) == EINVAL and gemm(x=P8) == EALIGN and gemm(ldx=20) == ESHAPE and gemm(ldx=8) == EINVAL
     assert gemm(W=None) == EINVAL and gemm(W=P8) == EALIGN and gemm(ldw=20) == ESHAPE
     assert gemm(sw=120) == ESHAPE and gemm(sw=132) == ESHAPE
