@@ -109,8 +109,11 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void remote_arrive(uint32_t bar) {   // shared::cluster address
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Behind writes to this CTA's own shared memory, on a barrier of either (shared::cluster
+// address): they are complete before the arrival leaves. (A release at cluster scope takes
+// 890 cycles, this one 40.)
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The same where no write has to be seen behind it. (A releasing arrival waits for the
 // stores before it: an epilogue that gives its accumulator back after a tile's stores, or a
@@ -491,8 +494,6 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
             if (more_items) prepare(0, 0);
             while (more_items) {
                 next = it;
-                ++i;
-                more_items = find(i, next);
                 const bool dw = kBack && it.z;
                 const uint32_t idesc = p.idesc | static_cast<uint32_t>(it.nt >> 3) << 17 | (dw ? 1u << 16 : 0u);
                 const int depth = dw ? count[it.e] : p.K;
@@ -514,6 +515,10 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
 #pragma unroll
                     for (int kk = 0; kk < 3; ++kk)
                         if (kk < steps) mma(kk);
+                    if (kb == 0) {   // found while those run
+                        ++i;
+                        more_items = find(i, next);
+                    }
                     if (++stage == S) stage = 0, phase ^= 1;
                     if (kb + 1 < it.kb || more_items) prepare(stage, phase);
                     if (steps > 3) mma(3);
