@@ -12,7 +12,7 @@ __all__ = ["KdaPlan", "KpCfg", "KdaProjError", "skinny_gemm", "select_config", "
            "gated_ffn_backward",
            "MoeRoute", "moe_route", "moe_route_backward", "moe_dispatch", "moe_dispatch_backward", "moe_combine",
            "moe_combine_backward", "grouped_gemm", "grouped_gemm_backward", "grouped_gated_ffn",
-           "grouped_gated_ffn_backward"]
+           "grouped_gated_ffn_backward", "layer_norm", "layer_norm_backward"]
 
 
 def __getattr__(name):

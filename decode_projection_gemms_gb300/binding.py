@@ -36,7 +36,7 @@ ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 FFN_MX4_GEMM, FFN_MX4_GATED, FFN_GATED, FFN_GATED_BACKWARD = 0, 1, 2, 3
 BRANCH_QKVG, BRANCH_FAB, BRANCH_FB = 0, 1, 2
 # enum kp_moe_op, enum kp_moe_score
-MOE_ROUTE, MOE_GATED_BACKWARD = 0, 1
+MOE_ROUTE, MOE_GATED_BACKWARD, MOE_NORM_BACKWARD = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 # exported symbols (must match include/kdaproj.h)
@@ -50,7 +50,7 @@ EXPORTS = (
     "kp_mx4_gated_ffn", "kp_gated_ffn", "kp_gated_ffn_backward",
     "kp_moe_workspace", "kp_moe_route", "kp_moe_route_backward", "kp_moe_dispatch", "kp_moe_combine",
     "kp_moe_combine_backward", "kp_grouped_gemm", "kp_grouped_gemm_backward", "kp_grouped_gated_ffn",
-    "kp_grouped_gated_ffn_backward",
+    "kp_grouped_gated_ffn_backward", "kp_layer_norm", "kp_layer_norm_backward",
 )
 DEV_SELFTEST = 5   # device error code of kp_selftest_timeout
 
@@ -140,6 +140,8 @@ def load(path: str | None = None):
                                      vp],
             "kp_grouped_gated_ffn_backward": [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, i64, vp, vp, vp,
                                               ci, ci, ci, ci, ci, ci, vp, sz, vp],
+            "kp_layer_norm": [vp, i64, vp, vp, vp, i64, vp, vp, ci, ci, ctypes.c_float, ci, ci, vp],
+            "kp_layer_norm_backward": [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, ci, ci, ci, vp, sz, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -826,6 +828,87 @@ def _pair_floats(t, name: str, r: MoeRoute) -> int:
     if t.shape != (r.tokens, r.top_k) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {(r.tokens, r.top_k)}, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _vector(t, name: str, n: int, dtype, index: int) -> int:
+    """Address of a contiguous vector of n elements, checked."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, is on {t.device}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements, got shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
+               center: bool = True, y: torch.Tensor | None = None, save: bool = False, stream=None):
+    """``y = round((x - mean) * rstd * weight + bias)`` over the rows of ``x`` [T, K], with
+    ``rstd = 1 / sqrt(mean((x - mean)**2) + eps)``, all of it in fp32; with ``center``
+    False the root-mean-square norm, whose mean counts as 0. ``x``, ``weight`` and ``bias`` [K]
+    are all bfloat16, float16 or float32, K at most 16384, rows may be strided. With ``save``
+    returns ``(y, mean, rstd)``, float32 [T] (mean None without centring), for
+    ``layer_norm_backward``."""
+    index = _here(x, "x", stream)
+    if index < 0:
+        with _on(x.device, stream, x, weight, bias, y):
+            return layer_norm(x, weight, bias, eps, center, y, save)
+    ldx = _rows(x, "x", None, index)
+    dt = _FFN_DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    T, K = x.shape
+    wp = _vector(weight, "weight", K, x.dtype, index)
+    bp = None if bias is None else _vector(bias, "bias", K, x.dtype, index)
+    y, ldy = _out(y, "y", T, K, x.dtype, index)
+    mean = rstd = mp = rp = None
+    if save:
+        rstd = torch.empty((T,), dtype=torch.float32, device=_device(index))
+        rp = rstd.data_ptr()
+        if center:
+            mean = torch.empty((T,), dtype=torch.float32, device=_device(index))
+            mp = mean.data_ptr()
+    rc = load().kp_layer_norm(x.data_ptr(), ldx, wp, bp, y.data_ptr(), ldy, mp, rp, T, K, eps, int(bool(center)), dt,
+                              _raw_stream(index))
+    if rc:
+        _check(rc)
+    return (y, mean, rstd) if save else y
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | None,
+                        rstd: torch.Tensor, bias: bool = False, stream=None):
+    """Gradients ``(dx, dweight, dbias)`` of ``layer_norm`` for the gradient ``dy`` [T, K] of
+    its output, from its operands and the ``mean`` (None: without centring) and ``rstd`` it
+    saved; ``dbias`` is None unless ``bias`` asks for it. The weights' gradients are summed in
+    fp32, in the same order every time."""
+    index = _here(x, "x", stream)
+    if index < 0:
+        with _on(x.device, stream, dy, x, weight, mean, rstd):
+            return layer_norm_backward(dy, x, weight, mean, rstd, bias)
+    ldx = _rows(x, "x", None, index)
+    dt = _FFN_DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    T, K = x.shape
+    lddy = _rows(dy, "dy", x.dtype, index)
+    if dy.shape != (T, K):
+        raise ValueError(f"dy must be {(T, K)}, got {tuple(dy.shape)}")
+    wp = _vector(weight, "weight", K, x.dtype, index)
+    mp = None if mean is None else _vector(mean, "mean", T, torch.float32, index)
+    rp = _vector(rstd, "rstd", T, torch.float32, index)
+    dev = _device(index)
+    dx = torch.empty((T, K), dtype=x.dtype, device=dev)
+    dw = torch.empty((K,), dtype=x.dtype, device=dev)
+    db = torch.empty((K,), dtype=x.dtype, device=dev) if bias else None
+    work, kp, kn = _moe_work(MOE_NORM_BACKWARD, T, 1, K, index)
+    rc = load().kp_layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, wp, mp, rp, dx.data_ptr(), K,
+                                       dw.data_ptr(), None if db is None else db.data_ptr(), T, K, dt, kp, kn,
+                                       _raw_stream(index))
+    if rc:
+        _check(rc)
+    return dx, dw, db
 
 
 def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,

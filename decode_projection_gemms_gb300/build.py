@@ -41,9 +41,10 @@ SOURCES = [
     "kp_moe_route.cu",
     "kp_moe_rows.cu",
     "kp_moe_tile.cu",
+    "kp_norm.cu",
     "kp_moe_api.cu",
 ]
-HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh", "kp_ffn.cuh", "kp_mx4.cuh", "kp_moe.cuh"]
+HEADERS = ["kp_internal.cuh", "kp_cc_kernel.cuh", "kp_ffn.cuh", "kp_mx4.cuh", "kp_moe.cuh", "kp_norm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

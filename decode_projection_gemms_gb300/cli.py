@@ -20,10 +20,11 @@ feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T. It is trained for `steps`
 steps on a batch of the largest M (towards a teacher block's outputs, on Wg and
 Wu), its weights are converted to microscaled 4 bits, and both forms then serve
 each M: times per call and how far the 4-bit outputs are from the 16-bit ones.
---moe: a mixture-of-experts layer, y = sum over a token's top-k experts e of w_e (act(x
-Wg_e^T) * (x Wu_e^T)) Wd_e^T with experts and weights from router logits x Wr^T. It is
-trained for `steps` steps on a batch of the largest M (towards a teacher layer's outputs, on
-all four weights) and then serves each M: time per call and rows of the busiest expert.
+--moe: a mixture-of-experts layer behind a norm, y = x + f(z), z the root-mean-square norm
+of x, f(z) the sum over a token's top-k experts e of w_e (act(z Wg_e^T) * (z Wu_e^T)) Wd_e^T
+with experts and weights from router logits z Wr^T. It is trained for `steps` steps on a batch
+of the largest M (towards a teacher layer's outputs, on the norm's weight and the layer's four)
+and then serves each M: time per call and rows of the busiest expert.
 Inputs are seeded synthetic bf16 (or fp16 with --fp16).
 """
 from __future__ import annotations
@@ -177,6 +178,25 @@ def moe_layer_backward(dy, x, Wr, Wg, Wu, Wd, saved, act: str = "silu"):
     return dx, dWr, dWg, dWu, dWd
 
 
+def norm_moe_layer(x, gamma, *weights, top_k: int, act: str = "silu", score: str = "softmax", save: bool = False):
+    """``x + moe_layer(z, *weights)`` with z the root-mean-square norm of x; with ``save`` also
+    what ``norm_moe_layer_backward`` needs, else the routing."""
+    if not save:
+        y, route = moe_layer(binding.layer_norm(x, gamma, center=False), *weights, top_k, act, score)
+        return x + y, route
+    z, _, rstd = binding.layer_norm(x, gamma, center=False, save=True)
+    y, saved = moe_layer(z, *weights, top_k, act, score, save=True)
+    return x + y, (z, rstd, saved)
+
+
+def norm_moe_layer_backward(dy, x, gamma, *weights, saved, act: str = "silu"):
+    """Gradients (dx, dgamma, dWr, dWg, dWu, dWd) of ``norm_moe_layer``."""
+    z, rstd, inner = saved
+    dz, *grads = moe_layer_backward(dy, z, *weights, inner, act)
+    dx, dgamma, _ = binding.layer_norm_backward(dz, x, gamma, None, rstd)
+    return (dy + dx, dgamma, *grads)
+
+
 def run_moe(m_list, E: int, top_k: int, F: int, K: int, score: str, act: str, steps: int, reps: int, dtype):
     dev = torch.device("cuda", torch.cuda.current_device())
 
@@ -187,29 +207,31 @@ def run_moe(m_list, E: int, top_k: int, F: int, K: int, score: str, act: str, st
             v = torch.empty(shape, dtype=dtype, device=dev)
             return v.normal_(0.0, shape[-1] ** -0.5, generator=g)
 
-        return w(E, K), w(E, F, K), w(E, F, K), w(E, K, F)
+        gamma = torch.ones(K, dtype=dtype, device=dev)
+        return gamma, w(E, K), w(E, F, K), w(E, F, K), w(E, K, F)
 
     weights, teacher = layer(1), layer(2)
+    how = {"top_k": top_k, "act": act, "score": score}
     T = max(m_list)
     x = gen_x(T, K, seed=4, device=dev, dtype=dtype)
-    target, _ = moe_layer(x, weights[0], *teacher[1:], top_k, act, score)   # other experts, the same router
+    target, _ = norm_moe_layer(x, *weights[:2], *teacher[2:], **how)   # other experts, the same router
     losses = []
     for step in range(steps + 1):
-        y, saved = moe_layer(x, *weights, top_k, act, score, save=True)
+        y, saved = norm_moe_layer(x, *weights, **how, save=True)
         diff = y - target
         losses.append(float(diff.float().square().mean()))
         if step == steps:
             break
-        grads = moe_layer_backward(diff, x, *weights, saved, act)[1:]
+        grads = norm_moe_layer_backward(diff, x, *weights, saved=saved, act=act)[1:]
         for W, dW in zip(weights, grads):   # a step of fixed length along the gradient
             W.add_(dW, alpha=-0.05 * float(W.float().norm() / (dW.float().norm() + 1e-30)))
     print(json.dumps({"training": {"tokens": T, "experts": E, "top_k": top_k, "F": F, "K": K, "score": score, "act": act,
                                    "losses": [round(v, 5) for v in losses]}}))
     for M in m_list:
         xs = x[:M]
-        _, route = moe_layer(xs, *weights, top_k, act, score)
+        _, route = norm_moe_layer(xs, *weights, **how)
         n = (route.offsets[1:] - route.offsets[:-1]).tolist()
-        us = _time_us(lambda: moe_layer(xs, *weights, top_k, act, score), reps)
+        us = _time_us(lambda: norm_moe_layer(xs, *weights, **how), reps)
         print(json.dumps({"M": M, "us": round(us, 2), "rows": sum(n), "busiest_expert": max(n),
                           "experts_used": sum(v > 0 for v in n),
                           "tflops": round(6.0 * sum(n) * F * K / us / 1e6, 2), "device_error": binding.device_error()}))

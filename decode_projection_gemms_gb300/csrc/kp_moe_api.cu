@@ -1,7 +1,11 @@
-// C entry points of the mixture-of-experts operators (include/kdaproj.h): argument
+// C entry points of the mixture-of-experts operators and of the layer norm in front of
+// them (include/kdaproj.h): argument
 // checks, workspace layout and the order of their launches. Nothing throws and nothing
 // is kept between calls; the caller owns every buffer.
+#include <cmath>
+
 #include "kp_moe.cuh"
+#include "kp_norm.cuh"
 
 namespace kp {
 
@@ -66,6 +70,18 @@ static int check_shuffle(const char *fn, int T, int k, int K, int dtype) {
     if (static_cast<int64_t>(T) * k > 0x7FFFFFFF) return set_error(KP_ESHAPE, "%s: %d x %d rows are too many", fn, T, k);
     return KP_OK;
 }
+static int check_norm(const char *fn, int T, int K, int dtype) {
+    if (T < 0 || K < 1) return set_error(KP_EINVAL, "%s: bad sizes: %d rows, %d columns", fn, T, K);
+    if (!is16(dtype) && dtype != KP_FP32) return set_error(KP_EINVAL, "%s: unknown element type %d", fn, dtype);
+    if (K > kNormMaxCols) return set_error(KP_ESHAPE, "%s: %d columns: at most %d", fn, K, kNormMaxCols);
+    return KP_OK;
+}
+// A matrix of any of the three types, aligned to its elements.
+static int check_matrix(const char *fn, const char *name, const void *p, int64_t ld, int cols, int dtype) {
+    const int rc = check_rows(fn, name, p, ld, cols);
+    if (rc || dtype != KP_FP32 || !misaligned(p, 4)) return rc;
+    return set_error(KP_EALIGN, "%s: %s must be 4-byte aligned", fn, name);
+}
 static int check_grouped(const char *fn, int R, int E, int N, int K, int dtype) {
     if (R < 0 || E < 1 || N < 1 || K < 1)
         return set_error(KP_EINVAL, "%s: bad sizes: %d rows, %d experts, %d features, %d columns", fn, R, E, N, K);
@@ -106,7 +122,7 @@ int kp_moe_workspace(int op, int M, int N, int K, size_t *bytes) {
     const char *fn = "kp_moe_workspace";
     if (!bytes || M < 0 || N < 1 || K < 1)
         return set_error(KP_EINVAL, "%s: bad sizes: %d, %d, %d", fn, M, N, K);
-    if (op != KP_MOE_ROUTE && op != KP_MOE_GATED_BACKWARD) return set_error(KP_EINVAL, "%s: unknown operator %d", fn, op);
+    if (op != KP_MOE_ROUTE && op != KP_MOE_GATED_BACKWARD && op != KP_MOE_NORM_BACKWARD) return set_error(KP_EINVAL, "%s: unknown operator %d", fn, op);
     *bytes = 0;
     if (op == KP_MOE_ROUTE) {
         *bytes = moe_route_scratch(M, N);
@@ -115,7 +131,7 @@ int kp_moe_workspace(int op, int M, int N, int K, size_t *bytes) {
     FfnDev d;
     const int rc = ffn_device(&d);
     if (rc) return rc;
-    if (M) *bytes = gated_backward_work(M, N, d.sms).bytes;
+    if (M) *bytes = op == KP_MOE_GATED_BACKWARD ? gated_backward_work(M, N, d.sms).bytes : norm_backward_scratch(M, K, d.sms);
     return KP_OK;
 }
 
@@ -231,6 +247,80 @@ int kp_moe_combine_backward(const void *dy, int64_t lddy, const void *rows, int6
         return rc;
     const cudaError_t e = moe_combine_backward_launch(dy, lddy, rows, ldr, weights, position, drows, lddr, dweights, T,
                                                       k, K, dtype, d, stream);
+    return e == cudaSuccess ? KP_OK : cuda_failed(e, fn);
+}
+
+int kp_layer_norm(const void *x, int64_t ldx, const void *weight, const void *bias, void *y, int64_t ldy, float *mean,
+                  float *rstd, int T, int K, float eps, int center, int dtype, kp_stream_t stream) {
+    const char *fn = "kp_layer_norm";
+    int rc = check_norm(fn, T, K, dtype);
+    if (rc) return rc;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return set_error(KP_EINVAL, "%s: eps must be finite and not negative", fn);
+    if (T == 0) return KP_OK;
+    if ((rc = check_matrix(fn, "x", x, ldx, K, dtype)) || (rc = check_matrix(fn, "y", y, ldy, K, dtype)) ||
+        (rc = check_matrix(fn, "weight", weight, K, K, dtype)) ||
+        (bias && (rc = check_matrix(fn, "bias", bias, K, K, dtype))) || (mean && (rc = check_ints(fn, "mean", mean))) ||
+        (rstd && (rc = check_ints(fn, "rstd", rstd))))
+        return rc;
+    FfnDev d;
+    if ((rc = ffn_device(&d))) return rc;
+    NormArgs a;
+    a.x = x;
+    a.ldx = ldx;
+    a.w = weight;
+    a.b = bias;
+    a.y = y;
+    a.ldy = ldy;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.T = T;
+    a.K = K;
+    a.eps = eps;
+    a.center = center != 0;
+    a.dtype = dtype;
+    const cudaError_t e = norm_launch(a, stream);
+    return e == cudaSuccess ? KP_OK : cuda_failed(e, fn);
+}
+
+int kp_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *weight,
+                           const float *mean, const float *rstd, void *dx, int64_t lddx, void *dweight, void *dbias,
+                           int T, int K, int dtype, void *work, size_t work_bytes, kp_stream_t stream) {
+    const char *fn = "kp_layer_norm_backward";
+    int rc = check_norm(fn, T, K, dtype);
+    if (rc || (rc = check_matrix(fn, "dweight", dweight, K, K, dtype)) ||
+        (dbias && (rc = check_matrix(fn, "dbias", dbias, K, K, dtype))))
+        return rc;
+    FfnDev d;
+    const size_t row = static_cast<size_t>(K) * (dtype == KP_FP32 ? 4 : 2);
+    if (T == 0) {   // no rows: the weights' gradients are zero
+        if ((rc = ffn_device(&d))) return rc;
+        cudaError_t e = cudaMemsetAsync(dweight, 0, row, stream);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, row, stream);
+        return e == cudaSuccess ? KP_OK : cuda_failed(e, fn);
+    }
+    if ((rc = check_matrix(fn, "dy", dy, lddy, K, dtype)) || (rc = check_matrix(fn, "x", x, ldx, K, dtype)) ||
+        (rc = check_matrix(fn, "weight", weight, K, K, dtype)) || (rc = check_matrix(fn, "dx", dx, lddx, K, dtype)) ||
+        (mean && (rc = check_ints(fn, "mean", mean))) || (rc = check_ints(fn, "rstd", rstd)) || (rc = ffn_device(&d)) ||
+        (rc = check_workspace(fn, work, work_bytes, norm_backward_scratch(T, K, d.sms))))
+        return rc;
+    NormArgs a;
+    a.x = x;
+    a.ldx = ldx;
+    a.w = weight;
+    a.dy = dy;
+    a.lddy = lddy;
+    a.y = dx;
+    a.ldy = lddx;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.dw = dweight;
+    a.dbias = dbias;
+    a.part = static_cast<float *>(work);
+    a.T = T;
+    a.K = K;
+    a.center = mean != nullptr;
+    a.dtype = dtype;
+    const cudaError_t e = norm_backward_launch(a, d, stream);
     return e == cudaSuccess ? KP_OK : cuda_failed(e, fn);
 }
 

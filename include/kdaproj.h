@@ -420,7 +420,7 @@ KP_API int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, in
 /* ---------------------------------------------------------------------------
  * Mixture-of-experts operators: the router, the tokens' rows on their way to their
  * experts and back, and products grouped by expert, each with its gradients. A layer is
- *   kp_moe_route -> kp_moe_dispatch -> kp_grouped_gated_ffn -> kp_grouped_gemm ->
+ *   kp_layer_norm -> kp_moe_route -> kp_moe_dispatch -> kp_grouped_gated_ffn -> kp_grouped_gemm ->
  *   kp_moe_combine.
  *
  * Common to all of them, as to the feed-forward operators: matrices are row-major with
@@ -441,10 +441,28 @@ KP_API int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, in
 
 enum kp_moe_op {
     KP_MOE_ROUTE = 0,            /* M tokens, N experts, top K */
-    KP_MOE_GATED_BACKWARD = 1    /* M rows, N features, K columns */
+    KP_MOE_GATED_BACKWARD = 1,   /* M rows, N features, K columns */
+    KP_MOE_NORM_BACKWARD = 2     /* M rows, K columns (N: 1) */
 };
 /* Bytes of `work`, on the current device. */
 KP_API int kp_moe_workspace(int op, int M, int N, int K, size_t *bytes);
+
+/* Layer norm, in front of a router or a projection: y[t] = round( (x[t] - mean) rstd weight
+ * + bias ), rstd = 1 / sqrt(mean((x[t] - mean)^2) + eps); with center 0 (root-mean-square
+ * norm) the mean counts as 0. x, y [T, K], weight, bias [K] (bias may be NULL) all of dtype
+ * KP_BF16, KP_FP16 or KP_FP32, aligned to their elements; K at most 16384. mean and rstd
+ * [T] fp32 receive the rows' statistics for the backward pass; either may be NULL. */
+KP_API int kp_layer_norm(const void *x, int64_t ldx, const void *weight, const void *bias, void *y, int64_t ldy,
+                         float *mean, float *rstd, int T, int K, float eps, int center, int dtype,
+                         kp_stream_t stream);
+/* Its gradients, with xhat = (x - mean) rstd and g = dy weight: dx = round( rstd (g - mean(g) -
+ * xhat mean(g xhat)) ), dweight = round( sum_t dy xhat ), dbias = round( sum_t dy ) (dbias may
+ * be NULL). mean NULL: the norm without centring, whose dx has no mean(g). With T = 0
+ * dweight and dbias are set to zero. */
+KP_API int kp_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *weight,
+                                  const float *mean, const float *rstd, void *dx, int64_t lddx, void *dweight,
+                                  void *dbias, int T, int K, int dtype, void *work, size_t work_bytes,
+                                  kp_stream_t stream);
 
 /* Scores that the weights are taken from: softmax over the experts, or each expert's
  * 1 / (1 + e^-logit). */

@@ -198,6 +198,30 @@ def test_layer_function_gradients():
         assert err < 8 * 2.0 ** -8, (name, err)
 
 
+def test_layer_behind_a_norm_gradients():
+    """y = x + layer(norm(x)), with its norm's weight, against automatic differentiation."""
+    x, dy, *weights = layer(5, T=50, E=4)
+    gamma = normal(264, seed=77, dtype=torch.bfloat16, std=0.2) + 1
+    y, saved = cli.norm_moe_layer(x, gamma, *weights, top_k=2, save=True)
+    assert torch.equal(cli.norm_moe_layer(x, gamma, *weights, top_k=2)[0], y)
+    got = cli.norm_moe_layer_backward(dy, x, gamma, *weights, saved=saved)
+    ops = [t.double().requires_grad_() for t in (x, gamma, *weights)]
+    xd, cd, rd, gd, ud, dd = ops
+    z = xd / torch.sqrt((xd * xd).mean(dim=1, keepdim=True) + 1e-5) * cd
+    ids = saved[2][1].ids.long()
+    w = torch.softmax((z @ rd.t()).gather(1, ids), dim=1)
+    ref = xd
+    for j in range(2):
+        e = ids[:, j]
+        a = torch.nn.functional.silu(torch.einsum("tk,tfk->tf", z, gd[e]))
+        ref = ref + w[:, j:j + 1] * torch.einsum("tf,tkf->tk", a * torch.einsum("tk,tfk->tf", z, ud[e]), dd[e])
+    ref.backward(dy.double())
+    # as above, with the norm's roundings
+    for name, a, b in zip(("y", "dx", "dgamma", "dWr", "dWg", "dWu", "dWd"), (y, *got), (ref.detach(), *(t.grad for t in ops))):
+        err = float((a.double() - b).norm() / b.norm())
+        assert err < 10 * 2.0 ** -8, (name, err)
+
+
 def test_command_trains_and_serves(capsys):
     cli.main(["--moe", "--M", "1", "37", "--experts", "6", "--top-k", "2", "--F", "136", "--K", "264", "--steps", "2",
               "--reps", "2"])

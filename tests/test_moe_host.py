@@ -87,6 +87,50 @@ def test_rows_argument_errors(lib):
     assert back(lddy=7) == EINVAL and back(lddr=7) == EINVAL and back(K=-1) == EINVAL
 
 
+def test_norm_argument_errors(lib):
+    def norm(x=P, ldx=8, weight=P, bias=None, y=P, ldy=8, mean=None, rstd=None, T=1, K=8, eps=1e-5, center=1, dtype=0):
+        return lib.kp_layer_norm(x, ldx, weight, bias, y, ldy, mean, rstd, T, K, eps, center, dtype, None)
+
+    assert norm(T=0) == OK
+    assert norm(T=-1) == EINVAL and norm(K=0) == EINVAL and norm(dtype=3) == EINVAL
+    assert norm(K=16385, ldx=16385, ldy=16385) == ESHAPE
+    assert norm(eps=-1.0) == EINVAL and norm(eps=float("nan")) == EINVAL and norm(eps=float("inf")) == EINVAL
+    assert norm(x=None) == EINVAL and norm(x=ODD) == EALIGN and norm(ldx=7) == EINVAL and norm(y=None) == EINVAL
+    assert norm(x=ctypes.c_void_p(258), dtype=2) == EALIGN
+    assert norm(weight=None) == EINVAL and norm(bias=ODD) == EALIGN and norm(mean=ODD) == EALIGN and norm(rstd=ODD) == EALIGN
+
+    def back(dy=P, lddy=8, x=P, ldx=8, weight=P, mean=P, rstd=P, dx=P, lddx=8, dweight=P, dbias=None, T=1, K=8, dtype=0):
+        return lib.kp_layer_norm_backward(dy, lddy, x, ldx, weight, mean, rstd, dx, lddx, dweight, dbias, T, K, dtype,
+                                          None, 0, None)
+
+    assert back(T=-1) == EINVAL and back(K=20000, ldx=20000, lddy=20000, lddx=20000) == ESHAPE and back(dtype=-1) == EINVAL
+    assert back(dweight=None) == EINVAL and back(dbias=ODD) == EALIGN
+    assert back(dy=None) == EINVAL and back(lddy=4) == EINVAL and back(x=ODD) == EALIGN and back(dx=None) == EINVAL
+    assert back(rstd=None) == EINVAL and back(mean=ODD) == EALIGN and back(weight=None) == EINVAL
+
+
+def test_norm_refusals(library):  # noqa: F811
+    x, w, f = on(5, 24), on(24), on(5, dtype=torch.float32)
+    binding.layer_norm(x, w, on(24), save=True)
+    binding.layer_norm_backward(on(5, 24), x, w, None, f, bias=True)
+    assert [c for c in library.calls if not c.endswith("workspace")] == ["kp_layer_norm", "kp_layer_norm_backward"]
+    library.calls.clear()
+    for call, error in ((lambda: binding.layer_norm(on(5, 24, dtype=torch.int32), w), TypeError),
+                        (lambda: binding.layer_norm(x, on(23)), ValueError),
+                        (lambda: binding.layer_norm(x, on(24, dtype=torch.float32)), TypeError),
+                        (lambda: binding.layer_norm(x, w, on(24, 1)), ValueError),
+                        (lambda: binding.layer_norm(x, w, y=on(5, 23)), ValueError),
+                        (lambda: binding.layer_norm(on(24, 5).t(), w), ValueError),
+                        (lambda: binding.layer_norm(x, w, stream=StreamOf(1)), ValueError),
+                        (lambda: binding.layer_norm_backward(on(5, 23), x, w, f, f), ValueError),
+                        (lambda: binding.layer_norm_backward(on(5, 24, dtype=torch.float16), x, w, f, f), TypeError),
+                        (lambda: binding.layer_norm_backward(on(5, 24), x, w, on(5), f), TypeError),
+                        (lambda: binding.layer_norm_backward(on(5, 24), x, w, f, on(4, dtype=torch.float32)), ValueError)):
+        with pytest.raises(error):
+            call()
+    assert library.calls == []
+
+
 def test_grouped_argument_errors(lib):
     def gemm(x=P, ldx=16, W=P, ldw=16, sw=128, y=P, ldy=8, offsets=P, R=1, E=3, N=8, K=16, dtype=0):
         return lib.kp_grouped_gemm(x, ldx, W, ldw, sw, y, ldy, offsets, R, E, N, K, dtype, None)
