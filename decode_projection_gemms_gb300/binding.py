@@ -792,8 +792,6 @@ def _experts(W, name: str, dtype, index: int):
     if W.dim() != 3:
         raise ValueError(f"{name} must be a 3-D tensor [experts, features, columns]")
     E, rows, cols = W.shape
-    if W.is_contiguous() and cols & 7 == 0:
-        return cols, rows * cols
     se, ld, inner = W.stride()
     if rows <= 1:   # the stride of a single row, and of a single expert, says nothing
         ld = (cols + 7) // 8 * 8
@@ -977,6 +975,9 @@ def moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, route: MoeR
 
 def _half_rows(t, name: str, rows: int, index: int, dtype=None) -> int:
     """Check a 16-bit matrix with that many rows; returns its row stride."""
+    if type(t) is torch.Tensor and t.dtype in _DTYPES and (dtype is None or t.dtype is dtype) and t.dim() == 2 \
+            and t.shape[0] == rows and t.get_device() == index and t.is_contiguous():
+        return t.shape[1]
     ld = _rows(t, name, dtype, index)
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
@@ -1066,6 +1067,15 @@ def _grouped_operands(x, W, name: str, offsets, index: int):
     dt = x.dtype
     if dt not in _DTYPES:
         raise TypeError(f"x must be bfloat16 or float16, got {dt}")
+    try:   # the common case in a few cheap checks; the rest also to name the problem
+        R, K = x.shape
+        E, N, Kw = W.shape
+        if (K == Kw and K & 7 == 0 and W.dtype is dt and offsets.dtype is torch.int32 and W.get_device() == index
+                and offsets.get_device() == index and x.is_contiguous() and W.is_contiguous()
+                and offsets.shape == (E + 1,) and offsets.is_contiguous()):
+            return R, E, N, K, K, K, N * K, dt, offsets.data_ptr()
+    except (AttributeError, TypeError, ValueError):
+        pass
     ldx = _rows(x, "x", dt, index)
     ldw, sw = _experts(W, name, dt, index)
     R, K = x.shape
@@ -1118,7 +1128,10 @@ def grouped_gemm_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, of
 
 def _grouped_gated_operands(x, Wg, Wu, offsets, index: int):
     R, E, F, K, ldx, ldg, sg, dt, op = _grouped_operands(x, Wg, "Wg", offsets, index)
-    ldu, su = _experts(Wu, "Wu", dt, index)
+    if type(Wu) is torch.Tensor and Wu.dtype is dt and Wu.get_device() == index and Wu.is_contiguous() and K & 7 == 0:
+        ldu, su = K, F * K
+    else:
+        ldu, su = _experts(Wu, "Wu", dt, index)
     if Wu.shape != Wg.shape:
         raise ValueError(f"Wg {tuple(Wg.shape)} and Wu {tuple(Wu.shape)} must have the same shape")
     return R, E, F, K, ldx, ldg, sg, ldu, su, dt, op
