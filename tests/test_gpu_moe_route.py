@@ -40,7 +40,7 @@ def check(logits, k, score, bias=None):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 6), (2, 3, 3), (5, 33, 32), (31, 8, 2), (32, 64, 4), (33, 64, 4),
-                                   (64, 65, 8), (100, 256, 8), (129, 1024, 32), (700, 17, 5), (1025, 384, 8)])
+                                   (64, 65, 8), (64, 1024, 32), (65, 1024, 32), (100, 256, 8), (129, 1024, 32), (700, 17, 5), (1025, 384, 8)])
 def test_route(T, E, k, score, dtype):
     check(normal(T, E, T + E, dtype), k, score)   # 16-bit logits have many ties
 
