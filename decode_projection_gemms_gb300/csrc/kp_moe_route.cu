@@ -8,6 +8,11 @@
 // choices by expert, the counts of the blocks before it are summed, and a pair's row is
 // its expert's first row, plus those of the blocks before, plus the pairs before it
 // within the block. Counts are whole numbers, so nothing depends on timing.
+//
+// Bound: latency for few tokens (one: 4.3 us, in one block that does everything; up to
+// kAllTokens), instructions for many: 16384 tokens, top 8 of 256, sigmoid and bias, fp32 36 us (23
+// without bias), of which the choice 31 (74 % of the issue slots; of its 1000 instructions a token
+// a third are the sigmoids); gradient 6. The bytes would take 8.
 #include <algorithm>
 #include <type_traits>
 
