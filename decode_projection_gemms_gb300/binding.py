@@ -395,6 +395,8 @@ def _rows(t, name: str, dtype, index: int) -> int:
     except ValueError:
         raise ValueError(f"{name} must be a 2-D tensor") from None
     rows, cols = t.shape
+    if (rows | cols) >> 31:   # the library takes sizes as int
+        raise ValueError(f"{name} must have less than 2^31 rows and columns, got {tuple(t.shape)}")
     if rows <= 1:   # the stride of a single row says nothing
         ld = (cols + 7) // 8 * 8
     if ld < cols or (inner != 1 and cols > 1):
@@ -792,6 +794,8 @@ def _experts(W, name: str, dtype, index: int):
     if W.dim() != 3:
         raise ValueError(f"{name} must be a 3-D tensor [experts, features, columns]")
     E, rows, cols = W.shape
+    if (E | rows | cols) >> 31:
+        raise ValueError(f"{name} must have less than 2^31 features and columns, got {tuple(W.shape)}")
     se, ld, inner = W.stride()
     if rows <= 1:   # the stride of a single row, and of a single expert, says nothing
         ld = (cols + 7) // 8 * 8
@@ -976,7 +980,7 @@ def moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, route: MoeR
 def _half_rows(t, name: str, rows: int, index: int, dtype=None) -> int:
     """Check a 16-bit matrix with that many rows; returns its row stride."""
     if type(t) is torch.Tensor and t.dtype in _DTYPES and (dtype is None or t.dtype is dtype) and t.dim() == 2 \
-            and t.shape[0] == rows and t.get_device() == index and t.is_contiguous():
+            and t.shape[0] == rows and not t.shape[1] >> 31 and t.get_device() == index and t.is_contiguous():
         return t.shape[1]
     ld = _rows(t, name, dtype, index)
     if t.dtype not in _DTYPES:
@@ -1070,7 +1074,7 @@ def _grouped_operands(x, W, name: str, offsets, index: int):
     try:   # the common case in a few cheap checks; the rest also to name the problem
         R, K = x.shape
         E, N, Kw = W.shape
-        if (K == Kw and K & 7 == 0 and W.dtype is dt and offsets.dtype is torch.int32 and W.get_device() == index
+        if (K == Kw and K & 7 == 0 and not (R | N | K) >> 31 and W.dtype is dt and offsets.dtype is torch.int32 and W.get_device() == index
                 and offsets.get_device() == index and x.is_contiguous() and W.is_contiguous()
                 and offsets.shape == (E + 1,) and offsets.is_contiguous()):
             return R, E, N, K, K, K, N * K, dt, offsets.data_ptr()

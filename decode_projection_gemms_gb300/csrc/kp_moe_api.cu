@@ -56,19 +56,25 @@ static int check_workspace(const char *fn, const void *work, size_t have, size_t
     if (need && misaligned(work, 256)) return set_error(KP_EALIGN, "%s: the workspace must be 256-byte aligned", fn);
     return KP_OK;
 }
+// Sizes that have the size of a block or a tile added to them in 32 bits.
+static constexpr int kMost = 1 << 30;
+static int check_pairs(const char *fn, int T, int k) {
+    if (static_cast<int64_t>(T) * k > kMost)
+        return set_error(KP_ESHAPE, "%s: %d tokens, top %d: at most 2^30 rows", fn, T, k);
+    return KP_OK;
+}
 static int check_route(const char *fn, int T, int E, int k) {
     if (T < 0 || E < 1 || k < 1 || k > E)
         return set_error(KP_EINVAL, "%s: bad sizes: %d tokens, %d experts, top %d", fn, T, E, k);
     if (E > kMoeMaxExperts || k > kMoeMaxTopK)
         return set_error(KP_ESHAPE, "%s: %d experts, top %d: at most %d and %d", fn, E, k, kMoeMaxExperts, kMoeMaxTopK);
-    if (static_cast<int64_t>(T) * k > 0x7FFFFFFF) return set_error(KP_ESHAPE, "%s: %d x %d rows are too many", fn, T, k);
-    return KP_OK;
+    return check_pairs(fn, T, k);
 }
 static int check_shuffle(const char *fn, int T, int k, int K, int dtype) {
     if (T < 0 || k < 1 || K < 1) return set_error(KP_EINVAL, "%s: bad sizes: %d tokens, top %d, %d columns", fn, T, k, K);
     if (!is16(dtype)) return set_error(KP_EINVAL, "%s: unknown element type %d", fn, dtype);
-    if (static_cast<int64_t>(T) * k > 0x7FFFFFFF) return set_error(KP_ESHAPE, "%s: %d x %d rows are too many", fn, T, k);
-    return KP_OK;
+    if (K > kMost) return set_error(KP_ESHAPE, "%s: %d columns: at most 2^30", fn, K);
+    return check_pairs(fn, T, k);
 }
 static int check_norm(const char *fn, int T, int K, int dtype) {
     if (T < 0 || K < 1) return set_error(KP_EINVAL, "%s: bad sizes: %d rows, %d columns", fn, T, K);
@@ -88,8 +94,7 @@ static int check_grouped(const char *fn, int R, int E, int N, int K, int dtype) 
     if (!is16(dtype)) return set_error(KP_EINVAL, "%s: unknown element type %d", fn, dtype);
     if (E > kMoeMaxExperts) return set_error(KP_ESHAPE, "%s: %d experts: at most %d", fn, E, kMoeMaxExperts);
     if (K & 7) return set_error(KP_ESHAPE, "%s: K=%d is not a multiple of 8", fn, K);
-    // (tiles reach past the end by less than their size, in 32 bits)
-    if (R > (1 << 30) || N > (1 << 30) || K > (1 << 30))
+    if (R > kMost || N > kMost || K > kMost)
         return set_error(KP_ESHAPE, "%s: %d rows, %d features, %d columns: at most 2^30", fn, R, N, K);
     return KP_OK;
 }

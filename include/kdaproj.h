@@ -437,7 +437,7 @@ KP_API int kp_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, in
  * (E + 1 ascending numbers from 0 to at most R); rows from offsets[E] on belong to
  * nobody. The grouped products take any such offsets, whoever made them; they lie in
  * device memory, so they are not checked, but no value of theirs leads outside [0, R).
- * The grouped products take at most 2^30 rows, features and columns. */
+ * The mixture-of-experts operators take at most 2^30 rows (pairs), features and columns. */
 
 enum kp_moe_op {
     KP_MOE_ROUTE = 0,            /* M tokens, N experts, top K */

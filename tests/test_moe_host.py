@@ -44,6 +44,7 @@ def test_route_argument_errors(lib):
     assert call(logits=None) == EINVAL and call(logits=ODD) == EALIGN
     assert call(logits=ctypes.c_void_p(258), dtype=2) == EALIGN
     assert call(ld=7) == EINVAL
+    assert call(T=2 ** 31 - 1, k=1) == ESHAPE                      # sums of a size and a block's pass 32 bits
     for name in ("ids", "weights", "offsets", "order", "position"):
         assert call(**{name: None}) == EINVAL and call(**{name: ODD}) == EALIGN
     assert call(T=1000) == EINVAL                                  # no workspace
@@ -66,6 +67,7 @@ def test_rows_argument_errors(lib):
     assert dispatch(T=0) == OK
     assert dispatch(T=-1) == EINVAL and dispatch(k=0) == EINVAL and dispatch(K=0) == EINVAL and dispatch(dtype=2) == EINVAL
     assert dispatch(T=2 ** 30) == ESHAPE
+    assert dispatch(K=2 ** 31 - 1, ldx=2 ** 31, ldr=2 ** 31) == ESHAPE
     assert dispatch(x=None) == EINVAL and dispatch(x=ODD) == EALIGN and dispatch(ldx=7) == EINVAL
     assert dispatch(rows=None) == EINVAL and dispatch(ldr=7) == EINVAL and dispatch(position=ODD) == EALIGN
 
@@ -75,6 +77,7 @@ def test_rows_argument_errors(lib):
     assert combine(T=0) == OK
     assert combine(T=-1) == EINVAL and combine(dtype=2) == EINVAL
     assert combine(rows=ODD) == EALIGN and combine(y=None) == EINVAL and combine(weights=ODD) == EALIGN
+    assert combine(K=2 ** 31 - 8, ldr=2 ** 31, ldy=2 ** 31) == ESHAPE
     assert combine(position=None) == EINVAL and combine(ldy=4) == EINVAL
 
     def back(dy=P, lddy=8, rows=P, ldr=8, weights=P, position=P, drows=P, lddr=8, dweights=P, T=1, k=2, K=8, dtype=0):
@@ -85,6 +88,7 @@ def test_rows_argument_errors(lib):
     assert back(dy=None) == EINVAL and back(rows=None) == EINVAL and back(drows=ODD) == EALIGN
     assert back(weights=None) == EINVAL and back(position=None) == EINVAL and back(dweights=ODD) == EALIGN
     assert back(lddy=7) == EINVAL and back(lddr=7) == EINVAL and back(K=-1) == EINVAL
+    assert back(K=2 ** 31 - 8, lddy=2 ** 31, ldr=2 ** 31, lddr=2 ** 31) == ESHAPE
 
 
 def test_norm_argument_errors(lib):
@@ -287,3 +291,29 @@ def test_grouped_refusals(library):  # noqa: F811
         with pytest.raises(error):
             binding.grouped_gated_ffn_backward(dh, p["x"], p["W"], p["W"], p["offsets"], g, u)
     assert library.calls == []
+
+
+def test_sizes_past_32_bits_are_refused(library):  # noqa: F811
+    # the entry points take sizes as int; none may arrive there without its upper bits
+    def huge(*shape, dtype=torch.bfloat16):
+        return OnDevice(torch.empty(shape, dtype=dtype, device="meta"))
+
+    n = 2 ** 32 + 3
+    p = grouped_operands()
+    off = p["offsets"]
+    r = route_of()
+    r.tokens, r.top_k = 3, 1
+    for call in (lambda: binding.layer_norm(huge(n, 8), on(8)), lambda: binding.moe_route(huge(n, 8), 2),
+                 lambda: binding.moe_dispatch(huge(3, n), r), lambda: binding.moe_combine(huge(3, n), r),
+                 lambda: binding.grouped_gemm(huge(n, 24), p["W"], off),
+                 lambda: binding.grouped_gemm(p["x"], huge(3, n, 24), off),
+                 lambda: binding.grouped_gemm(huge(5, n + 5), huge(3, 16, n + 5), off)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    assert library.calls == []
+    plain = torch.empty((3, n), dtype=torch.bfloat16, device="meta")   # what the quick checks take
+    with pytest.raises(ValueError, match="2\\^31"):
+        binding._half_rows(plain, "x", 3, plain.get_device())
+    x, W = plain[:, :24].contiguous(), torch.empty((3, n, 24), dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        binding._grouped_operands(x, W, "W", torch.zeros(4, dtype=torch.int32, device="meta"), x.get_device())
