@@ -58,6 +58,29 @@ def test_grouped_gemm(name, N, K, dtype):
     quiet()
 
 
+# experts are looked up 32 at a time: the edges of that, runs without rows, several tiles an expert
+@pytest.mark.parametrize("n", [[1] * 31, [1] * 32, [1] * 33, [0] * 31 + [3], [0] * 32 + [3], [0] * 33 + [3], [3] + [0] * 64,
+                               [2] + [0] * 31 + [1], [0] * 64 + [5] + [0] * 31 + [300], [17] * 65,
+                               [1] + [0] * 40 + [600] + [0] * 31 + [7], [0, 1] * 100, [0] * 1023 + [2]],
+                         ids=lambda n: f"{len(n)}x{sum(n)}")
+def test_many_experts(n):
+    off = torch.tensor([0] + n, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    R, E, N, K = int(off[-1]) + 2, len(n), 264, 72
+    x, W = normal(R, K, seed=1, dtype=torch.bfloat16), normal(E, N, K, seed=2, dtype=torch.bfloat16, std=0.1)
+    dy = normal(R, N, seed=3, dtype=torch.bfloat16, std=0.05)
+    x[-2:], dy[-2:] = math.nan, math.inf
+    y = torch.full((R, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    kda.grouped_gemm(x, W, off, y=y)
+    ref, bound = grouped(x, W, off)
+    close(y[:-2], ref[:-2], bound[:-2], "y")
+    assert (y[-2:] == 3.0).all()
+    dx, dW = kda.grouped_gemm_backward(dy, x, W, off)
+    ref = grouped_grads(dy, x, W, off)
+    close(dx[:-2], ref["dx"][0][:-2], ref["dx"][1][:-2], "dx")
+    close(dW, *ref["dW"], "dW")
+    quiet()
+
+
 @pytest.mark.parametrize("dtype", HALF)
 @pytest.mark.parametrize("N,K", [(8, 8), (40, 64), (136, 72), (264, 320), (520, 1032)])
 @pytest.mark.parametrize("name", sorted(GROUPS))
