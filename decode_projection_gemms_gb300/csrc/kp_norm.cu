@@ -4,14 +4,15 @@
 // (without centring: mean and mean(g) are 0, root-mean-square norm).
 //
 // A row is read once and stays in the registers of a team of warps, so that the squares are
-// summed around the mean that was found first: no difference of two large sums. All sums
-// are fp32. Backward, a block takes rows b, b + blocks, ... and a thread keeps the same
+// summed around the mean that was found first: no difference of two large sums. The gradients
+// start from x - mean too: x rstd - mean rstd is a rounding of mean rstd off for a whole row
+// (rows of 1e5 +- 1 in fp32: 8e-4 on every xhat, which adds up in dw). All sums are fp32. Backward, a block takes rows b, b + blocks, ... and a thread keeps the same
 // columns, whose dw and db it adds up in registers; the blocks' sums go to a workspace and a
 // second kernel adds them in order, so nothing depends on timing.
 //
 // Bound: HBM forward (8192 x 7168 bf16: 39 us, 6.0 TB/s; 16384 x 4096 6.5). Backward the
 // instructions, about 28 an element of which a row's sums and addresses are 10, and the wait for
-// the row's sums: 83 us, 4.2 TB/s. What it took to get there from 139: rows ahead through shared
+// the row's sums: 84 us, 4.2 TB/s. What it took to get there from 139: rows ahead through shared
 // memory, a block's teams' sums joined in it (a block's sums cost as much memory as four rows), the
 // two sums of a row halved between the lanes, the next row's statistics read beforehand.
 #include <algorithm>
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(32 * W * teams_of(W), 32 / (W * teams_of(W)))
     float next_mean = p.center && first < p.T ? __ldg(p.mean + first) : 0.f;
     for (int64_t t = first; t < p.T; t += step, dx += ystep) {
         const T *x = static_cast<const T *>(p.x) + t * p.ldx, *dy = static_cast<const T *>(p.dy) + t * p.lddy;   // (no ring)
-        const float rstd = next_rstd, shift = -next_mean * rstd;
+        const float rstd = next_rstd, mean = next_mean;
         if (t + step < p.T) {
             next_rstd = __ldg(p.rstd + t + step);
             if (p.center) next_mean = __ldg(p.mean + t + step);
@@ -356,10 +357,11 @@ __global__ void __launch_bounds__(32 * W * teams_of(W), 32 / (W * teams_of(W)))
             Piece<T> xp, dp, wp;
             piece(i, c, xp, dp);
             wp.load(static_cast<const T *>(p.w), c, p.K, kRing);
+            // (x is widened here: with the mixed-precision sum 8192 x 12288 bf16 takes 174 us instead of 162)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (!kRing && c + j >= p.K) break;
-                const float xh = fmaf(xp[j], rstd, shift), g = dp.mul_add(j, wp, 0.f);
+                const float xh = (xp[j] - mean) * rstd, g = dp.mul_add(j, wp, 0.f);
                 dw[i][j] = fmaf(dp[j], xh, dw[i][j]);
                 sum[0] += g;
                 sum[1] = fmaf(g, xh, sum[1]);
@@ -369,9 +371,9 @@ __global__ void __launch_bounds__(32 * W * teams_of(W), 32 / (W * teams_of(W)))
                 for (int j = 0; j < 8; ++j) db[i][j] = dp.add(j, db[i][j]);   // zeros past K
         }
         team_sum2<W>(sum, sh[team], turn, team);
-        // rstd (g - a - xhat m) = g rstd + x (-rstd^2 m) + (-rstd a - shift rstd m)
-        const float a = p.center ? sum[0] / static_cast<float>(p.K) : 0.f, m = sum[1] / static_cast<float>(p.K);
-        const float slope = -rstd * m * rstd, offset = -rstd * fmaf(shift, m, a);
+        // rstd (g - a - xhat m), with xhat m = (x - mean) (rstd m)
+        const float a = p.center ? sum[0] / static_cast<float>(p.K) : 0.f;
+        const float slope = -rstd * (sum[1] / static_cast<float>(p.K));
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = (i * kLanes + lane) * 8;
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(32 * W * teams_of(W), 32 / (W * teams_of(W)))
             wp.load(static_cast<const T *>(p.w), c, p.K, kRing);
             float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = fmaf(dp.mul_add(j, wp, 0.f), rstd, fmaf(xp[j], slope, offset));
+            for (int j = 0; j < 8; ++j) f[j] = fmaf(xp[j] - mean, slope, dp.mul_add(j, wp, -a)) * rstd;
             store8(dx, c, p.K, kRing, f);
         }
         if (++s == kAhead + 1) s = 0;
