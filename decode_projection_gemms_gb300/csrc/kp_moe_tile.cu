@@ -114,13 +114,22 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// Behind writes to this CTA's own shared memory, on a barrier of either (shared::cluster
-// address): they are complete before the arrival leaves. (A release at cluster scope takes
-// 890 cycles, this one 40.)
-__device__ __forceinline__ void remote_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Behind writes to this CTA's shared memory that a thread of either CTA hands to its MMAs,
+// on that thread's barrier (shared::cluster address). Cluster scope on both sides, since
+// they may be two CTAs: one that ends at the CTA orders nothing between them. (890 cycles
+// instead of 40, while the stages before it are still in the MMAs' queue.)
+__device__ __forceinline__ void remote_arrive_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same where no write has to be seen behind it. (A releasing arrival waits for the
+// The other side: once the phase has been waited for.
+__device__ __forceinline__ void acquire_cluster(uint32_t bar, uint32_t parity) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(parity)
+        : "memory");
+}
+// An arrival that no write has to be seen behind. (A releasing arrival waits for the
 // stores before it: an epilogue that gives its accumulator back after a tile's stores, or a
 // copying warp at every stage, then lags behind by their latency.)
 __device__ __forceinline__ void remote_arrive_relaxed(uint32_t bar) {
@@ -485,8 +494,6 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
             const bool mine = elect_one();
             int stage = 0, as = 0;
             uint32_t phase = 0, aphase = 1;
-            // (Rows that warp 10 clears are handed to the asynchronous proxy by its own fence;
-            // this thread reads nothing of them.)
             auto prepare = [&](int s, uint32_t ph) {
                 mbar_wait_bounded(smem_u32(full + s), ph, abort_flag, p.err, DEV_TIMEOUT_FULL);
                 tc_fence_after();
@@ -509,6 +516,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
                 const uint32_t idesc = p.idesc | static_cast<uint32_t>(it.nt >> 3) << 17 | (dw ? 1u << 16 : 0u);
                 const int depth = dw ? count[it.e] : p.K;
                 const uint32_t bstep = dw ? 128 : 2;
+                const int clear = dw && (depth & 15) ? it.kb - 1 : -1;   // warp 10 clears rows in this block
                 mbar_wait_bounded(smem_u32(acce + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
                 tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(as) * 256;
@@ -517,6 +525,12 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
                     const uint64_t ad = kBack ? desc_mn(st) : desc_kmajor(st);
                     const uint64_t bd = dw ? desc_mn(st + kHalf) : desc_kmajor(st + kHalf);
                     const uint32_t bar = smem_u32(empty + stage);
+                    // (here and not in every block's wait: dx and dW of 512 rows on each of 16 180.4
+                    // us instead of 182.4; those rows reach the asynchronous proxy by warp 10's fence)
+                    if (kBack && __builtin_expect(kb == clear, 0)) {
+                        acquire_cluster(smem_u32(full + stage), phase);
+                        tc_fence_after();
+                    }
                     const int at = kBack && !dw && kb >= p.KB ? kb - p.KB : kb;
                     const int steps = min(4, (depth - at * 64 + 15) >> 4);
                     auto mma = [&](int kk) {
@@ -674,7 +688,7 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
             // the tensor cores read them through the asynchronous proxy
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) remote_arrive(full0 + 8 * s);
+            if (lane == 0) remote_arrive_release(full0 + 8 * s);
         }
         __syncwarp();
     }
