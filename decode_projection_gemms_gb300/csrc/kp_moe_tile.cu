@@ -246,6 +246,11 @@ __host__ __device__ __forceinline__ float tile_cycles(float nt, float kb) {
     return fmaxf(kb * block, 800.f + 18.f * nt) + 1500.f;
 }
 
+// Limit of a wait that `blocks` K blocks of the CTA's own products may lie behind: 1 s, and
+// 4 us a block, which takes 0.2 to 0.6 of one. (An expert's 2^29 rows contracted by one
+// cluster are 2^23 blocks, 2.2 s.)
+__device__ __forceinline__ uint64_t wait_limit_ns(uint64_t blocks) { return 1000000000ull + 4000ull * blocks; }
+
 template <int kForm>
 __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kThreads, 1) __cluster_dims__(2, 1, 1)
     grouped_kernel(const __grid_constant__ GroupedMaps tm, const GroupedParams p) {
@@ -579,7 +584,8 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
                     put_box<32>(dst + c * ldy, ldy, box, m, p.M, it.rows - c, lane, vec);
                 continue;
             }
-            mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL);
+            mbar_wait_bounded(smem_u32(accf + as), aphase, abort_flag, p.err, DEV_TIMEOUT_ACC_FULL,
+                              wait_limit_ns(it.kb));
             tc_fence_after();
             const uint32_t t = tmem + static_cast<uint32_t>(as) * 256 + (static_cast<uint32_t>(q * 32) << 16);
             for (int c = 32 * half; c < it.nt; c += 64) {
@@ -666,16 +672,18 @@ __global__ void __launch_bounds__(kForm == GROUPED_BACKWARD ? kThreadsBack : kTh
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);
         uint32_t seen = 0;   // phases of `ends`, a bit a stage
         int end = 0;         // the stage behind the last one of the item before
+        uint64_t behind = 0; // K blocks since the last wait
         Item it = {};
         for (int i = 0; get(i, it); ++i) {
             const int left = count[it.e] & 15;
             end = (end + it.kb) % S;
+            behind += it.kb + 8;   // and an item's way out
             if (!it.z || !it.kb || !left) continue;
             const int s = end ? end - 1 : S - 1;
-            // This warp has nothing to do while dx is computed, which may take its time: it gives
-            // up by itself after 100 s only, but at once when another wait of the CTA did, and
-            // those go with the stages.
-            mbar_wait_bounded(smem_u32(ends + s), (seen >> s) & 1, abort_flag, p.err, DEV_TIMEOUT_FULL, 100000000000ull);
+            // (this warp has nothing to do while dx is computed)
+            mbar_wait_bounded(smem_u32(ends + s), (seen >> s) & 1, abort_flag, p.err, DEV_TIMEOUT_FULL,
+                              wait_limit_ns(behind));
+            behind = 0;
             seen ^= 1u << s;
             const int r0 = count[it.e] & 63, n = 16 - left;      // K rows r0 .. r0 + n - 1 of every 8 KB group
             const int groups = 2 + (it.nt >> 7);

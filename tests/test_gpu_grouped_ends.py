@@ -43,3 +43,25 @@ def test_every_remainder_again_and_again(N, K, dtype):
         assert torch.isnan(dW[1::2]).all() and torch.isnan(dx[bad]).all()
     torch.cuda.synchronize()
     assert binding.device_error() == 0
+
+
+def test_a_contraction_of_more_than_a_second():
+    """2^29 rows of one expert, which a single cluster contracts to its dW in 2.2 s: longer than
+    the kernels' other waits last."""
+    R, N, K, dt = 2 ** 29, 8, 8, torch.bfloat16
+    off = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    x, dy = torch.zeros((R, K), dtype=dt, device="cuda"), torch.zeros((R, N), dtype=dt, device="cuda")
+    W = normal(1, N, K, seed=1, dtype=dt)
+    at = torch.tensor([0, 1, 77, 2 ** 28 - 1, 2 ** 28, R - 64, R - 1], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for t in (x, dy):
+        t[at] = torch.randint(-3, 4, (len(at), 8), generator=g, device="cuda").to(dt)
+    dx, dW = kda.grouped_gemm_backward(dy, x, W, off)
+    torch.cuda.synchronize()
+    assert binding.device_error() == 0
+    assert torch.equal(dW[0].double(), dy[at].double().t() @ x[at].double())      # whole numbers below 256
+    want = dy[at].double() @ W[0].double()
+    # eight products summed in fp32, rounded to bf16
+    tol = 2.0 ** -21 * (dy[at].double().abs() @ W[0].double().abs())
+    assert ((dx[at].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all()
+    assert int(torch.count_nonzero(dx)) <= 8 * len(at)
