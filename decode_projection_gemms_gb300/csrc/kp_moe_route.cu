@@ -14,6 +14,7 @@
 // without bias), of which the choice 31 (74 % of the issue slots; of its 1000 instructions a token
 // a third are the sigmoids); gradient 6. The bytes would take 8.
 #include <algorithm>
+#include <mutex>
 #include <type_traits>
 
 #include "kp_moe.cuh"
@@ -423,6 +424,16 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// Shared memory of a block that places `slots` choices: base, the scan's sums, and each
+// warp's counts by expert.
+size_t place_smem(int threads, int E, int64_t slots) {
+    const int warps = static_cast<int>(std::min<int64_t>((slots + 31) / 32, threads / 32));
+    return (static_cast<size_t>(E) * (1 + warps) + threads / 32) * sizeof(int32_t);
+}
+
+std::mutex g_mu;
+bool g_ready[64];   // devices whose kernels of one block have their shared memory raised
+
 int blocks_of(int T) { return T <= kAllTokens ? 1 : (T + kTokens - 1) / kTokens; }
 
 }  // namespace
@@ -432,44 +443,51 @@ size_t moe_route_scratch(int T, int E) {
     return b > 1 ? (static_cast<size_t>(b) + 1) * E * sizeof(int32_t) : 0;
 }
 
-cudaError_t moe_route_launch(const MoeRouteArgs &a, const FfnDev &, cudaStream_t s) {
+cudaError_t moe_route_launch(const MoeRouteArgs &a, const FfnDev &d, cudaStream_t s) {
     using Fn = void (*)(RouteParams);
-    auto pick = [&](auto all) -> Fn {
+    auto pick = [](auto all, bool bias, int v) -> Fn {   // of 32 << v experts
         constexpr bool kAll = decltype(all)::value;
         static const Fn kernels[2][6] = {
             {route_kernel<1, false, kAll>, route_kernel<2, false, kAll>, route_kernel<4, false, kAll>,
              route_kernel<8, false, kAll>, route_kernel<16, false, kAll>, route_kernel<32, false, kAll>},
             {route_kernel<1, true, kAll>, route_kernel<2, true, kAll>, route_kernel<4, true, kAll>,
              route_kernel<8, true, kAll>, route_kernel<16, true, kAll>, route_kernel<32, true, kAll>}};
-        int v = 0;
-        while (32 << v < a.E) ++v;
-        return kernels[a.bias != nullptr][v];
+        return kernels[bias][v];
     };
+    const bool bias = a.bias != nullptr;
+    int v = 0;
+    while (32 << v < a.E) ++v;
     RouteParams p;
     p.a = a;
     p.blocks = blocks_of(a.T);
     p.counts = static_cast<int32_t *>(a.work);
     p.totals = p.blocks > 1 ? p.counts + static_cast<int64_t>(p.blocks) * a.E : nullptr;
-    // base, the scan's sums, and each warp's counts by expert
-    auto place = [&](int threads, int64_t slots) {
-        const int warps = static_cast<int>(std::min<int64_t>((slots + 31) / 32, threads / 32));
-        return (static_cast<size_t>(a.E) * (1 + warps) + threads / 32) * sizeof(int32_t);
-    };
     if (p.blocks == 1) {
-        const size_t smem = place(kAllThreads, static_cast<int64_t>(a.T) * a.k);
-        Fn f = pick(std::true_type());
+        const size_t smem = place_smem(kAllThreads, a.E, static_cast<int64_t>(a.T) * a.k);
         if (smem > 48 * 1024) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
+            // once, to the most that a kernel may need: a limit set for this call would be
+            // lowered by a call with fewer tokens on another thread before this one's launch
+            std::lock_guard<std::mutex> lk(g_mu);
+            if (d.dev >= 64 || !g_ready[d.dev]) {
+                for (int i = 0; 32 << i <= kMoeMaxExperts; ++i) {
+                    const size_t most = place_smem(kAllThreads, 32 << i, kAllTokens * kMoeMaxTopK);
+                    for (const bool b : {false, true}) {
+                        if (most <= 48 * 1024) continue;
+                        const cudaError_t e = cudaFuncSetAttribute(pick(std::true_type(), b, i), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                                   static_cast<int>(most));
+                        if (e != cudaSuccess) return e;
+                    }
+                }
+                if (d.dev < 64) g_ready[d.dev] = true;
+            }
         }
-        f<<<1, kAllThreads, smem, s>>>(p);
+        pick(std::true_type(), bias, v)<<<1, kAllThreads, smem, s>>>(p);
         return cudaGetLastError();
     }
-    pick(std::false_type())<<<p.blocks, kChoosers, a.E * sizeof(int32_t), s>>>(p);
+    pick(std::false_type(), bias, v)<<<p.blocks, kChoosers, a.E * sizeof(int32_t), s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const size_t smem = place(kPlacers, static_cast<int64_t>(kTokens) * a.k);
+    const size_t smem = place_smem(kPlacers, a.E, static_cast<int64_t>(kTokens) * a.k);
     if (p.blocks > kSumBlocks) {
         route_scan_kernel<<<(a.E + kScanExperts - 1) / kScanExperts, 1024, 0, s>>>(p);
         route_place_kernel<false><<<p.blocks, kPlacers, smem, s>>>(p);
