@@ -795,7 +795,7 @@ def _experts(W, name: str, dtype, index: int):
         raise ValueError(f"{name} must be a 3-D tensor [experts, features, columns]")
     E, rows, cols = W.shape
     if (E | rows | cols) >> 31:
-        raise ValueError(f"{name} must have less than 2^31 features and columns, got {tuple(W.shape)}")
+        raise ValueError(f"{name} must have less than 2^31 experts, features and columns, got {tuple(W.shape)}")
     se, ld, inner = W.stride()
     if rows <= 1:   # the stride of a single row, and of a single expert, says nothing
         ld = (cols + 7) // 8 * 8
@@ -1074,9 +1074,10 @@ def _grouped_operands(x, W, name: str, offsets, index: int):
     try:   # the common case in a few cheap checks; the rest also to name the problem
         R, K = x.shape
         E, N, Kw = W.shape
-        if (K == Kw and K & 7 == 0 and not (R | N | K) >> 31 and W.dtype is dt and offsets.dtype is torch.int32 and W.get_device() == index
-                and offsets.get_device() == index and x.is_contiguous() and W.is_contiguous()
-                and offsets.shape == (E + 1,) and offsets.is_contiguous()):
+        if (K == Kw and K & 7 == 0 and not (R | E | N | K) >> 31 and W.dtype is dt
+                and offsets.dtype is torch.int32 and W.get_device() == index and offsets.get_device() == index
+                and x.is_contiguous() and W.is_contiguous() and offsets.shape == (E + 1,)
+                and offsets.is_contiguous()):
             return R, E, N, K, K, K, N * K, dt, offsets.data_ptr()
     except (AttributeError, TypeError, ValueError):
         pass
