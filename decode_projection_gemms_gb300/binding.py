@@ -707,7 +707,9 @@ class MoeRoute:
     best ``top_k`` of ``experts`` each. On the device, int32 unless said otherwise:
 
     * ``ids`` [tokens, top_k]: the experts, best first; -1 where there is none;
-    * ``weights`` [tokens, top_k] float32: of their outputs, adding up to 1;
+    * ``weights`` [tokens, top_k] float32: of their outputs, adding up to 1. ``moe_combine`` and
+      both backward passes read them, ``moe_route_backward`` as what the router made: who wants
+      the outputs scaled scales those, not the weights in place;
     * ``offsets`` [experts + 1]: expert e has rows ``offsets[e]`` to ``offsets[e + 1] - 1``;
     * ``order`` [tokens * top_k]: the pair ``token * top_k + slot`` of every row, -1 behind
       the last;
@@ -955,7 +957,7 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: to
 def moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, route: MoeRoute, stream=None) -> torch.Tensor:
     """The gradient of ``moe_route``'s logits (of their type) for the gradient
     ``dweights`` [T, top_k] float32 of its weights: zero but for the chosen experts. A bias
-    has none."""
+    has none. ``route.weights`` have to be as the router made them."""
     index = _here(logits, "logits", stream)
     if index < 0:
         with _on(logits.device, stream, dweights, logits, route):

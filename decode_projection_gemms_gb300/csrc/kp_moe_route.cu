@@ -28,7 +28,11 @@ constexpr int kTokens = 16;      // of a block
 constexpr int kChoosers = 32 * kTokens, kPlacers = 128;   // threads of a block that chooses, that places
 constexpr int kScanExperts = 8;  // of a block that sums counts
 constexpr int kSumBlocks = 32;   // whose counts a block that places sums itself (512 x 256, top 8: 10.9 us, summed before)
-constexpr int kAllThreads = 1024, kAllTokens = 64;   // of the one block that does everything
+// Of the one block that does everything. Up to 64 tokens, since a call from the host then takes 11
+// us instead of 19 (a launch and a workspace less); on the device alone it is behind from 32 on
+// (64 experts, top 6: 5.7 us, 4.9 in several blocks; 64 tokens 7.5 and 5.2; 256 experts, top 8 10.7
+// and 7.3; 1024, top 32 77 and 34, which the host does not hide).
+constexpr int kAllThreads = 1024, kAllTokens = 64;
 
 struct RouteParams {
     MoeRouteArgs a;

@@ -759,7 +759,9 @@ cudaError_t grouped_launch(const GroupedArgs &a, const FfnDev &d, cudaStream_t s
     p.vec[0] = starts(a.y, a.ldy);
     p.vec[1] = starts(a.dw0, a.K);
     p.idesc = idesc_f16(a.dtype, 256, 0, back);
-    // Copies of rows: in as few pieces as do not bring many of other experts.
+    // Copies of rows: in as few pieces as do not bring many of other experts. (Gated, one row on
+    // each of 64 experts, 1024 x 2048: 51.5 us with 16 rows a copy, 53.8 with 64; 512 on each of 8,
+    // 2048 x 4096: 88.2 with 16, 86.2 with 64; from 8 to 256 rows all three within 4 %, as runs are.)
     const int used = std::min(a.E, a.R), mean = a.R / used;
     p.cap = a.R < kTile ? (a.R + 31) / 32 * 32 : kTile;
     p.box = std::min(mean >= 128 ? 64 : mean >= 32 ? 32 : 16, p.cap / 2);

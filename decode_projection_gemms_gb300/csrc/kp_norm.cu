@@ -11,7 +11,7 @@
 // second kernel adds them in order, so nothing depends on timing.
 //
 // Bound: HBM forward (8192 x 7168 bf16: 39 us, 6.0 TB/s; 16384 x 4096 6.5). Backward the
-// instructions, about 28 an element of which a row's sums and addresses are 10, and the wait for
+// instructions, about 30 an element of which a row's sums and addresses are 10, and the wait for
 // the row's sums: 84 us, 4.2 TB/s. What it took to get there from 139: rows ahead through shared
 // memory, a block's teams' sums joined in it (a block's sums cost as much memory as four rows), the
 // two sums of a row halved between the lanes, the next row's statistics read beforehand.
@@ -585,6 +585,7 @@ cudaError_t norm_backward_launch(const NormArgs &a, const FfnDev &d, cudaStream_
     p.center = a.center;
     p.bias = a.dbias != nullptr;
     const int threads = 32 * sh.W * teams_of(sh.W);
+    // (fp32 rows of more than 8192 columns have no room for a ring: 4096 x 16384 559 us, bf16 103)
     const size_t ring = static_cast<size_t>(kAhead + 1) * 2 * sh.P * threads * 8 * es;
     const size_t sums = static_cast<size_t>(sh.P) * 8 * threads * sizeof(float);   // (no more than a ring)
     const bool vec = a.K % 8 == 0 && starts16(a.x, a.ldx, es) && starts16(a.y, a.ldy, es) && starts16(a.dy, a.lddy, es) &&

@@ -489,7 +489,8 @@ KP_API int kp_moe_route(const void *logits, int64_t ld, const float *bias, int T
                         int32_t *position, void *work, size_t work_bytes, kp_stream_t stream);
 /* dlogits [T, E] (of the logits' type, row stride ldd) from dweights [T, k]: with
  * d_j = w_j (dw_j - sum_i w_i dw_i), a chosen expert's is d_j (softmax) or d_j times one
- * minus its score (sigmoid), the others' 0. */
+ * minus its score (sigmoid), the others' 0. weights are those that kp_moe_route wrote: scaled
+ * ones give another gradient than the logits'. */
 KP_API int kp_moe_route_backward(const float *dweights, const void *logits, int64_t ld, const int32_t *ids,
                                  const float *weights, void *dlogits, int64_t ldd, int T, int E, int k, int score,
                                  int dtype, kp_stream_t stream);
