@@ -6,9 +6,10 @@
 // A row is read once and stays in the registers of a team of warps, so that the squares are
 // summed around the mean that was found first: no difference of two large sums. The gradients
 // start from x - mean too: x rstd - mean rstd is a rounding of mean rstd off for a whole row
-// (rows of 1e5 +- 1 in fp32: 8e-4 on every xhat, which adds up in dw). All sums are fp32. Backward, a block takes rows b, b + blocks, ... and a thread keeps the same
-// columns, whose dw and db it adds up in registers; the blocks' sums go to a workspace and a
-// second kernel adds them in order, so nothing depends on timing.
+// (rows of 1e5 +- 1 in fp32: 8e-4 on every xhat, which adds up in dw). All sums are fp32.
+// Backward, a block takes rows b, b + blocks, ... and a thread keeps the same columns, whose
+// dw and db it adds up in registers; the blocks' sums go to a workspace and a second kernel
+// adds them in order, so nothing depends on timing.
 //
 // Bound: HBM forward (8192 x 7168 bf16: 39 us, 6.0 TB/s; 16384 x 4096 6.5). Backward the
 // instructions, about 30 an element of which a row's sums and addresses are 10, and the wait for
